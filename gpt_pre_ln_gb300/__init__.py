@@ -23,7 +23,11 @@ __all__ = [
     "gpt2_mlp_workspace_bytes", "gpt2_mlp", "gpt2_mlp_noalloc", "gpt2_mlp_noalloc_max_scratch_bytes",
     "gpt2_workspace_bytes", "gpt2_block_forward", "gpt2_forward_logits", "gpt2_loss_workspace_bytes",
     "gpt2_forward_loss", "gpt2_prefill_workspace_bytes", "gpt2_prefill",
-    "gpt2_kv_cache_bytes", "gpt2_decode_workspace_bytes", "gpt2_decode_step", "gpt2_profile_begin",
+    "gpt2_kv_cache_bytes", "gpt2_decode_workspace_bytes", "gpt2_decode_step", "PagedCache", "paged_cache",
+    "gpt2_paged_cache_bytes", "gpt2_pages_workspace_bytes", "gpt2_pages_reserve", "gpt2_pages_fork",
+    "gpt2_pages_free", "gpt2_pages_compact", "gpt2_pages_write", "gpt2_attention_paged_workspace_bytes",
+    "gpt2_attention_paged", "gpt2_prefill_paged_workspace_bytes", "gpt2_prefill_paged",
+    "gpt2_decode_step_paged_workspace_bytes", "gpt2_decode_step_paged", "gpt2_token_logprobs", "gpt2_profile_begin",
     "gpt2_profile_end", "gpt2_profile_read", "ProfileEntry",
 ]
 
@@ -75,6 +79,12 @@ class ModelWeights(ctypes.Structure):
                 ("lnf_b", ctypes.c_void_p), ("blocks", ctypes.POINTER(BlockWeights))]
 
 
+class PagedCache(ctypes.Structure):
+    _fields_ = ([(k, ctypes.c_void_p) for k in ("pages", "refs", "table", "lens")]
+                + [(k, ctypes.c_int) for k in ("n_pages", "page_size", "n_layer", "n_kv_head", "n_seq", "max_pages",
+                                               "dtype")])
+
+
 class ProfileEntry(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_int), ("ms", ctypes.c_double),
                 ("flops", ctypes.c_double), ("bytes", ctypes.c_double)]
@@ -120,6 +130,23 @@ _SIGS = {
                             _VP, _I64, _VP, _SZ, _VP]),
     "gpt2_decode_step": (_I32, [ctypes.POINTER(Dims), ctypes.POINTER(ModelWeights), _VP, _I32, _I32, _VP, _VP, _VP,
                                 _VP, _I64, _VP, _SZ, _VP]),
+    "gpt2_paged_cache_bytes": (_SZ, [ctypes.POINTER(PagedCache)]),
+    "gpt2_pages_workspace_bytes": (_SZ, [ctypes.POINTER(PagedCache)]),
+    "gpt2_pages_reserve": (_I32, [ctypes.POINTER(PagedCache), _VP, _VP, _SZ, _VP]),
+    "gpt2_pages_fork": (_I32, [ctypes.POINTER(PagedCache), _VP, _VP, _I32, _VP]),
+    "gpt2_pages_free": (_I32, [ctypes.POINTER(PagedCache), _VP, _I32, _I32, _I32, _VP]),
+    "gpt2_pages_compact": (_I32, [ctypes.POINTER(PagedCache), _VP, _VP, _SZ, _VP]),
+    "gpt2_pages_write": (_I32, [ctypes.POINTER(PagedCache), _I32, _VP, _VP, _I64, _I32, _VP, _VP]),
+    "gpt2_attention_paged_workspace_bytes": (_SZ, [ctypes.POINTER(PagedCache), _I32]),
+    "gpt2_attention_paged": (_I32, [ctypes.POINTER(PagedCache), _I32, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP, _I32,
+                                    _F, _I32, _I32, _VP, _SZ, _VP]),
+    "gpt2_prefill_paged_workspace_bytes": (_SZ, [ctypes.POINTER(Dims), ctypes.POINTER(PagedCache), _I32]),
+    "gpt2_prefill_paged": (_I32, [ctypes.POINTER(Dims), ctypes.POINTER(ModelWeights), ctypes.POINTER(PagedCache), _VP,
+                                  _I32, _VP, _VP, _I64, _VP, _SZ, _VP]),
+    "gpt2_decode_step_paged_workspace_bytes": (_SZ, [ctypes.POINTER(Dims), ctypes.POINTER(PagedCache)]),
+    "gpt2_decode_step_paged": (_I32, [ctypes.POINTER(Dims), ctypes.POINTER(ModelWeights), ctypes.POINTER(PagedCache),
+                                      _I32, _I32, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
+    "gpt2_token_logprobs": (_I32, [_VP, _I64, _I32, _I64, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
     "gpt2_mlp_noalloc_max_scratch_bytes": (_SZ, []),
     "gpt2_mlp_noalloc": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I32, _I32, _I32, _VP]),
     "gpt2_profile_begin": (_I32, [_I32]),
@@ -316,6 +343,100 @@ def gpt2_decode_step(dims: Dims, w: ModelWeights, kv_cache, B, T_max, past_len, 
     _check(lib().gpt2_decode_step(ctypes.byref(dims), ctypes.byref(w), _ptr(kv_cache), B, T_max, _ptr(past_len),
                                   _ptr(tokens), _ptr(next_tokens), _ptr(logits_opt), ld, _ptr(ws), ws_bytes,
                                   _stream(stream)), "gpt2_decode_step")
+
+
+def paged_cache(pages, refs, table, lens) -> PagedCache:
+    """PagedCache of device tensors (which the caller keeps alive): pages [n_pages, n_layer, 2, n_kv_head, page_size,
+    64] in bf16 or fp16, refs int32 [n_pages], table int32 [n_seq, max_pages], lens int32 [n_seq]."""
+    import torch
+    if pages.dim() != 6 or pages.shape[2] != 2 or pages.shape[5] != 64:
+        raise ValueError("pages must be [n_pages, n_layer, 2, n_kv_head, page_size, 64]")
+    if pages.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError("pages must be bf16 or fp16")
+    n_pages, n_layer, _, n_kv_head, page_size, _ = pages.shape
+    if refs.shape != (n_pages,) or table.dim() != 2 or lens.shape != (table.shape[0],):
+        raise ValueError("refs must be [n_pages], table [n_seq, max_pages] and lens [n_seq]")
+    for t in (refs, table, lens):
+        if t.dtype != torch.int32:
+            raise ValueError("refs, table and lens must be int32")
+    for t in (pages, refs, table, lens):
+        if not t.is_contiguous() or t.device != pages.device:
+            raise ValueError("pages, refs, table and lens must be contiguous and on one device")
+    return PagedCache(_ptr(pages), _ptr(refs), _ptr(table), _ptr(lens), n_pages, page_size, n_layer, n_kv_head,
+                      table.shape[0], table.shape[1], F16 if pages.dtype == torch.float16 else BF16)
+
+
+def gpt2_paged_cache_bytes(cache: PagedCache) -> int:
+    return lib().gpt2_paged_cache_bytes(ctypes.byref(cache))
+
+
+def gpt2_pages_workspace_bytes(cache: PagedCache) -> int:
+    return lib().gpt2_pages_workspace_bytes(ctypes.byref(cache))
+
+
+def gpt2_pages_reserve(cache: PagedCache, n_new, ws, ws_bytes, stream=None):
+    _check(lib().gpt2_pages_reserve(ctypes.byref(cache), _ptr(n_new), _ptr(ws), ws_bytes, _stream(stream)),
+           "gpt2_pages_reserve")
+
+
+def gpt2_pages_fork(cache: PagedCache, parents, children, n, stream=None):
+    _check(lib().gpt2_pages_fork(ctypes.byref(cache), _ptr(parents), _ptr(children), n, _stream(stream)),
+           "gpt2_pages_fork")
+
+
+def gpt2_pages_free(cache: PagedCache, seqs, n, keep_first=0, keep_last=0, stream=None):
+    _check(lib().gpt2_pages_free(ctypes.byref(cache), _ptr(seqs), n, keep_first, keep_last, _stream(stream)),
+           "gpt2_pages_free")
+
+
+def gpt2_pages_compact(cache: PagedCache, n_used, ws, ws_bytes, stream=None):
+    _check(lib().gpt2_pages_compact(ctypes.byref(cache), _ptr(n_used), _ptr(ws), ws_bytes, _stream(stream)),
+           "gpt2_pages_compact")
+
+
+def gpt2_pages_write(cache: PagedCache, layer, k, v, ldkv, T, n_new=None, stream=None):
+    _check(lib().gpt2_pages_write(ctypes.byref(cache), layer, _ptr(k), _ptr(v), ldkv, T, _ptr(n_new),
+                                  _stream(stream)), "gpt2_pages_write")
+
+
+def gpt2_attention_paged_workspace_bytes(cache: PagedCache, n_head: int) -> int:
+    return lib().gpt2_attention_paged_workspace_bytes(ctypes.byref(cache), n_head)
+
+
+def gpt2_attention_paged(cache: PagedCache, layer, q, ldq, k_new, v_new, ldkv, out, ldo, lse, n_head, score_scale,
+                         window, sinks, ws, ws_bytes, stream=None):
+    _check(lib().gpt2_attention_paged(ctypes.byref(cache), layer, _ptr(q), ldq, _ptr(k_new), _ptr(v_new), ldkv,
+                                      _ptr(out), ldo, _ptr(lse), n_head, score_scale, window, sinks, _ptr(ws),
+                                      ws_bytes, _stream(stream)), "gpt2_attention_paged")
+
+
+def gpt2_prefill_paged_workspace_bytes(dims: Dims, cache: PagedCache, T: int) -> int:
+    return lib().gpt2_prefill_paged_workspace_bytes(ctypes.byref(dims), ctypes.byref(cache), T)
+
+
+def gpt2_prefill_paged(dims: Dims, w: ModelWeights, cache: PagedCache, tokens, T, next_tokens, logits_opt, ld, ws,
+                       ws_bytes, stream=None):
+    _check(lib().gpt2_prefill_paged(ctypes.byref(dims), ctypes.byref(w), ctypes.byref(cache), _ptr(tokens), T,
+                                    _ptr(next_tokens), _ptr(logits_opt), ld, _ptr(ws), ws_bytes, _stream(stream)),
+           "gpt2_prefill_paged")
+
+
+def gpt2_decode_step_paged_workspace_bytes(dims: Dims, cache: PagedCache) -> int:
+    return lib().gpt2_decode_step_paged_workspace_bytes(ctypes.byref(dims), ctypes.byref(cache))
+
+
+def gpt2_decode_step_paged(dims: Dims, w: ModelWeights, cache: PagedCache, window, sinks, tokens, next_tokens,
+                           logits_opt, ld, ws, ws_bytes, stream=None):
+    _check(lib().gpt2_decode_step_paged(ctypes.byref(dims), ctypes.byref(w), ctypes.byref(cache), window, sinks,
+                                        _ptr(tokens), _ptr(next_tokens), _ptr(logits_opt), ld, _ptr(ws), ws_bytes,
+                                        _stream(stream)), "gpt2_decode_step_paged")
+
+
+def gpt2_token_logprobs(logits, ld, logits_t, M, V, tokens, logprob, entropy, lse, top_n, top_ids, top_logprobs,
+                        stream=None):
+    _check(lib().gpt2_token_logprobs(_ptr(logits), ld, logits_t, M, V, _ptr(tokens), _ptr(logprob), _ptr(entropy),
+                                     _ptr(lse), top_n, _ptr(top_ids), _ptr(top_logprobs), _stream(stream)),
+           "gpt2_token_logprobs")
 
 
 def gpt2_profile_begin(max_launches: int):

@@ -226,6 +226,11 @@ struct KeyBuilder {
     return add(d->n_layer).add(d->d_model).add(d->n_head).add(d->d_ff).add(d->vocab).add(d->n_pos).add(eps_bits)
         .add(d->dtype).add(d->flags);
   }
+  KeyBuilder& paged(const gpt2_paged_cache* c) {
+    ptr(c->pages).ptr(c->refs).ptr(c->table).ptr(c->lens);
+    return add(c->n_pages).add(c->page_size).add(c->n_layer).add(c->n_kv_head).add(c->n_seq).add(c->max_pages)
+        .add(c->dtype);
+  }
   KeyBuilder& model(const gpt2_model_weights* m, int n_layer) {
     ptr(m->wte).ptr(m->wpe).ptr(m->lnf_g).ptr(m->lnf_b);
     for (int l = 0; l < n_layer; ++l) {
@@ -379,9 +384,11 @@ Acts carve_acts(void* ws, const gpt2_dims* d, int64_t M) {
 // The body of block `layer` (counted from 0) from `a = LN_1(x)` already
 // computed; x -> x_out.  With kv_layer (16-bit paths), the layer's K and V of
 // all B T positions are also written to cache slots 0..T-1 of a
-// [2, B, n_head, T_max, 64] layer.
+// [2, B, n_head, T_max, 64] layer; with paged, to positions lens[b] .. lens[b]
+// + T - 1 of that cache.
 int block_body(const gpt2_dims* d, const gpt2_block_weights* w, int layer, const float* x, float* x_out, int B, int T,
-               const Acts& A, cudaStream_t s, void* kv_layer = nullptr, int T_max = 0) {
+               const Acts& A, cudaStream_t s, void* kv_layer = nullptr, int T_max = 0,
+               const gpt2_paged_cache* paged = nullptr) {
   const gpt2_dtype dt = d->dtype;
   const int64_t M = static_cast<int64_t>(B) * T;
   const int D = d->d_model, F = d->d_ff, H = d->n_head;
@@ -390,12 +397,49 @@ int block_body(const gpt2_dims* d, const gpt2_block_weights* w, int layer, const
     ProfScope prof("kv_from_qkv", 0.0, 2.0 * M * 2 * D * esize(dt), s);
     GPT2_CUDA(launch_kv_from_qkv(dt, A.qkv, kv_layer, B, T, H, T_max, s));
   }
+  if (paged) {
+    ProfScope prof("pages_write", 0.0, 2.0 * M * 2 * D * esize(dt), s);
+    const char* k = static_cast<const char*>(A.qkv) + D * esize(dt);
+    GPT2_CUDA(launch_pages_write(paged, layer, k, k + D * esize(dt), 3 * D, T, nullptr, s));
+  }
   GPT2_CUDA(attention(dt, A.qkv, A.o, B, T, H, score_scale(d, layer), s));
   GPT2_CUDA(linear(dt, A.o, w->w_o, w->b_o, x, A.h, M, D, D, D, false, GPT2_EPI_BIAS_RESIDUAL, GPT2_F32, s));
   GPT2_CUDA(layernorm(A.h, w->ln2_g, w->ln2_b, A.a, M, D, d->eps, GPT2_F32, dt, s));
   GPT2_CUDA(linear(dt, A.a, w->w_fc, w->b_fc, nullptr, A.g, M, F, D, F, false, mlp_epilogue(d), dt, s));
   GPT2_CUDA(linear(dt, A.g, w->w_proj, w->b_proj, A.h, x_out, M, D, F, D, false, GPT2_EPI_BIAS_RESIDUAL, GPT2_F32, s));
   return GPT2_OK;
+}
+
+// `data`: also the pointers that every call on the cache needs.
+int check_paged(const gpt2_paged_cache* c, bool data) {
+  if (!c) return GPT2_ERR_ARG;
+  if (!valid_dtype(c->dtype)) return GPT2_ERR_ARG;
+  if (c->n_pages <= 0 || c->page_size <= 0 || c->n_layer <= 0 || c->n_kv_head <= 0 || c->n_seq < 0 ||
+      c->max_pages <= 0)
+    return GPT2_ERR_ARG;
+  if (!is16(c->dtype) || c->page_size % 16 != 0 || c->page_size > 4096 || c->n_seq > kMaxPagedSeqs)
+    return GPT2_ERR_UNSUPPORTED;
+  if (c->n_layer > 4096 || c->n_kv_head > 1024) return GPT2_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(c->max_pages) * c->page_size > INT_MAX ||
+      static_cast<int64_t>(c->n_seq) * c->max_pages > INT_MAX)
+    return GPT2_ERR_UNSUPPORTED;
+  if (!data) return GPT2_OK;
+  const void* ps[4] = {c->pages, c->refs, c->table, c->lens};
+  for (const void* p : ps)
+    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return GPT2_ERR_ARG;
+  return aligned16(c->pages) ? GPT2_OK : GPT2_ERR_ARG;
+}
+
+// A model's paged cache: one key-value head per head, every layer of the model.
+int check_paged_model(const gpt2_dims* d, const gpt2_paged_cache* c) {
+  GPT2_TRY(check_paged(c, true));
+  if (c->dtype != d->dtype || c->n_layer != d->n_layer || c->n_kv_head != d->n_head) return GPT2_ERR_ARG;
+  return GPT2_OK;
+}
+
+int check_ws(const void* ws, size_t have, size_t need) {
+  if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return GPT2_ERR_ARG;
+  return have < need ? GPT2_ERR_WORKSPACE : GPT2_OK;
 }
 
 int check_model(const gpt2_dims* dims, const gpt2_model_weights* w) {
@@ -439,6 +483,11 @@ struct DecodeGroup {
   float2* cand;             // fused argmax (nb <= kMaxRowsGemm)
   float* lg;                // otherwise the logits for argmax_rows
   cudaStream_t s;
+  // in place of kv_cache and past_len: a paged cache, whose idle slots are
+  // skipped, and the attention's window and workspace
+  const gpt2_paged_cache* paged = nullptr;
+  int window = 0, sinks = 0;
+  void* paged_ws = nullptr;
 
   void carve(char* base) {
     Carve c(base);
@@ -462,7 +511,7 @@ struct DecodeGroup {
     const int D = d->d_model;
     ProfScope prof("decode_embed_layernorm", 8.0 * nb * D, static_cast<double>(nb) * D * 10.0, s);
     return launch_decode_embed_ln(d->dtype, tokens, past_len, w->wte, w->wpe, w->blocks[0].ln1_g,
-                                  w->blocks[0].ln1_b, A.x, A.a, nb, D, d->vocab, d->n_pos, T_max, d->eps, valid, s);
+                                  w->blocks[0].ln1_b, A.x, A.a, nb, D, d->vocab, d->n_pos, T_max, d->eps, valid, s, paged != nullptr);
   }
 
   cudaError_t layer(int l) {
@@ -477,7 +526,13 @@ struct DecodeGroup {
       return e;
     const size_t layer_elems = static_cast<size_t>(2) * B_cache * H * static_cast<size_t>(T_max) * 64;
     void* kv_layer = static_cast<char*>(kv_cache) + l * layer_elems * esize(dt);
-    {
+    if (paged) {
+      ProfScope prof("paged_attn", 0.0, 0.0, s);
+      const char* q = static_cast<const char*>(A.qkv);
+      if ((e = launch_attention_paged(paged, l, q, 3 * D, q + D * 2, q + D * 4, 3 * D, A.o, D, nullptr, H,
+                                      score_scale(d, l), window, sinks, paged_ws, s)) != cudaSuccess)
+        return e;
+    } else {
       // the cached lengths live on the device: the bytes of this kernel are
       // left to the caller, who knows them
       ProfScope prof("decode_attn", 0.0, 0.0, s);
@@ -527,9 +582,11 @@ struct DecodeGroup {
 
 // Embedding, the n_layer blocks and ln_f: A.a = LN_f(x_L) (type dims.dtype).
 // With kv_cache ([n_layer, 2, B, n_head, T_max, 64]) every layer's K and V
-// are kept in it; with lnf = false the ln_f step is left out.
+// are kept in it (or in the paged cache); with lnf = false the ln_f step is
+// left out.
 int forward_to_lnf(const gpt2_dims* dims, const gpt2_model_weights* w, const int32_t* tokens, int B, int T,
-                   const Acts& A, cudaStream_t s, void* kv_cache = nullptr, int T_max = 0, bool lnf = true) {
+                   const Acts& A, cudaStream_t s, void* kv_cache = nullptr, int T_max = 0, bool lnf = true,
+                   const gpt2_paged_cache* paged = nullptr) {
   const int64_t M = static_cast<int64_t>(B) * T;
   const gpt2_dtype dt = dims->dtype;
   const int D = dims->d_model;
@@ -546,7 +603,7 @@ int forward_to_lnf(const gpt2_dims* dims, const gpt2_model_weights* w, const int
     if (kv_cache)
       kv_layer = static_cast<char*>(kv_cache) +
                  static_cast<size_t>(l) * 2 * B * dims->n_head * static_cast<size_t>(T_max) * 64 * esize(dt);
-    GPT2_TRY(block_body(dims, bw, l, A.x, A.x, B, T, A, s, kv_layer, T_max));
+    GPT2_TRY(block_body(dims, bw, l, A.x, A.x, B, T, A, s, kv_layer, T_max, paged));
   }
   if (lnf) GPT2_CUDA(layernorm(A.x, w->lnf_g, w->lnf_b, A.a, M, D, dims->eps, GPT2_F32, dt, s));
   return GPT2_OK;
@@ -560,6 +617,48 @@ size_t prefill_extra_bytes(const gpt2_dims* d, int B) {
   size_t n = align256(b * 4) + align256(b * d->d_model * 4) + align256(b * d->d_model * 2);
   n += B <= kMaxRowsGemm ? align256(b * rows_argmax_candidates(d->vocab) * sizeof(float2)) : align256(b * Vp * 4);
   return n;
+}
+
+// The work of gpt2_prefill and gpt2_prefill_paged (kv_cache or paged; with a
+// paged cache past_len is its lens, and sequences must start at length 0).
+int prefill(const gpt2_dims* dims, const gpt2_model_weights* w, const int32_t* tokens, int B, int T, void* kv_cache,
+            int T_max, int32_t* past_len, int32_t* next_tokens, float* logits_opt, int64_t ld, void* ws,
+            cudaStream_t s, const gpt2_paged_cache* paged) {
+  const int64_t M = static_cast<int64_t>(B) * T;
+  const gpt2_dtype dt = dims->dtype;
+  const int D = dims->d_model, V = dims->vocab;
+  Acts A = carve_acts(ws, dims, M);
+  Carve c(static_cast<char*>(ws) + acts_bytes(dims, M));
+  int* valid = c.take<int>(B, 4);
+  float* x_last = c.take<float>(static_cast<size_t>(B) * D, 4);
+  void* a_last = c.take<char>(static_cast<size_t>(B) * D, 2);
+  GPT2_TRY(forward_to_lnf(dims, w, tokens, B, T, A, s, kv_cache, T_max, false, paged));
+  {
+    ProfScope prof("prefill_last_rows", 0.0, 8.0 * B * D, s);
+    GPT2_CUDA(launch_prefill_last_rows(A.x, B, T, D, x_last, valid, past_len, s, paged != nullptr));
+  }
+  GPT2_CUDA(layernorm(x_last, w->lnf_g, w->lnf_b, a_last, B, D, dims->eps, GPT2_F32, dt, s));
+  if (B <= kMaxRowsGemm) {
+    float2* cand = c.take<float2>(static_cast<size_t>(B) * rows_argmax_candidates(V), sizeof(float2));
+    const int n_cand = rows_argmax_candidates(V);
+    {
+      ProfScope prof(dt == GPT2_BF16 ? "gemm_rows_bf16_tcgen05" : "gemm_rows_f16_tcgen05", 2.0 * B * V * D,
+                     (static_cast<double>(B) + V) * D * esize(dt) + (logits_opt ? 4.0 * B * V : 0.0), s);
+      GPT2_CUDA(launch_gemm_rows_16(dt, a_last, w->wte, nullptr, nullptr, logits_opt, B, V, D, logits_opt ? ld : V,
+                                    true, GPT2_EPI_NONE, GPT2_F32, s, cand));
+    }
+    ProfScope prof("argmax_candidates", static_cast<double>(B) * n_cand, static_cast<double>(B) * n_cand * 8.0, s);
+    GPT2_CUDA(launch_argmax_candidates(cand, n_cand, B, valid, next_tokens, nullptr, s));
+    return GPT2_OK;
+  }
+  const int64_t Vp = (static_cast<int64_t>(V) + 3) & ~static_cast<int64_t>(3);
+  float* lg = c.take<float>(static_cast<size_t>(B) * Vp, 4);
+  float* out = logits_opt ? logits_opt : lg;
+  const int64_t lld = logits_opt ? ld : Vp;
+  GPT2_CUDA(linear(dt, a_last, w->wte, nullptr, nullptr, out, B, V, D, lld, true, GPT2_EPI_NONE, GPT2_F32, s));
+  ProfScope prof("argmax_rows", static_cast<double>(B) * V, static_cast<double>(B) * V * 4.0, s);
+  GPT2_CUDA(launch_argmax_rows(out, lld, B, V, valid, next_tokens, nullptr, s));
+  return GPT2_OK;
 }
 
 // The loss path fuses log-sum-exp into the lm_head GEMM (16-bit, more than
@@ -1333,42 +1432,189 @@ int gpt2_prefill(const gpt2_dims* dims, const gpt2_model_weights* w, const int32
   if (logits_opt && ld % 4 != 0) return GPT2_ERR_UNSUPPORTED;
   if (!ws || (reinterpret_cast<uintptr_t>(ws) & 255u)) return GPT2_ERR_ARG;
   if (ws_bytes < gpt2_prefill_workspace_bytes(dims, B, T)) return GPT2_ERR_WORKSPACE;
-  const int64_t M = static_cast<int64_t>(B) * T;
-  const gpt2_dtype dt = dims->dtype;
-  const int D = dims->d_model, V = dims->vocab;
-  cudaStream_t s = cs(stream);
-  Acts A = carve_acts(ws, dims, M);
-  Carve c(static_cast<char*>(ws) + acts_bytes(dims, M));
-  int* valid = c.take<int>(B, 4);
-  float* x_last = c.take<float>(static_cast<size_t>(B) * D, 4);
-  void* a_last = c.take<char>(static_cast<size_t>(B) * D, 2);
-  GPT2_TRY(forward_to_lnf(dims, w, tokens, B, T, A, s, kv_cache, T_max, false));
-  {
-    ProfScope prof("prefill_last_rows", 0.0, 8.0 * B * D, s);
-    GPT2_CUDA(launch_prefill_last_rows(A.x, B, T, D, x_last, valid, past_len, s));
-  }
-  GPT2_CUDA(layernorm(x_last, w->lnf_g, w->lnf_b, a_last, B, D, dims->eps, GPT2_F32, dt, s));
-  if (B <= kMaxRowsGemm) {
-    float2* cand = c.take<float2>(static_cast<size_t>(B) * rows_argmax_candidates(V), sizeof(float2));
-    const int n_cand = rows_argmax_candidates(V);
-    {
-      ProfScope prof(dt == GPT2_BF16 ? "gemm_rows_bf16_tcgen05" : "gemm_rows_f16_tcgen05", 2.0 * B * V * D,
-                     (static_cast<double>(B) + V) * D * esize(dt) + (logits_opt ? 4.0 * B * V : 0.0), s);
-      GPT2_CUDA(launch_gemm_rows_16(dt, a_last, w->wte, nullptr, nullptr, logits_opt, B, V, D, logits_opt ? ld : V,
-                                    true, GPT2_EPI_NONE, GPT2_F32, s, cand));
-    }
-    ProfScope prof("argmax_candidates", static_cast<double>(B) * n_cand, static_cast<double>(B) * n_cand * 8.0, s);
-    GPT2_CUDA(launch_argmax_candidates(cand, n_cand, B, valid, next_tokens, nullptr, s));
+  return prefill(dims, w, tokens, B, T, kv_cache, T_max, past_len, next_tokens, logits_opt, ld, ws, cs(stream),
+                 nullptr);
+}
+
+size_t gpt2_paged_cache_bytes(const gpt2_paged_cache* cache) {
+  if (check_paged(cache, false) != GPT2_OK) return 0;
+  return static_cast<size_t>(cache->n_pages) * cache->n_layer * 2 * cache->n_kv_head * cache->page_size * 64 * 2;
+}
+
+size_t gpt2_pages_workspace_bytes(const gpt2_paged_cache* cache) {
+  return check_paged(cache, false) == GPT2_OK ? pages_workspace(cache) : 0;
+}
+
+int gpt2_pages_reserve(const gpt2_paged_cache* cache, const int32_t* n_new, void* ws, size_t ws_bytes,
+                       gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (cache->n_seq == 0) return GPT2_OK;
+  if (!n_new) return GPT2_ERR_ARG;
+  GPT2_TRY(check_ws(ws, ws_bytes, pages_workspace(cache)));
+  ProfScope prof("pages_reserve", 0.0, 0.0, cs(stream));
+  return cuda_status(launch_pages_reserve(cache, n_new, ws, cs(stream)));
+}
+
+int gpt2_pages_fork(const gpt2_paged_cache* cache, const int32_t* parents, const int32_t* children, int n,
+                    gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (n < 0 || n > cache->n_seq) return GPT2_ERR_ARG;
+  if (n == 0) return GPT2_OK;
+  if (!parents || !children) return GPT2_ERR_ARG;
+  ProfScope prof("pages_fork", 0.0, 0.0, cs(stream));
+  return cuda_status(launch_pages_fork(cache, parents, children, n, cs(stream)));
+}
+
+int gpt2_pages_free(const gpt2_paged_cache* cache, const int32_t* seqs, int n, int keep_first, int keep_last,
+                    gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (n < 0 || n > cache->n_seq || keep_first < 0 || keep_last < 0) return GPT2_ERR_ARG;
+  if (n == 0) return GPT2_OK;
+  if (!seqs) return GPT2_ERR_ARG;
+  ProfScope prof("pages_free", 0.0, 0.0, cs(stream));
+  return cuda_status(launch_pages_free(cache, seqs, n, keep_first, keep_last, cs(stream)));
+}
+
+int gpt2_pages_compact(const gpt2_paged_cache* cache, int32_t* n_used, void* ws, size_t ws_bytes,
+                       gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (!n_used) return GPT2_ERR_ARG;
+  GPT2_TRY(check_ws(ws, ws_bytes, pages_workspace(cache)));
+  ProfScope prof("pages_compact", 0.0, 0.0, cs(stream));
+  return cuda_status(launch_pages_compact(cache, n_used, ws, cs(stream)));
+}
+
+int gpt2_pages_write(const gpt2_paged_cache* cache, int layer, const void* k, const void* v, int64_t ldkv, int T,
+                     const int32_t* n_new, gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (layer < 0 || layer >= cache->n_layer || T < 0 || ldkv < 64ll * cache->n_kv_head) return GPT2_ERR_ARG;
+  if (static_cast<int64_t>(cache->n_seq) * T > INT_MAX) return GPT2_ERR_ARG;
+  if (ldkv % 8 != 0) return GPT2_ERR_UNSUPPORTED;
+  if (cache->n_seq == 0 || T == 0) return GPT2_OK;
+  if (!k || !v || !aligned16(k) || !aligned16(v)) return GPT2_ERR_ARG;
+  const double rows = static_cast<double>(cache->n_seq) * T;
+  ProfScope prof("pages_write", 0.0, rows * cache->n_kv_head * 512.0, cs(stream));
+  return cuda_status(launch_pages_write(cache, layer, k, v, ldkv, T, n_new, cs(stream)));
+}
+
+size_t gpt2_attention_paged_workspace_bytes(const gpt2_paged_cache* cache, int n_head) {
+  if (check_paged(cache, false) != GPT2_OK || n_head <= 0 || n_head % cache->n_kv_head != 0) return 0;
+  return attention_paged_workspace(cache, n_head);
+}
+
+int gpt2_attention_paged(const gpt2_paged_cache* cache, int layer, const void* q, int64_t ldq, const void* k_new,
+                         const void* v_new, int64_t ldkv, void* out, int64_t ldo, float* lse, int n_head,
+                         float score_scale, int window, int sinks, void* ws, size_t ws_bytes, gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (layer < 0 || layer >= cache->n_layer || n_head <= 0 || window < 0 || sinks < 0) return GPT2_ERR_ARG;
+  if (!std::isfinite(score_scale) || !(score_scale > 0.f)) return GPT2_ERR_ARG;
+  if (n_head % cache->n_kv_head != 0 || n_head > 1024) return GPT2_ERR_UNSUPPORTED;
+  if ((k_new == nullptr) != (v_new == nullptr)) return GPT2_ERR_ARG;
+  const int64_t width = 64ll * n_head, kv_width = 64ll * cache->n_kv_head;
+  if (ldq < width || ldo < width || (k_new && ldkv < kv_width)) return GPT2_ERR_ARG;
+  if (ldq % 8 != 0 || ldo % 8 != 0 || (k_new && ldkv % 8 != 0)) return GPT2_ERR_UNSUPPORTED;
+  if (!attention_paged_fits(cache, n_head)) return GPT2_ERR_UNSUPPORTED;
+  if (cache->n_seq == 0) return GPT2_OK;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new)) return GPT2_ERR_ARG;
+  if (reinterpret_cast<uintptr_t>(lse) & 3u) return GPT2_ERR_ARG;
+  GPT2_TRY(check_ws(ws, ws_bytes, attention_paged_workspace(cache, n_head)));
+  // the lengths live on the device: the work of this kernel is left to the
+  // caller, who knows them
+  ProfScope prof("paged_attn", 0.0, 0.0, cs(stream));
+  return cuda_status(launch_attention_paged(cache, layer, q, ldq, k_new, v_new, ldkv, out, ldo, lse, n_head,
+                                            score_scale, window, sinks, ws, cs(stream)));
+}
+
+size_t gpt2_prefill_paged_workspace_bytes(const gpt2_dims* dims, const gpt2_paged_cache* cache, int T) {
+  if (check_paged(cache, false) != GPT2_OK) return 0;
+  return gpt2_prefill_workspace_bytes(dims, cache->n_seq, T);
+}
+
+int gpt2_prefill_paged(const gpt2_dims* dims, const gpt2_model_weights* w, const gpt2_paged_cache* cache,
+                       const int32_t* tokens, int T, int32_t* next_tokens, float* logits_opt, int64_t ld, void* ws,
+                       size_t ws_bytes, gpt2_stream_t stream) {
+  GPT2_TRY(check_model(dims, w));
+  if (!is16(dims->dtype)) return GPT2_ERR_UNSUPPORTED;
+  GPT2_TRY(check_paged_model(dims, cache));
+  const int B = cache->n_seq;
+  if (T < 0 || static_cast<int64_t>(B) * T > INT_MAX) return GPT2_ERR_ARG;
+  if (B == 0) return GPT2_OK;
+  if (T < 1 || T > dims->n_pos || T > cache->max_pages * cache->page_size) return GPT2_ERR_ARG;
+  if (!tokens || !next_tokens) return GPT2_ERR_ARG;
+  if (logits_opt && (ld < dims->vocab || !aligned16(logits_opt))) return GPT2_ERR_ARG;
+  if (logits_opt && ld % 4 != 0) return GPT2_ERR_UNSUPPORTED;
+  GPT2_TRY(check_ws(ws, ws_bytes, gpt2_prefill_paged_workspace_bytes(dims, cache, T)));
+  return prefill(dims, w, tokens, B, T, nullptr, 0, cache->lens, next_tokens, logits_opt, ld, ws, cs(stream), cache);
+}
+
+size_t gpt2_decode_step_paged_workspace_bytes(const gpt2_dims* dims, const gpt2_paged_cache* cache) {
+  if (check_dims(dims, true) != GPT2_OK || check_paged(cache, false) != GPT2_OK ||
+      dims->n_head % cache->n_kv_head != 0)
+    return 0;
+  return decode_ws_bytes(dims, cache->n_seq) + attention_paged_workspace(cache, dims->n_head);
+}
+
+int gpt2_decode_step_paged(const gpt2_dims* dims, const gpt2_model_weights* w, const gpt2_paged_cache* cache,
+                           int window, int sinks, const int32_t* tokens, int32_t* next_tokens, float* logits_opt,
+                           int64_t ld, void* ws, size_t ws_bytes, gpt2_stream_t stream) {
+  GPT2_TRY(check_model(dims, w));
+  if (!is16(dims->dtype)) return GPT2_ERR_UNSUPPORTED;
+  GPT2_TRY(check_paged_model(dims, cache));
+  const int B = cache->n_seq;
+  if (window < 0 || sinks < 0) return GPT2_ERR_ARG;
+  if (!attention_paged_fits(cache, dims->n_head)) return GPT2_ERR_UNSUPPORTED;
+  if (B == 0) return GPT2_OK;
+  if (!tokens || !next_tokens) return GPT2_ERR_ARG;
+  if (logits_opt && (ld < dims->vocab || !aligned16(logits_opt))) return GPT2_ERR_ARG;
+  if (logits_opt && ld % 4 != 0) return GPT2_ERR_UNSUPPORTED;
+  GPT2_TRY(check_ws(ws, ws_bytes, gpt2_decode_step_paged_workspace_bytes(dims, cache)));
+  char* base = static_cast<char*>(ws);
+  KeyBuilder kb;
+  kb.add(6).dims(dims).model(w, dims->n_layer).paged(cache).add(window).add(sinks).ptr(tokens).ptr(next_tokens)
+      .ptr(logits_opt).add(ld).ptr(ws);
+  return run_graphed(kb, cs(stream), [&](cudaStream_t s) -> int {
+    DecodeGroup G;
+    G.d = dims;
+    G.w = w;
+    G.kv_cache = nullptr;
+    G.B_cache = B;
+    G.T_max = cache->max_pages * cache->page_size;
+    G.b0 = 0;
+    G.nb = B;
+    G.past_len = cache->lens;
+    G.tokens = tokens;
+    G.next_tokens = next_tokens;
+    G.logits = logits_opt;
+    G.ld = ld;
+    G.valid = reinterpret_cast<int*>(base);
+    G.carve(base + align256(static_cast<size_t>(B) * 4));
+    G.s = s;
+    G.paged = cache;
+    G.window = window;
+    G.sinks = sinks;
+    G.paged_ws = base + decode_ws_bytes(dims, B);
+    GPT2_CUDA(G.embed());
+    for (int l = 0; l < dims->n_layer; ++l) GPT2_CUDA(G.layer(l));
+    GPT2_CUDA(G.head());
     return GPT2_OK;
-  }
-  const int64_t Vp = (static_cast<int64_t>(V) + 3) & ~static_cast<int64_t>(3);
-  float* lg = c.take<float>(static_cast<size_t>(B) * Vp, 4);
-  float* out = logits_opt ? logits_opt : lg;
-  const int64_t lld = logits_opt ? ld : Vp;
-  GPT2_CUDA(linear(dt, a_last, w->wte, nullptr, nullptr, out, B, V, D, lld, true, GPT2_EPI_NONE, GPT2_F32, s));
-  ProfScope prof("argmax_rows", static_cast<double>(B) * V, static_cast<double>(B) * V * 4.0, s);
-  GPT2_CUDA(launch_argmax_rows(out, lld, B, V, valid, next_tokens, nullptr, s));
-  return GPT2_OK;
+  });
+}
+
+int gpt2_token_logprobs(const void* logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V, const int32_t* tokens,
+                        float* logprob, float* entropy, float* lse, int top_n, int32_t* top_ids,
+                        float* top_logprobs, gpt2_stream_t stream) {
+  if (!valid_dtype(logits_t)) return GPT2_ERR_ARG;
+  if (M < 0 || M > INT_MAX || V <= 0 || ld < V || top_n < 0 || top_n > V) return GPT2_ERR_ARG;
+  if (top_n > kMaxTopN || (ld * static_cast<int64_t>(esize(logits_t))) % 16 != 0) return GPT2_ERR_UNSUPPORTED;
+  if ((tokens == nullptr) != (logprob == nullptr)) return GPT2_ERR_ARG;
+  if (top_n == 0) top_ids = nullptr, top_logprobs = nullptr;
+  if (top_n > 0 && (!top_ids || !top_logprobs)) return GPT2_ERR_ARG;
+  if (!logprob && !entropy && !lse && top_n == 0) return GPT2_ERR_ARG;
+  if (M == 0) return GPT2_OK;
+  if (!logits || !aligned16(logits)) return GPT2_ERR_ARG;
+  ProfScope prof("token_logprobs", 6.0 * M * V, static_cast<double>(M) * V * esize(logits_t), cs(stream));
+  return cuda_status(launch_token_logprobs(logits, ld, logits_t, M, V, tokens, logprob, entropy, lse, top_n, top_ids,
+                                           top_logprobs, cs(stream)));
 }
 
 int gpt2_profile_begin(int max_launches) {

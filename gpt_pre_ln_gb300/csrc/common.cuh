@@ -38,6 +38,11 @@ enum ErrSite : unsigned {
   kSiteLossLabel = 17,
   kSiteSelfTestWait = 18,
   kSiteAttnBwd = 19,
+  kSitePagedLength = 20,  // a sequence's positions do not fit its table row
+  kSitePagedPage = 21,    // a table entry that is needed names no page
+  kSitePagedRow = 22,     // a sequence out of range, or named twice
+  kSitePagedFull = 23,    // too few free pages
+  kSiteScoreToken = 24,
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per wait

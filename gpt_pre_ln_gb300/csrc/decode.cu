@@ -32,7 +32,7 @@ __global__ void decode_embed_ln(const int32_t* __restrict__ tokens, const int32_
                                 const T16* __restrict__ wte, const T16* __restrict__ wpe,
                                 const T16* __restrict__ gamma, const T16* __restrict__ beta, float* __restrict__ x,
                                 T16* __restrict__ y, int B, int D, int V, int n_pos, int T_max, float eps,
-                                int* __restrict__ valid, unsigned* err) {
+                                int* __restrict__ valid, bool idle_slots, unsigned* err) {
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -44,8 +44,9 @@ __global__ void decode_embed_ln(const int32_t* __restrict__ tokens, const int32_
   const bool tok_ok = tok >= 0 && tok < V;
   if (lane == 0) {
     valid[b] = (pos_ok && tok_ok) ? 1 : 0;
-    if (!pos_ok) record_error(err, kErrRange, kSiteDecodePos);
-    if (!tok_ok) record_error(err, kErrRange, kSiteDecodeToken);
+    const bool idle = idle_slots && pos == -1;
+    if (!pos_ok && !idle) record_error(err, kErrRange, kSiteDecodePos);
+    if (!tok_ok && !idle) record_error(err, kErrRange, kSiteDecodeToken);
   }
   const bool ok = pos_ok && tok_ok;
   const T16* er = wte + static_cast<long long>(ok ? tok : 0) * D;
@@ -369,9 +370,11 @@ __global__ void kv_from_qkv(const T16* __restrict__ qkv, T16* __restrict__ kv_la
 }
 
 // After the prompt: x_last[b] = x[b T + T - 1] (the residual stream of each
-// sequence's last position), valid[b] = 1, past_len[b] = T.
+// sequence's last position), valid[b] = 1, past_len[b] = T (with from_zero
+// only where past_len[b] was 0).
 __global__ void prefill_last_rows(const float* __restrict__ x, int T, int D, float* __restrict__ x_last,
-                                  int* __restrict__ valid, int32_t* __restrict__ past_len) {
+                                  int* __restrict__ valid, int32_t* __restrict__ past_len, bool from_zero,
+                                  unsigned* err) {
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x;
@@ -380,8 +383,12 @@ __global__ void prefill_last_rows(const float* __restrict__ x, int T, int D, flo
     *reinterpret_cast<float4*>(x_last + static_cast<long long>(b) * D + i) =
         *reinterpret_cast<const float4*>(src + i);
   if (threadIdx.x == 0) {
-    valid[b] = 1;
-    past_len[b] = T;
+    const bool ok = !from_zero || past_len[b] == 0;
+    valid[b] = ok ? 1 : 0;
+    if (ok)
+      past_len[b] = T;
+    else
+      record_error(err, kErrRange, kSitePagedLength);
   }
 }
 
@@ -400,13 +407,15 @@ cudaError_t launch_kv_from_qkv(gpt2_dtype dt, const void* qkv, void* kv_layer, i
 }
 
 cudaError_t launch_prefill_last_rows(const float* x, int B, int T, int D, float* x_last, int* valid,
-                                     int32_t* past_len, cudaStream_t stream) {
-  return launch_pdl(prefill_last_rows, B, 256, 0, stream, 0, x, T, D, x_last, valid, past_len);
+                                     int32_t* past_len, cudaStream_t stream, bool from_zero) {
+  return launch_pdl(prefill_last_rows, B, 256, 0, stream, 0, x, T, D, x_last, valid, past_len, from_zero,
+                    device_error_word());
 }
 
 cudaError_t launch_decode_embed_ln(gpt2_dtype dt, const int32_t* tokens, const int32_t* past_len, const void* wte,
                                    const void* wpe, const void* gamma, const void* beta, float* x, void* y, int B,
-                                   int D, int V, int n_pos, int T_max, float eps, int* valid, cudaStream_t stream) {
+                                   int D, int V, int n_pos, int T_max, float eps, int* valid, cudaStream_t stream,
+                                   bool idle_slots) {
   const int warps = 4;
   const dim3 grid((B + warps - 1) / warps), block(warps * 32);
   unsigned* err = device_error_word();
@@ -414,12 +423,12 @@ cudaError_t launch_decode_embed_ln(gpt2_dtype dt, const int32_t* tokens, const i
     using T = __half;
     return launch_pdl(decode_embed_ln<T>, grid, block, 0, stream, 0, tokens, past_len, static_cast<const T*>(wte),
                       static_cast<const T*>(wpe), static_cast<const T*>(gamma), static_cast<const T*>(beta), x,
-                      static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, err);
+                      static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, idle_slots, err);
   }
   using T = __nv_bfloat16;
   return launch_pdl(decode_embed_ln<T>, grid, block, 0, stream, 0, tokens, past_len, static_cast<const T*>(wte),
                     static_cast<const T*>(wpe), static_cast<const T*>(gamma), static_cast<const T*>(beta), x,
-                    static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, err);
+                    static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, idle_slots, err);
 }
 
 namespace {

@@ -132,10 +132,13 @@ cudaError_t launch_attention_backward_tc(gpt2_dtype dt, const void* qkv, const v
 cudaError_t launch_attention_f32(const float* qkv, float* out, int B, int T, int n_head, float score_scale,
                                  cudaStream_t stream);
 
-// Decode-step kernels (16-bit paths; dt GPT2_BF16 or GPT2_F16).
+// Decode-step kernels (16-bit paths; dt GPT2_BF16 or GPT2_F16).  With
+// idle_slots a past_len of -1 is a slot without a sequence: not valid, and no
+// error.
 cudaError_t launch_decode_embed_ln(gpt2_dtype dt, const int32_t* tokens, const int32_t* past_len, const void* wte,
                                    const void* wpe, const void* gamma, const void* beta, float* x, void* y, int B,
-                                   int D, int V, int n_pos, int T_max, float eps, int* valid, cudaStream_t stream);
+                                   int D, int V, int n_pos, int T_max, float eps, int* valid, cudaStream_t stream,
+                                   bool idle_slots = false);
 // Rows 0..B-1 of qkv / out / past_len / valid are sequences b_cache0 ..
 // b_cache0 + B - 1 of a cache laid out for B_cache sequences.
 cudaError_t launch_decode_attention(gpt2_dtype dt, const void* qkv, void* kv_layer, void* out, const int32_t* past_len,
@@ -146,8 +149,10 @@ cudaError_t launch_decode_attention(gpt2_dtype dt, const void* qkv, void* kv_lay
 cudaError_t launch_kv_from_qkv(gpt2_dtype dt, const void* qkv, void* kv_layer, int B, int T, int n_head, int T_max,
                                cudaStream_t stream);
 // x_last[b] = x[b T + T - 1] (fp32 [B, D]), valid[b] = 1, past_len[b] = T.
+// With from_zero a sequence whose past_len is not 0 is not valid (an error)
+// and keeps its past_len.
 cudaError_t launch_prefill_last_rows(const float* x, int B, int T, int D, float* x_last, int* valid,
-                                     int32_t* past_len, cudaStream_t stream);
+                                     int32_t* past_len, cudaStream_t stream, bool from_zero = false);
 // past_len may be null in the two argmax launchers (no increment).
 cudaError_t launch_argmax_rows(const float* logits, int64_t ld, int B, int V, const int* valid, int32_t* next_tokens,
                                int32_t* past_len, cudaStream_t stream);
@@ -165,6 +170,31 @@ cudaError_t launch_lse_from_logits(const float* logits, int64_t ld, int64_t M, i
                                    float2* part, float* tgt, cudaStream_t stream);
 cudaError_t launch_argmax_candidates(const float2* cand, int n_cand, int B, const int* valid, int32_t* next_tokens,
                                      int32_t* past_len, cudaStream_t stream);
+
+// Paged key-value cache (16-bit paths; paged_attention.cu, pages.cu).  The
+// cache struct and what each call does are described in gpt2gb.h.
+constexpr int kMaxPagedSeqs = 1024;
+bool attention_paged_fits(const gpt2_paged_cache* c, int n_head);
+size_t attention_paged_workspace(const gpt2_paged_cache* c, int n_head);
+cudaError_t launch_attention_paged(const gpt2_paged_cache* c, int layer, const void* q, int64_t ldq,
+                                   const void* k_new, const void* v_new, int64_t ldkv, void* out, int64_t ldo,
+                                   float* lse, int n_head, float score_scale, int window, int sinks, void* ws,
+                                   cudaStream_t s);
+size_t pages_workspace(const gpt2_paged_cache* c);
+cudaError_t launch_pages_free(const gpt2_paged_cache* c, const int32_t* rows, int n, int keep_first, int keep_last,
+                              cudaStream_t s);
+cudaError_t launch_pages_fork(const gpt2_paged_cache* c, const int32_t* parents, const int32_t* children, int n,
+                              cudaStream_t s);
+cudaError_t launch_pages_reserve(const gpt2_paged_cache* c, const int32_t* n_new, void* ws, cudaStream_t s);
+cudaError_t launch_pages_compact(const gpt2_paged_cache* c, int32_t* n_used, void* ws, cudaStream_t s);
+cudaError_t launch_pages_write(const gpt2_paged_cache* c, int layer, const void* k, const void* v, int64_t ldkv,
+                               int T, const int32_t* n_new, cudaStream_t s);
+
+// Scores from stored logits (logprobs.cu; gpt2_token_logprobs in gpt2gb.h).
+constexpr int kMaxTopN = 32;
+cudaError_t launch_token_logprobs(const void* logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V,
+                                  const int32_t* tokens, float* logprob, float* entropy, float* lse, int top_n,
+                                  int32_t* top_ids, float* top_logprobs, cudaStream_t s);
 
 // 16-bit backward kernels (backward_16.cu; bf16).
 // out[N] = column sums of in[M, N] (row pitch ld; fp32 or, with in16, bf16),

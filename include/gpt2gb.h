@@ -447,6 +447,167 @@ int gpt2_decode_step(const gpt2_dims *dims, const gpt2_model_weights *w, void *k
                      int32_t *past_len, const int32_t *tokens, int32_t *next_tokens, float *logits_opt, int64_t ld,
                      void *ws, size_t ws_bytes, gpt2_stream_t stream);
 
+/* ---------------------------------------------------------- paged KV cache
+ * A key-value cache cut into pages of page_size positions, each of them one
+ * contiguous block with the K and V of all layers:
+ *   pages [n_pages, n_layer, 2 (K, V), n_kv_head, page_size, 64]
+ * of type `dtype`.  Sequence b keeps positions c * page_size ..
+ * (c + 1) * page_size - 1 on page table[b, c] (-1: none).  Pages may be shared
+ * between sequences; refs[p] is the number of table entries that name page p
+ * (0: the page is free).  lens[b] is the number of positions that sequence b
+ * holds, or -1 for a slot without a sequence.
+ * The caller owns all four device buffers and starts with refs 0, table -1
+ * and lens -1; a new sequence begins with lens[b] = 0.  The state lives on the
+ * device, so that a whole serving step (reserve, decode) can be captured into
+ * a CUDA graph.  A struct whose table and lens point at a later slot, with a
+ * smaller n_seq, is a cache of those slots alone.
+ *   page_size a multiple of 16 and at most 4096; n_seq at most 1024; max_pages
+ *   is the length of a table row, with max_pages * page_size < 2^31.  16-bit
+ *   types only (GPT2_ERR_UNSUPPORTED for GPT2_F32). */
+typedef struct {
+  void *pages;
+  int32_t *refs;  /* [n_pages] */
+  int32_t *table; /* [n_seq, max_pages] */
+  int32_t *lens;  /* [n_seq] */
+  int n_pages, page_size, n_layer, n_kv_head, n_seq, max_pages;
+  gpt2_dtype dtype;
+} gpt2_paged_cache;
+
+/* Bytes of gpt2_paged_cache.pages (0 if the struct is invalid; its pointers
+ * are not looked at). */
+size_t gpt2_paged_cache_bytes(const gpt2_paged_cache *cache);
+
+/* Workspace of gpt2_pages_reserve and gpt2_pages_compact. */
+size_t gpt2_pages_workspace_bytes(const gpt2_paged_cache *cache);
+
+/* Makes room for n_new[b] more positions of every sequence b (int32 [n_seq]
+ * device; rows with lens[b] < 0 or n_new[b] <= 0 are left alone): table
+ * entries of positions lens[b] .. lens[b] + n_new[b] - 1 that are -1 receive a
+ * free page, and where such an entry's page is shared it is replaced by a free
+ * page, with the positions below lens[b] that it holds copied there in every
+ * layer (its other positions are left as they were).  Of the sequences
+ * that write to one shared page in the same call the last (highest b) keeps
+ * it if no other entry names it.  Free pages are taken lowest id first, for
+ * the entries in the order (b, c).  lens is not changed.
+ * When positions do not fit the table, an entry names no page of the cache, or
+ * free pages run short, nothing is changed and GPT2_ERR_RANGE is recorded on
+ * the device. */
+int gpt2_pages_reserve(const gpt2_paged_cache *cache, const int32_t *n_new, void *ws, size_t ws_bytes,
+                       gpt2_stream_t stream);
+
+/* Sequence children[i] becomes a copy of sequence parents[i], for all i < n at
+ * once (int32 [n] device each; parents are read as they were before the call,
+ * so beams may be permuted): it shares the pages that hold the parent's
+ * positions and takes its length; the pages that it named before lose a
+ * reference.  No cache contents move: gpt2_pages_reserve splits off what is
+ * written to later.  children must be distinct and all indices in
+ * [0, n_seq), else nothing is changed and GPT2_ERR_RANGE is recorded.
+ * 0 <= n <= n_seq. */
+int gpt2_pages_fork(const gpt2_paged_cache *cache, const int32_t *parents, const int32_t *children, int n,
+                    gpt2_stream_t stream);
+
+/* Gives back pages of sequences seqs[i], i < n (int32 [n] device, distinct, in
+ * [0, n_seq), else nothing is changed and GPT2_ERR_RANGE is recorded): entries
+ * become -1 and their pages lose a reference.  With keep_first = keep_last = 0
+ * the whole sequence goes and lens becomes -1.  Otherwise pages that hold one
+ * of the first keep_first or of the last keep_last positions stay, as do pages
+ * that reach behind lens, and lens does not change: with keep_first = sinks
+ * and keep_last = window - 1 nothing that a later query under that window sees
+ * is given back.  0 <= n <= n_seq. */
+int gpt2_pages_free(const gpt2_paged_cache *cache, const int32_t *seqs, int n, int keep_first, int keep_last,
+                    gpt2_stream_t stream);
+
+/* Moves the pages in use to the ids 0 .. U - 1, U of them (written to
+ * *n_used, device): the first free page below U takes the contents of the last
+ * page in use, and so on.  refs and every entry of the n_seq table rows follow
+ * (pages named by another table, or by rows outside this struct, must not be
+ * compacted).  Contents of pages at or above U are no longer defined by the
+ * call. */
+int gpt2_pages_compact(const gpt2_paged_cache *cache, int32_t *n_used, void *ws, size_t ws_bytes,
+                       gpt2_stream_t stream);
+
+/* Stores the K and V of new tokens of one layer: row b * T + t of k and v (n_kv_head * 64
+ * values of the cache's type, row stride ldkv elements, a multiple of 8) goes
+ * to position lens[b] + t of sequence b, for t < n_new[b] (int32 [n_seq]
+ * device; NULL: all T).  Rows of slots with lens[b] < 0 are skipped.  k and v
+ * may point into a c_attn output [n_seq * T, 3D].  The pages must be there
+ * and not shared (gpt2_pages_reserve); a position without a page is skipped
+ * and GPT2_ERR_RANGE recorded.  n_seq * T < 2^31. */
+int gpt2_pages_write(const gpt2_paged_cache *cache, int layer, const void *k, const void *v, int64_t ldkv, int T,
+                     const int32_t *n_new, gpt2_stream_t stream);
+
+/* Workspace of gpt2_attention_paged (depends on the current device). */
+size_t gpt2_attention_paged_workspace_bytes(const gpt2_paged_cache *cache, int n_head);
+
+/* Attention of one new token per sequence over the paged cache ("逐行拆GPT-2
+ * 源码", GPT2Attention with past key-values), with query heads that may share
+ * key-value heads and an optional sliding window:
+ *   out[b, h*64 + d] = sum_{p visible} softmax_p(score_scale q[b, h] . K[b, p,
+ *   g]) V[b, p, g, d],   g = h / (n_head / n_kv_head)
+ * over the n = lens[b] cached positions and, when k_new and v_new are given,
+ * the new token's own at position lens[b] (n = lens[b] + 1), which are also
+ * stored in the cache there (its page must be there and not shared, see
+ * gpt2_pages_reserve; lens is not changed).  window = 0: every position is
+ * visible; window > 0: those with p >= n - window or p < sinks.  Entries of
+ * table rows for pages without a visible position are not read.
+ *   q [n_seq, n_head * 64] with row stride ldq; k_new, v_new (both or neither)
+ *   [n_seq, n_kv_head * 64] with row stride ldkv; out [n_seq, n_head * 64] with
+ *   row stride ldo, all of the cache's type, strides in elements and multiples of 8 (q, k_new and
+ *   v_new may point into one c_attn output); lse: NULL or fp32 [n_seq, n_head]:
+ *   log2 sum_{p visible} 2^(score_scale log2(e) q . K), as
+ *   gpt2_attention_causal_lse.  out must not overlap q, k_new or v_new.
+ *   n_head a multiple of n_kv_head.
+ * Scores, softmax statistics and sums are fp32, and the probabilities enter
+ * the product with V as the sum of two 16-bit numbers.  A sequence without a
+ * visible position gets zeros and an lse of -inf; rows of slots with lens[b] < 0 are left as they
+ * were.  Positions on a page that the table does not name are left out, and a
+ * sequence longer than its table row is skipped; both record GPT2_ERR_RANGE.
+ * Results do not depend on timing.  ws: gpt2_attention_paged_workspace_bytes
+ * bytes, 256-byte aligned; calls that may run at the same time need one each. */
+int gpt2_attention_paged(const gpt2_paged_cache *cache, int layer, const void *q, int64_t ldq, const void *k_new,
+                         const void *v_new, int64_t ldkv, void *out, int64_t ldo, float *lse, int n_head,
+                         float score_scale, int window, int sinks, void *ws, size_t ws_bytes, gpt2_stream_t stream);
+
+/* gpt2_prefill into a paged cache of n_seq sequences with n_kv_head = n_head:
+ * every sequence must have lens[b] = 0 and pages for T positions
+ * (gpt2_pages_reserve); sets lens[b] = T.  A sequence with another length is
+ * left as it was and GPT2_ERR_RANGE recorded.  tokens [n_seq, T]; the other
+ * arguments as gpt2_prefill.  The prompt's own attention is causal over all of
+ * it (no window). */
+size_t gpt2_prefill_paged_workspace_bytes(const gpt2_dims *dims, const gpt2_paged_cache *cache, int T);
+int gpt2_prefill_paged(const gpt2_dims *dims, const gpt2_model_weights *w, const gpt2_paged_cache *cache,
+                       const int32_t *tokens, int T, int32_t *next_tokens, float *logits_opt, int64_t ld, void *ws,
+                       size_t ws_bytes, gpt2_stream_t stream);
+
+/* gpt2_decode_step over a paged cache (n_kv_head = n_head): position lens[b]
+ * of each sequence, its page reserved before (gpt2_pages_reserve with n_new =
+ * 1), attention as gpt2_attention_paged with `window` and `sinks`; lens[b] +=
+ * 1.  Slots with lens[b] = -1 are skipped: their next_tokens stay, and their
+ * row of logits_opt is not defined. */
+size_t gpt2_decode_step_paged_workspace_bytes(const gpt2_dims *dims, const gpt2_paged_cache *cache);
+int gpt2_decode_step_paged(const gpt2_dims *dims, const gpt2_model_weights *w, const gpt2_paged_cache *cache,
+                           int window, int sinks, const int32_t *tokens, int32_t *next_tokens, float *logits_opt,
+                           int64_t ld, void *ws, size_t ws_bytes, gpt2_stream_t stream);
+
+/* Scores of tokens from stored logits z [M, ld] of type logits_t (any of the
+ * three; V <= ld, ld times the element size a multiple of 16 bytes), as
+ * gpt2_forward_logits or a decode step leaves them.  Per row, each of the
+ * outputs that is given (at least one):
+ *   lse[m] = log sum_v e^(z_v); logprob[m] = z_t - lse with t = tokens[m]
+ *   (int32 [M] device; an id outside [0, V) gives NaN and GPT2_ERR_RANGE);
+ *   entropy[m] = -sum_v p(v) log p(v), p = e^(z - lse) (a logit of -inf adds
+ *   nothing); top_ids, top_logprobs [M, top_n]: the top_n most likely tokens
+ *   and their log probabilities, larger first, lowest id first on ties (a NaN
+ *   ranks as -inf).
+ * All outputs are fp32 (ids int32); sums in fp32 in a fixed order.  tokens and
+ * logprob go together, as do top_ids and top_logprobs (top_n = 0 without
+ * them).  0 <= top_n <= min(32, V).  A row with a NaN or +inf, or with
+ * nothing but -inf, has no distribution: its sums and log probabilities are
+ * NaN. */
+int gpt2_token_logprobs(const void *logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V, const int32_t *tokens,
+                        float *logprob, float *entropy, float *lse, int top_n, int32_t *top_ids,
+                        float *top_logprobs, gpt2_stream_t stream);
+
 /* ------------------------------------------------------------ profiling
  * Per-kernel timing of the calls made between gpt2_profile_begin() and
  * gpt2_profile_end(): the library records a CUDA event on the launching
