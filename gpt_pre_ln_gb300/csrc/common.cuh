@@ -43,6 +43,8 @@ enum ErrSite : unsigned {
   kSitePagedRow = 22,     // a sequence out of range, or named twice
   kSitePagedFull = 23,    // too few free pages
   kSiteScoreToken = 24,
+  kSiteScoreLoad = 25,
+  kSiteScoreJoin = 26,
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per wait

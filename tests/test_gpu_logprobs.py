@@ -202,3 +202,10 @@ def test_captured_and_on_another_stream():
     torch.cuda.synchronize()
     ref = _run(z, 5003, "f32", 5, tokens)
     assert torch.equal(ids.cpu(), ref["ids"]) and torch.equal(out[0].cpu(), ref["logprob"])
+
+
+@pytest.mark.parametrize("dtype, M, V", [("bf16", 6000, 1003), ("f32", 6000, 203), ("f32", 700, 52001),
+                                         ("f32", 400, 110003), ("bf16", 300, 300007)])
+def test_many_rows_through_the_same_buffers(dtype, M, V):
+    """More rows than CTAs (or clusters) are resident: each takes a dozen or more in turn."""
+    _check(_logits(M, V, dtype, seed=V), V, dtype, 20)
