@@ -43,6 +43,7 @@ enum ErrSite : unsigned {
   kSitePagedRow = 22,     // a sequence out of range, or named twice
   kSitePagedFull = 23,    // too few free pages
   kSiteScoreToken = 24,
+  kSitePagedLoad = 27,
   kSiteScoreLoad = 25,
   kSiteScoreJoin = 26,
 };

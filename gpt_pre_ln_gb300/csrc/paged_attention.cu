@@ -13,10 +13,11 @@
 // key-value head) and takes 4 * 64 flop per query head: at most 16 flop a byte
 // with 16 heads to a key-value head, far under what the tensor cores need to
 // be the limit, so the kernel is bound by HBM bandwidth and its layout serves
-// the loads.  The products run as mma.sync m16n8k16 on fragments loaded from
-// global memory straight into registers: no shared memory, no barriers, no
-// waits, and nothing to gain from tcgen05, whose operands would have to pass
-// through shared memory first.
+// the loads: each warp runs its own ring of TMA boxes (16 rows of K, 16 of V),
+// 128 KB of them on an SM, and waits for nobody else.  The products
+// are mma.sync m16n8k16 with the few query heads as rows: a tcgen05 tile would
+// be 128 rows, its operands shared by four warps, and the kernel has no use for
+// the rate.
 #include <type_traits>
 
 #include "common.cuh"
@@ -29,7 +30,13 @@ namespace {
 constexpr int kHd = 64;
 constexpr int kTile = 16;    // positions per tile; page sizes are multiples of it
 constexpr int kWarps = 4;    // warps per CTA, independent of one another
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 4;
+constexpr int kStages = 2;   // tiles per warp in flight or in use (3: 143 us instead of 137, see below)
+constexpr int kMinRun = 2;   // tiles per warp at least
+constexpr int kBoxBytes = kTile * kHd * 2;
+constexpr int kStageBytes = 2 * kBoxBytes;  // K, then V
+constexpr int kWarpBytes = kStages * kStageBytes;
+static_assert(kWarpBytes >= 16 * kHd * 4, "a warp's result fits its ring");
 
 template <typename T16>
 struct PagedArgs {
@@ -39,13 +46,14 @@ struct PagedArgs {
   T16* out;
   float* lse;  // nullable, [n_seq, H]
   T16* pages;  // the layer's part of page 0
+  int row0, page_rows;  // the pool as rows of 64: the layer's first row, rows per page
   const int32_t* table;
   const int32_t* lens;
   int* plan;       // base[n_seq + 1], then tiles per warp
   float* part_o;   // [2 * warps, HB, 64]
   float2* part_ml;  // [2 * warps, HB]: running maximum (log2 units) and sum
   unsigned* err;
-  long long ldq, ldkv, ldo, page_stride;
+  long long ldq, ldkv, ldo;
   int n_pages, page_size, max_pages, n_seq, n_kv, H, group;
   int n_hb, HB;  // blocks of query heads per key-value head, heads per block
   int window, sinks;
@@ -78,14 +86,6 @@ __device__ __forceinline__ Span span_of(const PagedArgs<T16>& a, int b, bool rec
   return s;
 }
 
-__device__ __forceinline__ uint4 load16(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
-
 template <typename T16>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -101,19 +101,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// One tile's keys and values in a warp's registers.  Lane (r = lane / 4,
-// j = lane % 4) holds of key rows r and r + 8 the dimensions 8j..8j+7 and
-// 32+8j..32+8j+7, and of value rows 2j, 2j+1, 2j+8, 2j+9 the dimensions
-// 8r..8r+7, each 16 bytes.  The sums over dimensions and the order of output
-// dimensions are free, so these are the B fragments of both products as they
-// come: keys with the contraction index permuted alike in q, values with
-// output column r of product t standing for dimension 8r + t.
-struct TileRegs {
-  uint4 k[2][2];
-  uint4 v[4];
-  int pos0;  // first position, or -1: the tile's page is not there
-};
-
 // (p rounded, what that lost) in 16 bits, so that their sum carries p to 16
 // bits (bf16) or 22 bits (fp16).
 template <typename T16>
@@ -123,21 +110,347 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
   lo = Type16<T16>::pack2(x - h.x, y - h.y);
 }
 
+// A warp's ring of tiles.
+struct Ring {
+  const CUtensorMap* map;
+  uint8_t* buf;   // [kStages][K box, V box], 1024-byte aligned
+  uint64_t* bar;  // [kStages]
+  int slot, parity;  // of the tile to take next
+};
+
+// What one warp makes of a run of tiles of one item: o (not divided by l), m
+// (log2 units) and l of its query heads.  Lane (r = lane / 4, j = lane % 4)
+// holds head r (and r + 8 when WIDE, in the upper halves): o[i] its dimensions
+// 16j + i and 16j + 8 + i.
+struct Acc {
+  float o[8][4];
+  float m[2], l[2];
+};
+
+// Where an item's keys, values and queries are.
+template <typename T16>
+struct Item {
+  Span sp;
+  const int32_t* pages;  // the sequence's table row
+  const T16* q;          // its first query head
+  const T16* k_new;      // the new token's rows of this key-value head
+  const T16* v_new;
+  int b, kvh, hb, head0, heads;
+};
+
+template <typename T16>
+__device__ __forceinline__ Item<T16> item_of(const PagedArgs<T16>& a, int b, int item, const Span& sp) {
+  Item<T16> x;
+  x.sp = sp;
+  x.b = b;
+  x.kvh = item / a.n_hb;
+  x.hb = item - x.kvh * a.n_hb;
+  x.head0 = x.kvh * a.group + x.hb * a.HB;
+  x.heads = min(a.HB, a.group - x.hb * a.HB);
+  x.pages = a.table + static_cast<long long>(b) * a.max_pages;
+  x.q = a.q + b * a.ldq + static_cast<long long>(x.head0) * kHd;
+  x.k_new = a.k_new ? a.k_new + b * a.ldkv + x.kvh * kHd : nullptr;
+  x.v_new = a.k_new ? a.v_new + b * a.ldkv + x.kvh * kHd : nullptr;
+  return x;
+}
+
+// fp16 probabilities are carried 2^12 times larger: their smallest step is then
+// 2^-36 of the row's largest and not 2^-24.
+template <typename T16>
+constexpr float kShift = std::is_same<T16, __half>::value ? 12.f : 0.f;
+
+// Attention of an item's query heads over its tiles j0, j0 + step, ... (cnt of
+// them) by one warp.  False if a wait ran out.
+//
+// The B fragments of both products come out of shared memory as they are:
+// sums over dimensions and the order of output dimensions are free, so lane
+// (r, j) reads of key rows r and r + 8 the dimensions 16j..16j+15 (q is loaded
+// alike) and of value rows 2j, 2j+1, 2j+8, 2j+9 the dimensions 8r..8r+7, where
+// output column r of product i stands for dimension 8r + i.  With the boxes'
+// 128-byte swizzle (16-byte unit u of row x at u ^ (x & 7)) the eight lanes of
+// a 16-byte access phase touch eight different units, so no bank twice.
+//
+// WIDE: 9 to 16 query heads fill the 16 rows of the A operand; the rounding
+// remainder of p then takes a second product.  Up to 8 heads leave rows 8..15
+// free and the remainder rides there.
+template <typename T16, bool WIDE>
+__device__ __forceinline__ bool attend(const PagedArgs<T16>& a, const Item<T16>& x, int j0, int step, int cnt,
+                                       Ring& ring, Acc& acc) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+  const int n = x.sp.n, pos_new = x.k_new ? n - 1 : -1;
+  constexpr int kRows = WIDE ? 2 : 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc.o[i][e] = 0.f;
+  acc.m[0] = acc.m[1] = -INFINITY;
+  acc.l[0] = acc.l[1] = 0.f;
+  auto tile_no = [&](int i) {
+    const int t = j0 + i * step;
+    return t < x.sp.ts ? t : x.sp.tw + (t - x.sp.ts);
+  };
+  // lane i: first row (K) of tile (i + a multiple of 32) of this run, -1 when
+  // its page is not there
+  int rows32 = -1, fetched = 0;
+  auto issue = [&](int i, int slot) {
+    if ((i & 31) == 0) {
+      rows32 = -1;
+      if (i + lane < cnt) {
+        const int pos = tile_no(i + lane) * kTile, c = pos / a.page_size;
+        const int page = x.pages[c];
+        if (page >= 0 && page < a.n_pages)
+          rows32 = page * a.page_rows + a.row0 + x.kvh * a.page_size + (pos - c * a.page_size);
+        else
+          record_error(a.err, kErrRange, kSitePagedPage);
+      }
+    }
+    const int row = __shfl_sync(0xffffffffu, rows32, i & 31);
+    if (lane == 0) {
+      const uint32_t bar = smem_u32(&ring.bar[slot]), dst = smem_u32(ring.buf + slot * kStageBytes);
+      if (row >= 0) {
+        mbar_arrive_expect_tx(bar, kStageBytes);
+        tma_load_2d(dst, ring.map, bar, 0, row);
+        tma_load_2d(dst + kBoxBytes, ring.map, bar, 0, row + a.n_kv * a.page_size);
+      } else {
+        mbar_arrive(bar);  // nothing to wait for
+      }
+    }
+    return row;
+  };
+  int rows[kStages];  // of the tiles in the ring, oldest first
+  int slot = ring.slot;
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) {
+    rows[s] = -1;
+    if (fetched < cnt) {
+      rows[s] = issue(fetched, slot);
+      ++fetched;
+      slot = slot + 1 == kStages ? 0 : slot + 1;
+    }
+  }
+  // q: lane (r, j) holds dimensions 16j..16j+15 of rows r (and r + 8)
+  uint4 qa[2] = {}, qb[2] = {};
+  if (r < x.heads) {
+    qa[0] = *reinterpret_cast<const uint4*>(x.q + static_cast<long long>(r) * kHd + 16 * j);
+    qa[1] = *reinterpret_cast<const uint4*>(x.q + static_cast<long long>(r) * kHd + 16 * j + 8);
+  }
+  if (WIDE && r + 8 < x.heads) {
+    qb[0] = *reinterpret_cast<const uint4*>(x.q + static_cast<long long>(r + 8) * kHd + 16 * j);
+    qb[1] = *reinterpret_cast<const uint4*>(x.q + static_cast<long long>(r + 8) * kHd + 16 * j + 8);
+  }
+  // the new token's row: lanes 0..7 its key, 8..15 its value, 16 bytes each
+  uint4 fresh = make_uint4(0, 0, 0, 0);
+  const bool has_new = pos_new >= 0 && j0 + (cnt - 1) * step == x.sp.nt - 1;
+  if (has_new && lane < 16) fresh = *(reinterpret_cast<const uint4*>(lane < 8 ? x.k_new : x.v_new) + (lane & 7));
+  auto visible = [&](int p) { return p < n && (a.window <= 0 || p >= n - a.window || p < a.sinks); };
+
+  for (int i = 0; i < cnt; ++i) {
+    const bool ok = mbar_wait(smem_u32(&ring.bar[ring.slot]), ring.parity);
+    if (!__all_sync(0xffffffffu, ok)) {
+      if (lane == 0) {
+        record_error(a.err, kErrTimeout, kSitePagedLoad);
+        for (int s = 0; s < kStages && i + s < cnt; ++s) {  // the loads in flight must not outlive the CTA
+          const int k = ring.slot + s;
+          (void)mbar_wait(smem_u32(&ring.bar[k % kStages]), ring.parity ^ (k >= kStages ? 1 : 0));
+        }
+      }
+      __syncwarp();
+      return false;
+    }
+    uint8_t* kb = ring.buf + ring.slot * kStageBytes;
+    uint8_t* vb = kb + kBoxBytes;
+    const int row = rows[0], pos0 = tile_no(i) * kTile;
+    if (has_new && i == cnt - 1 && row >= 0) {
+      const int at = pos_new - pos0;
+      if (lane < 16) {
+        *reinterpret_cast<uint4*>((lane < 8 ? kb : vb) + at * 128 + (((lane & 7) ^ (at & 7)) << 4)) = fresh;
+        if (x.hb == 0) {
+          T16* to = a.pages + (static_cast<long long>(row - a.row0) + at + (lane < 8 ? 0 : a.n_kv * a.page_size)) * kHd;
+          *reinterpret_cast<uint4*>(to + (lane & 7) * 8) = fresh;
+        }
+      }
+      __syncwarp();
+    }
+    if (row >= 0) {
+      float s[2][4];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint8_t* kr = kb + (r + 8 * e) * 128;
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kr + (((2 * j) ^ r) << 4));
+        const uint4 k1 = *reinterpret_cast<const uint4*>(kr + (((2 * j + 1) ^ r) << 4));
+        s[e][0] = s[e][1] = s[e][2] = s[e][3] = 0.f;
+        mma16816<T16>(s[e], qa[0].x, qb[0].x, qa[0].y, qb[0].y, k0.x, k0.y);
+        mma16816<T16>(s[e], qa[0].z, qb[0].z, qa[0].w, qb[0].w, k0.z, k0.w);
+        mma16816<T16>(s[e], qa[1].x, qb[1].x, qa[1].y, qb[1].y, k1.x, k1.y);
+        mma16816<T16>(s[e], qa[1].z, qb[1].z, qa[1].w, qb[1].w, k1.z, k1.w);
+      }
+      uint4 v[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int vr = 2 * j + (e & 1) + (e >> 1) * 8;
+        v[e] = *reinterpret_cast<const uint4*>(vb + vr * 128 + ((r ^ (vr & 7)) << 4));
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < 2 * kRows; ++k) s[e][k] *= a.scale_log2;
+      // a tile with rows outside the window, behind the end or before the
+      // window's first: their scores go to -inf and their values to zero (a
+      // row that nothing wrote may hold anything, NaN among it)
+      const bool whole = pos0 + kTile <= n && (a.window <= 0 || pos0 >= n - a.window || pos0 + kTile <= a.sinks);
+      if (!whole) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (!visible(pos0 + 8 * e + 2 * j + k)) {
+              s[e][k] = -INFINITY;
+              s[e][k + 2] = -INFINITY;
+              v[2 * e + k] = make_uint4(0, 0, 0, 0);
+            }
+      }
+      float alpha[2] = {1.f, 1.f};
+#pragma unroll
+      for (int g = 0; g < kRows; ++g) {
+        float mx = fmaxf(fmaxf(s[0][2 * g], s[0][2 * g + 1]), fmaxf(s[1][2 * g], s[1][2 * g + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(acc.m[g], mx);
+        const float ms = mn == -INFINITY ? 0.f : mn;  // every score so far is -inf
+        alpha[g] = acc.m[g] == mn ? 1.f : ex2_approx(acc.m[g] - ms);
+        acc.m[g] = mn;
+        acc.l[g] *= alpha[g];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            s[e][2 * g + k] = ex2_approx(s[e][2 * g + k] - ms + kShift<T16>);
+            acc.l[g] += s[e][2 * g + k];
+          }
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc.o[k][0] *= alpha[0];
+          acc.o[k][1] *= alpha[0];
+          acc.o[k][2] *= alpha[WIDE ? 1 : 0];
+          acc.o[k][3] *= alpha[WIDE ? 1 : 0];
+        }
+      }
+      uint32_t ph[2][2], pl[2][2];  // [position half][head half]
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int g = 0; g < kRows; ++g) split2<T16>(s[e][2 * g], s[e][2 * g + 1], ph[e][g], pl[e][g]);
+      const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&v[0]);
+      const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&v[1]);
+      const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&v[2]);
+      const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&v[3]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
+        const uint32_t b0 = __byte_perm(v0[k >> 1], v1[k >> 1], sel);
+        const uint32_t b1 = __byte_perm(v2[k >> 1], v3[k >> 1], sel);
+        if constexpr (WIDE) {
+          mma16816<T16>(acc.o[k], ph[0][0], ph[0][1], ph[1][0], ph[1][1], b0, b1);
+          mma16816<T16>(acc.o[k], pl[0][0], pl[0][1], pl[1][0], pl[1][1], b0, b1);
+        } else {
+          mma16816<T16>(acc.o[k], ph[0][0], pl[0][0], ph[1][0], pl[1][0], b0, b1);
+        }
+      }
+    }
+    // the slot is read: the tile kStages further on
+    __syncwarp();
+    if (lane == 0) fence_proxy_async_smem();
+#pragma unroll
+    for (int s = 0; s + 1 < kStages; ++s) rows[s] = rows[s + 1];
+    rows[kStages - 1] = -1;
+    if (fetched < cnt) {
+      rows[kStages - 1] = issue(fetched, ring.slot);
+      ++fetched;
+    }
+    if (++ring.slot == kStages) {
+      ring.slot = 0;
+      ring.parity ^= 1;
+    }
+  }
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {  // sums over the four lanes of a row
+    acc.l[g] += __shfl_xor_sync(0xffffffffu, acc.l[g], 1);
+    acc.l[g] += __shfl_xor_sync(0xffffffffu, acc.l[g], 2);
+  }
+  if (!WIDE) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      acc.o[i][0] += acc.o[i][2];
+      acc.o[i][1] += acc.o[i][3];
+    }
+  }
+  return true;
+}
+
+// The rows of one warp's result: dst[head][64], ml[head] = (m, l).
+template <typename T16, bool WIDE>
+__device__ __forceinline__ void put_piece(const Acc& acc, int heads, float* dst, float2* ml) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int g = 0; g < (WIDE ? 2 : 1); ++g) {
+    const int hh = r + 8 * g;
+    if (hh >= heads) continue;
+    float* po = dst + hh * kHd + 16 * j;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      *reinterpret_cast<float4*>(po + 8 * e) =
+          make_float4(acc.o[0][2 * g + e], acc.o[1][2 * g + e], acc.o[2][2 * g + e], acc.o[3][2 * g + e]);
+      *reinterpret_cast<float4*>(po + 8 * e + 4) =
+          make_float4(acc.o[4][2 * g + e], acc.o[5][2 * g + e], acc.o[6][2 * g + e], acc.o[7][2 * g + e]);
+    }
+    if (j == 0) ml[hh] = make_float2(acc.m[g] - kShift<T16>, acc.l[g]);
+  }
+}
+
+// Adds a piece (its 4 values x, its m and l) to (acc, M, L).
+__device__ __forceinline__ void merge(float4& acc, float& M, float& L, const float4& x, const float2& ml) {
+  if (ml.y == 0.f) return;  // nothing in it but scores of -inf
+  const float mn = fmaxf(M, ml.x);
+  const float c0 = M == mn ? 1.f : ex2_approx(M - mn), c1 = ml.x == mn ? 1.f : ex2_approx(ml.x - mn);
+  M = mn;
+  L = L * c0 + ml.y * c1;
+  acc.x = acc.x * c0 + x.x * c1;
+  acc.y = acc.y * c0 + x.y * c1;
+  acc.z = acc.z * c0 + x.z * c1;
+  acc.w = acc.w * c0 + x.w * c1;
+}
+
+template <typename T16>
+__device__ __forceinline__ Ring ring_of(const CUtensorMap* map, uint8_t* smem, uint64_t* bars, int warp) {
+  Ring ring{map, smem + warp * kWarpBytes, bars + warp * kStages, 0, 0};
+  if ((threadIdx.x & 31) == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&ring.bar[s]), 1);
+    fence_barrier_init();
+  }
+  __syncwarp();
+  return ring;
+}
+
 // Work is cut into equal runs of tiles over all (sequence, key-value head,
 // head block) items laid end to end, one run per warp, whatever the lengths
 // are.  A warp that holds all tiles of an item writes its output; pieces of an
-// item go to the workspace and paged_join adds them up.
-//
-// WIDE: 9 to 16 query heads per block fill the 16 rows of the A operand; the
-// rounding remainder of p then takes a second product.  Up to 8 heads leave
-// rows 8..15 free and the remainder rides there.
+// item go to the workspace and a second kernel joins them.
 template <typename T16, bool WIDE>
-__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn(const PagedArgs<T16> a) {
-  extern __shared__ int s_base[];  // [n_seq + 1]
+__global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
+    paged_attn(const __grid_constant__ CUtensorMap map, const PagedArgs<T16> a) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ __align__(8) uint64_t s_bar[kWarps * kStages];
   __shared__ int s_sum[kWarps];
-  griddep_wait();
-  griddep_launch_dependents();
+  uint8_t* s_tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  int* s_base = reinterpret_cast<int*>(s_tiles + kWarps * kWarpBytes);  // [n_seq + 1]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  Ring ring = ring_of<T16>(&map, s_tiles, s_bar, warp);
+  if (lane == 0) tma_prefetch_desc(&map);
+  // (no early launch of the join: its CTAs, waiting in the places of ours that
+  // are through, cost a window case of 128 sequences 169 us instead of 143)
+  griddep_wait();
   const int items = a.n_kv * a.n_hb;
   // base[b] = tiles of all items of sequences before b
   int carry = 0;
@@ -163,7 +476,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn(const Page
   __syncthreads();
   const int total = carry;
   const int n_warps = gridDim.x * kWarps;
-  const int run = max((total + n_warps - 1) / n_warps, 1);
+  // (a run of fewer than kMinRun tiles would make more pieces than it saves time)
+  const int run = max((total + n_warps - 1) / n_warps, kMinRun);
   if (blockIdx.x == 0) {
     for (int b = tid; b <= a.n_seq; b += kWarps * 32) a.plan[b] = s_base[b];
     if (tid == 0) a.plan[a.n_seq + 1] = run;
@@ -175,9 +489,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn(const Page
   int t = static_cast<int>(t_first);
   const int t_end = static_cast<int>(min(t_first + run, static_cast<long long>(total)));
   const int r = lane >> 2, j = lane & 3;
-  // fp16 probabilities are carried 2^12 times larger: their smallest step is
-  // then 2^-36 of the row's largest and not 2^-24
-  constexpr float kShift = std::is_same<T16, __half>::value ? 12.f : 0.f;
 
   while (t < t_end) {
     int lo = 0, hi = a.n_seq;  // last b with base[b] <= t
@@ -188,311 +499,205 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm) paged_attn(const Page
       else
         hi = mid;
     }
-    const int b = lo;
-    const Span sp = span_of(a, b, false);
-    const int item = (t - s_base[b]) / sp.nt;
-    const int j0 = (t - s_base[b]) - item * sp.nt;  // first tile of this piece within the item
+    const Span sp = span_of(a, lo, false);
+    const int item = (t - s_base[lo]) / sp.nt;
+    const int j0 = (t - s_base[lo]) - item * sp.nt;  // first tile of this piece within the item
     const int cnt = min(sp.nt - j0, t_end - t);
-    const int kvh = item / a.n_hb, hb = item - kvh * a.n_hb;
-    const int head0 = kvh * a.group + hb * a.HB;
-    const int heads = min(a.HB, a.group - hb * a.HB);
-    const int pos_new = a.k_new ? sp.n - 1 : -1;
-    const T16* kn = a.k_new + b * a.ldkv + kvh * kHd;
-    const T16* vn = a.v_new + b * a.ldkv + kvh * kHd;
-    const int32_t* trow = a.table + static_cast<long long>(b) * a.max_pages;
-
-    // q fragments: rows r (and r + 8 when WIDE)
-    uint4 qa[2] = {}, qb[2] = {};
-    {
-      const T16* qr = a.q + b * a.ldq + static_cast<long long>(head0 + r) * kHd + 8 * j;
-      if (r < heads) {
-        qa[0] = load16(qr);
-        qa[1] = load16(qr + 32);
-      }
-      if (WIDE && r + 8 < heads) {
-        qb[0] = load16(qr + 8 * kHd);
-        qb[1] = load16(qr + 8 * kHd + 32);
-      }
-    }
-    float o[8][4];
+    const Item<T16> x = item_of(a, lo, item, sp);
+    Acc acc;
+    if (!attend<T16, WIDE>(a, x, j0, 1, cnt, ring, acc)) return;
+    if (cnt == sp.nt) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+      for (int g = 0; g < (WIDE ? 2 : 1); ++g) {
+        const int hh = r + 8 * g;
+        if (hh >= x.heads) continue;
+        const float l = acc.l[g], inv = l == 0.f ? 0.f : 1.f / l;
+        T16* orow = a.out + x.b * a.ldo + static_cast<long long>(x.head0 + hh) * kHd + 16 * j;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-    int pages32 = -1;  // lane i: the page of tile (tile index & ~31) + i of this piece
-    auto tile_no = [&](int i) { return i < sp.ts ? i : sp.tw + (i - sp.ts); };
-    auto fetch = [&](int i, TileRegs& x) {  // i: tile within the piece
-      if ((i & 31) == 0) {
-        const int ii = j0 + i + lane;
-        pages32 = i + lane < cnt ? trow[tile_no(ii) * kTile / a.page_size] : -1;
-      }
-      const int page = __shfl_sync(0xffffffffu, pages32, i & 31);
-      const int pos0 = tile_no(j0 + i) * kTile;
-      if (page < 0 || page >= a.n_pages) {
-        if (lane == 0) record_error(a.err, kErrRange, kSitePagedPage);
-        x.pos0 = -1;
-        return;
-      }
-      x.pos0 = pos0;
-      const T16* kb = a.pages + page * a.page_stride +
-                      (static_cast<long long>(kvh) * a.page_size + pos0 % a.page_size) * kHd;
-      const T16* vb = kb + static_cast<long long>(a.n_kv) * a.page_size * kHd;
-      const T16* kr[2] = {kb + r * kHd, kb + (r + 8) * kHd};
-      const T16* vr[4] = {vb + (2 * j) * kHd, vb + (2 * j + 1) * kHd, vb + (2 * j + 8) * kHd,
-                          vb + (2 * j + 9) * kHd};
-      const int at = pos_new - pos0;  // the new token's row in this tile
-      if (pos_new >= 0 && at < kTile && at >= 0) {
-        // its key and value come from the caller's rows and go to the cache
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (at == r + 8 * e) kr[e] = kn;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (at == 2 * j + (e & 1) + (e >> 1) * 8) vr[e] = vn;
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        x.k[e][0] = load16(kr[e] + 8 * j);
-        x.k[e][1] = load16(kr[e] + 32 + 8 * j);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x.v[e] = load16(vr[e] + 8 * r);
-      if (pos_new >= 0 && at < kTile && at >= 0 && hb == 0) {
-        T16* kc = const_cast<T16*>(kb) + at * kHd;
-        T16* vc = const_cast<T16*>(vb) + at * kHd;
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-          if (at == r + 8 * e) {
-            *reinterpret_cast<uint4*>(kc + 8 * j) = x.k[e][0];
-            *reinterpret_cast<uint4*>(kc + 32 + 8 * j) = x.k[e][1];
-          }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (at == 2 * j + (e & 1) + (e >> 1) * 8) *reinterpret_cast<uint4*>(vc + 8 * r) = x.v[e];
-      }
-    };
-    auto visible = [&](int p) {
-      return p < sp.n && (a.window <= 0 || p >= sp.n - a.window || p < a.sinks);
-    };
-    auto consume = [&](TileRegs& x) {
-      if (x.pos0 < 0) return;
-      float s[2][4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        s[e][0] = s[e][1] = s[e][2] = s[e][3] = 0.f;
-        mma16816<T16>(s[e], qa[0].x, qb[0].x, qa[0].y, qb[0].y, x.k[e][0].x, x.k[e][0].y);
-        mma16816<T16>(s[e], qa[0].z, qb[0].z, qa[0].w, qb[0].w, x.k[e][0].z, x.k[e][0].w);
-        mma16816<T16>(s[e], qa[1].x, qb[1].x, qa[1].y, qb[1].y, x.k[e][1].x, x.k[e][1].y);
-        mma16816<T16>(s[e], qa[1].z, qb[1].z, qa[1].w, qb[1].w, x.k[e][1].z, x.k[e][1].w);
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[e][i] *= a.scale_log2;
-      // a tile with rows outside the window, behind the end or before the
-      // window's first: their scores go to -inf and their values to zero (a
-      // row that nothing wrote may hold anything, NaN among it)
-      const bool whole = x.pos0 + kTile <= sp.n &&
-                         (a.window <= 0 || x.pos0 >= sp.n - a.window || x.pos0 + kTile <= a.sinks);
-      if (!whole) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-            if (!visible(x.pos0 + 8 * e + 2 * j + i)) {
-              s[e][i] = -INFINITY;
-              s[e][i + 2] = -INFINITY;
-              x.v[2 * e + i] = make_uint4(0, 0, 0, 0);
-            }
-      }
-      constexpr int kRows = WIDE ? 2 : 1;
-      float alpha[2] = {1.f, 1.f};
-#pragma unroll
-      for (int g = 0; g < kRows; ++g) {
-        float mx = fmaxf(fmaxf(s[0][2 * g], s[0][2 * g + 1]), fmaxf(s[1][2 * g], s[1][2 * g + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[g], mx);
-        const float ms = mn == -INFINITY ? 0.f : mn;  // every score so far is -inf
-        alpha[g] = m[g] == mn ? 1.f : ex2_approx(m[g] - ms);
-        m[g] = mn;
-        l[g] *= alpha[g];
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            s[e][2 * g + i] = ex2_approx(s[e][2 * g + i] - ms + kShift);
-            l[g] += s[e][2 * g + i];
-          }
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i][0] *= alpha[0];
-          o[i][1] *= alpha[0];
-          o[i][2] *= alpha[WIDE ? 1 : 0];
-          o[i][3] *= alpha[WIDE ? 1 : 0];
+        for (int e = 0; e < 2; ++e) {
+          uint4 u;
+          u.x = Type16<T16>::pack2(acc.o[0][2 * g + e] * inv, acc.o[1][2 * g + e] * inv);
+          u.y = Type16<T16>::pack2(acc.o[2][2 * g + e] * inv, acc.o[3][2 * g + e] * inv);
+          u.z = Type16<T16>::pack2(acc.o[4][2 * g + e] * inv, acc.o[5][2 * g + e] * inv);
+          u.w = Type16<T16>::pack2(acc.o[6][2 * g + e] * inv, acc.o[7][2 * g + e] * inv);
+          *reinterpret_cast<uint4*>(orow + 8 * e) = u;
         }
+        if (a.lse && j == 0)
+          a.lse[static_cast<long long>(x.b) * a.H + x.head0 + hh] = acc.m[g] - kShift<T16> + log2f(l);
       }
-      uint32_t ph[2][2], pl[2][2];  // [position half][head half]
-#pragma unroll
-      for (int e = 0; e < 2; ++e)
-#pragma unroll
-        for (int g = 0; g < kRows; ++g) split2<T16>(s[e][2 * g], s[e][2 * g + 1], ph[e][g], pl[e][g]);
-      const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&x.v[0]);
-      const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&x.v[1]);
-      const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&x.v[2]);
-      const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&x.v[3]);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t sel = (i & 1) ? 0x7632u : 0x5410u;
-        const uint32_t b0 = __byte_perm(v0[i >> 1], v1[i >> 1], sel);
-        const uint32_t b1 = __byte_perm(v2[i >> 1], v3[i >> 1], sel);
-        if constexpr (WIDE) {
-          mma16816<T16>(o[i], ph[0][0], ph[0][1], ph[1][0], ph[1][1], b0, b1);
-          mma16816<T16>(o[i], pl[0][0], pl[0][1], pl[1][0], pl[1][1], b0, b1);
-        } else {
-          mma16816<T16>(o[i], ph[0][0], pl[0][0], ph[1][0], pl[1][0], b0, b1);
-        }
-      }
-    };
-
-    TileRegs x0, x1;
-    fetch(0, x0);
-    for (int i = 0; i < cnt; i += 2) {
-      if (i + 1 < cnt) fetch(i + 1, x1);
-      consume(x0);
-      if (i + 2 < cnt) fetch(i + 2, x0);
-      if (i + 1 < cnt) consume(x1);
-    }
-
-    // sums over the four lanes of a row
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      l[g] += __shfl_xor_sync(0xffffffffu, l[g], 1);
-      l[g] += __shfl_xor_sync(0xffffffffu, l[g], 2);
-    }
-    if (!WIDE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        o[i][0] += o[i][2];
-        o[i][1] += o[i][3];
-      }
-    }
-    const bool complete = cnt == sp.nt;
-    const int slot = 2 * w + (t == static_cast<int>(t_first) ? 0 : 1);
-    // lane (r, j) holds dimensions 16j + i and 16j + 8 + i of heads r (and r + 8)
-#pragma unroll
-    for (int g = 0; g < (WIDE ? 2 : 1); ++g) {
-      const int hh = r + 8 * g;
-      if (hh < heads) {
-        if (complete) {
-          const float inv = l[g] > 0.f ? 1.f / l[g] : 0.f;
-          T16* orow = a.out + b * a.ldo + static_cast<long long>(head0 + hh) * kHd + 16 * j;
-          uint4 lo4, hi4;
-          lo4.x = Type16<T16>::pack2(o[0][2 * g] * inv, o[1][2 * g] * inv);
-          lo4.y = Type16<T16>::pack2(o[2][2 * g] * inv, o[3][2 * g] * inv);
-          lo4.z = Type16<T16>::pack2(o[4][2 * g] * inv, o[5][2 * g] * inv);
-          lo4.w = Type16<T16>::pack2(o[6][2 * g] * inv, o[7][2 * g] * inv);
-          hi4.x = Type16<T16>::pack2(o[0][2 * g + 1] * inv, o[1][2 * g + 1] * inv);
-          hi4.y = Type16<T16>::pack2(o[2][2 * g + 1] * inv, o[3][2 * g + 1] * inv);
-          hi4.z = Type16<T16>::pack2(o[4][2 * g + 1] * inv, o[5][2 * g + 1] * inv);
-          hi4.w = Type16<T16>::pack2(o[6][2 * g + 1] * inv, o[7][2 * g + 1] * inv);
-          *reinterpret_cast<uint4*>(orow) = lo4;
-          *reinterpret_cast<uint4*>(orow + 8) = hi4;
-          if (a.lse && j == 0) a.lse[static_cast<long long>(b) * a.H + head0 + hh] = m[g] - kShift + log2f(l[g]);
-        } else {
-          float* po = a.part_o + (static_cast<long long>(slot) * a.HB + hh) * kHd + 16 * j;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            *reinterpret_cast<float4*>(po + 8 * e) =
-                make_float4(o[0][2 * g + e], o[1][2 * g + e], o[2][2 * g + e], o[3][2 * g + e]);
-            *reinterpret_cast<float4*>(po + 8 * e + 4) =
-                make_float4(o[4][2 * g + e], o[5][2 * g + e], o[6][2 * g + e], o[7][2 * g + e]);
-          }
-          if (j == 0) a.part_ml[static_cast<long long>(slot) * a.HB + hh] = make_float2(m[g] - kShift, l[g]);
-        }
-      }
+    } else {
+      const long long slot = 2ll * w + (t == static_cast<int>(t_first) ? 0 : 1);
+      put_piece<T16, WIDE>(acc, x.heads, a.part_o + slot * a.HB * kHd, a.part_ml + slot * a.HB);
     }
     t += cnt;
   }
 }
 
-// Joins the pieces of items that several warps shared, in the order of their
-// positions, and writes zeros (log-sum-exp -inf) for a sequence with nothing
-// visible.  One CTA per item; 16 threads hold one head's 64 dimensions, and
-// the threads left over take every n-th piece of it.
+// The pieces of an item: warps w0 .. w1 of paged_attn hold one each (w0 > w1:
+// no positions).  False if there is nothing to join.
+template <typename T16>
+__device__ __forceinline__ bool pieces_of(const PagedArgs<T16>& a, int b, int item, const Span& sp, int& w0, int& w1,
+                                          bool& second) {
+  const int run = a.plan[a.n_seq + 1];
+  const int s = a.plan[b] + item * sp.nt;
+  w0 = s / run;
+  w1 = sp.nt > 0 ? (s + sp.nt - 1) / run : w0 - 1;
+  second = s != w0 * run;  // the item began within the first warp's run: its second slot
+  return w0 != w1;         // else that warp wrote the output
+}
+
+// Four dimensions of one head over the pieces w, w + ways, ..., kAhead of them
+// on their way at a time.
+constexpr int kAhead = 4;
+template <typename T16>
+__device__ __forceinline__ void gather(const PagedArgs<T16>& a, int w, int ways, int w0, int w1, bool second, int hh,
+                                       int d4, float4& acc, float& M, float& L) {
+  for (; w <= w1; w += kAhead * ways) {
+    float4 x[kAhead];
+    float2 ml[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int wu = w + u * ways;
+      ml[u] = make_float2(-INFINITY, 0.f);
+      if (wu <= w1) {
+        const long long at = (2ll * wu + (wu == w0 && second ? 1 : 0)) * a.HB + hh;
+        ml[u] = a.part_ml[at];
+        x[u] = *reinterpret_cast<const float4*>(a.part_o + at * kHd + 4 * d4);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) merge(acc, M, L, x[u], ml[u]);
+  }
+}
+
+template <typename T16>
+__device__ __forceinline__ void put_joined(const PagedArgs<T16>& a, int b, int head, int d4, const float4& acc, float M,
+                                           float L) {
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint2 v;
+  v.x = Type16<T16>::pack2(acc.x * inv, acc.y * inv);
+  v.y = Type16<T16>::pack2(acc.z * inv, acc.w * inv);
+  *reinterpret_cast<uint2*>(a.out + b * a.ldo + static_cast<long long>(head) * kHd + 4 * d4) = v;
+  if (a.lse && d4 == 0) a.lse[static_cast<long long>(b) * a.H + head] = M + log2f(L);
+}
+
+// Joins the pieces of items that several warps shared, in a fixed order, and
+// writes zeros (log-sum-exp -inf) for a sequence with nothing visible.
+//
+// With many items each has few pieces: one warp per item, 16 lanes for a
+// head's 64 dimensions, two heads at a time or one head's pieces in two halves.
 constexpr int kJoinThreads = 128;
 template <typename T16>
-__global__ void __launch_bounds__(kJoinThreads) paged_join(const PagedArgs<T16> a) {
-  __shared__ float4 s_o[kJoinThreads];
-  __shared__ float2 s_ml[kJoinThreads];
+__global__ void __launch_bounds__(kJoinThreads) paged_join_many(const PagedArgs<T16> a) {
+  const int items = a.n_kv * a.n_hb, lane = threadIdx.x & 31;
+  const int k = blockIdx.x * (kJoinThreads / 32) + (threadIdx.x >> 5);
+  const int b = k / items, item = k - b * items;
+  // the lengths are older than the kernel before, which has waited for them
+  Span sp{0, 0, 0, -1};
+  if (b < a.n_seq) sp = span_of(a, b, false);
+  griddep_wait();
+  griddep_launch_dependents();
+  int w0, w1;
+  bool second;
+  if (sp.nt < 0 || !pieces_of(a, b, item, sp, w0, w1, second)) return;
+  const Item<T16> x = item_of(a, b, item, sp);
+  const int half = lane >> 4, d4 = lane & 15;
+  const bool one = x.heads == 1;
+  for (int h0 = 0; h0 < x.heads; h0 += 2) {
+    const int hh = one ? 0 : h0 + half;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (hh < x.heads) gather(a, one ? w0 + half : w0, one ? 2 : 1, w0, w1, second, hh, d4, acc, M, L);
+    if (one) {
+      const float4 o = make_float4(__shfl_xor_sync(0xffffffffu, acc.x, 16), __shfl_xor_sync(0xffffffffu, acc.y, 16),
+                                   __shfl_xor_sync(0xffffffffu, acc.z, 16), __shfl_xor_sync(0xffffffffu, acc.w, 16));
+      const float2 ml = make_float2(__shfl_xor_sync(0xffffffffu, M, 16), __shfl_xor_sync(0xffffffffu, L, 16));
+      merge(acc, M, L, o, ml);
+    }
+    if (one ? half == 0 : hh < x.heads) put_joined(a, b, x.head0 + hh, d4, acc, M, L);
+  }
+}
+
+// With few items each has many pieces: one CTA per item, `width` heads side by
+// side, and the `ways` groups of threads that are left take every ways-th
+// piece.
+constexpr int kJoinFewThreads = 512;
+template <typename T16>
+__global__ void __launch_bounds__(kJoinFewThreads) paged_join_few(const PagedArgs<T16> a, int width, int ways) {
+  __shared__ float4 s_o[kJoinFewThreads];
+  __shared__ float2 s_ml[kJoinFewThreads];
+  const int items = a.n_kv * a.n_hb;
+  const int b = blockIdx.x / items, item = blockIdx.x - b * items;
+  const Span sp = span_of(a, b, false);
+  griddep_wait();
+  griddep_launch_dependents();
+  int w0, w1;
+  bool second;
+  if (sp.nt < 0 || !pieces_of(a, b, item, sp, w0, w1, second)) return;
+  const Item<T16> x = item_of(a, b, item, sp);
+  const int tid = threadIdx.x, d4 = tid & 15, way = (tid >> 4) / width;
+  for (int h0 = 0; h0 < x.heads; h0 += width) {
+    const int hh = h0 + (tid >> 4) % width;
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (hh < x.heads) gather(a, w0 + way, ways, w0, w1, second, hh, d4, acc, M, L);
+    s_o[tid] = acc;
+    s_ml[tid] = make_float2(M, L);
+    __syncthreads();
+    if (way == 0 && hh < x.heads) {
+      for (int k = 1; k < ways; ++k) merge(acc, M, L, s_o[tid + 16 * width * k], s_ml[tid + 16 * width * k]);
+      put_joined(a, b, x.head0 + hh, d4, acc, M, L);
+    }
+    __syncthreads();
+  }
+}
+
+// The same work with one CTA per item and nothing to join afterwards: 16 warps
+// take every 16th tile and meet in shared memory.  For few items of bounded
+// length (one or a few conversations on a small model), where a second launch
+// would cost more than spreading an item over several SMs saves.
+constexpr int kSoloWarps = 16;
+constexpr int kSoloTiles = 128;  // 2048 positions
+template <typename T16, bool WIDE>
+__global__ void __launch_bounds__(kSoloWarps * 32, 1)
+    paged_attn_solo(const __grid_constant__ CUtensorMap map, const PagedArgs<T16> a) {
+  extern __shared__ uint8_t s_raw[];
+  __shared__ __align__(8) uint64_t s_bar[kSoloWarps * kStages];
+  __shared__ float2 s_ml[kSoloWarps * 16];
+  uint8_t* s_tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5;
+  Ring ring = ring_of<T16>(&map, s_tiles, s_bar, warp);
+  if (tid == 0) tma_prefetch_desc(&map);
   griddep_wait();
   griddep_launch_dependents();
   const int items = a.n_kv * a.n_hb;
   const int b = blockIdx.x / items, item = blockIdx.x - b * items;
-  const Span sp = span_of(a, b, false);
+  const Span sp = span_of(a, b, item == 0 && tid == 0);
   if (sp.nt < 0) return;
-  const int run = a.plan[a.n_seq + 1];
-  const int s = a.plan[b] + item * sp.nt, e = s + sp.nt;
-  const int w0 = s / run, w1 = sp.nt > 0 ? (e - 1) / run : w0 - 1;
-  if (w0 == w1) return;  // its warp wrote the output
-  const int kvh = item / a.n_hb, hb = item - kvh * a.n_hb;
-  const int head0 = kvh * a.group + hb * a.HB;
-  const int heads = min(a.HB, a.group - hb * a.HB);
-  const int tid = threadIdx.x, d4 = tid & 15;
-  int width = 1;  // heads side by side: a power of two, at most 8
-  while (width < heads && width < kJoinThreads / 16) width *= 2;
-  const int ways = kJoinThreads / 16 / width;
-  for (int h0 = 0; h0 < heads; h0 += width) {
-    const int hh = h0 + (tid >> 4) % width, way = (tid >> 4) / width;
+  const Item<T16> x = item_of(a, b, item, sp);
+  const int cnt = sp.nt > warp ? (sp.nt - warp + kSoloWarps - 1) / kSoloWarps : 0;
+  Acc acc;
+  // the ring's own bytes take the warp's result once its tiles are through: at
+  // most 16 heads of 256 bytes
+  float* mine = reinterpret_cast<float*>(ring.buf);
+  if (cnt > 0) {
+    if (attend<T16, WIDE>(a, x, warp, kSoloWarps, cnt, ring, acc)) {
+      __syncwarp();
+      put_piece<T16, WIDE>(acc, x.heads, mine, s_ml + warp * 16);
+    } else if ((tid & 31) < 16) {
+      s_ml[warp * 16 + (tid & 31)] = make_float2(-INFINITY, 0.f);
+    }
+  }
+  __syncthreads();
+  const int pieces = min(sp.nt, kSoloWarps);
+  for (int k = tid; k < x.heads * 16; k += kSoloWarps * 32) {
+    const int hh = k >> 4, d4 = k & 15;
     float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (hh < heads) {
-      for (int w = w0 + way; w <= w1; w += ways) {
-        const long long at = (2ll * w + (w == w0 && s != w * run ? 1 : 0)) * a.HB + hh;
-        const float2 ml = a.part_ml[at];
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * kHd + 4 * d4);
-        if (!(ml.y > 0.f)) {
-          if (ml.y == 0.f) continue;  // nothing in this piece but scores of -inf
-        }
-        const float mn = fmaxf(M, ml.x);
-        const float c0 = M == mn ? 1.f : ex2_approx(M - mn), c1 = ml.x == mn ? 1.f : ex2_approx(ml.x - mn);
-        M = mn;
-        L = L * c0 + ml.y * c1;
-        acc.x = acc.x * c0 + x.x * c1;
-        acc.y = acc.y * c0 + x.y * c1;
-        acc.z = acc.z * c0 + x.z * c1;
-        acc.w = acc.w * c0 + x.w * c1;
-      }
-    }
-    s_o[tid] = acc;
-    s_ml[tid] = make_float2(M, L);
-    __syncthreads();
-    if (way == 0 && hh < heads) {
-      for (int k = 1; k < ways; ++k) {
-        const float2 ml = s_ml[tid + 16 * width * k];
-        const float4 x = s_o[tid + 16 * width * k];
-        if (ml.y == 0.f) continue;
-        const float mn = fmaxf(M, ml.x);
-        const float c0 = M == mn ? 1.f : ex2_approx(M - mn), c1 = ml.x == mn ? 1.f : ex2_approx(ml.x - mn);
-        M = mn;
-        L = L * c0 + ml.y * c1;
-        acc.x = acc.x * c0 + x.x * c1;
-        acc.y = acc.y * c0 + x.y * c1;
-        acc.z = acc.z * c0 + x.z * c1;
-        acc.w = acc.w * c0 + x.w * c1;
-      }
-      const float inv = L == 0.f ? 0.f : 1.f / L;
-      uint2 v;
-      v.x = Type16<T16>::pack2(acc.x * inv, acc.y * inv);
-      v.y = Type16<T16>::pack2(acc.z * inv, acc.w * inv);
-      *reinterpret_cast<uint2*>(a.out + b * a.ldo + static_cast<long long>(head0 + hh) * kHd + 4 * d4) = v;
-      if (a.lse && d4 == 0) a.lse[static_cast<long long>(b) * a.H + head0 + hh] = M + log2f(L);
-    }
-    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int w = 0; w < pieces; ++w)
+      merge(o, M, L, *reinterpret_cast<const float4*>(s_tiles + w * kWarpBytes + (hh * kHd + 4 * d4) * 4),
+            s_ml[w * 16 + hh]);
+    put_joined(a, b, x.head0 + hh, d4, o, M, L);
   }
 }
 
@@ -515,7 +720,8 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   a.lse = lse;
   const long long layer_elems = 2ll * c->n_kv_head * c->page_size * kHd;
   a.pages = static_cast<T16*>(c->pages) + layer * layer_elems;
-  a.page_stride = layer_elems * c->n_layer;
+  a.page_rows = c->n_layer * 2 * c->n_kv_head * c->page_size;
+  a.row0 = layer * 2 * c->n_kv_head * c->page_size;
   a.table = c->table;
   a.lens = c->lens;
   a.err = device_error_word();
@@ -540,13 +746,47 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   a.part_ml = reinterpret_cast<float2*>(base);
   base += align256(2ull * max_warps() * a.HB * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(base);
-  const unsigned grid = static_cast<unsigned>(num_sms() * kCtasPerSm);
-  const size_t smem = (static_cast<size_t>(c->n_seq) + 1) * 4;
-  cudaError_t e = a.HB > 8 ? launch_pdl(paged_attn<T16, true>, grid, kWarps * 32, smem, s, 0, a)
-                           : launch_pdl(paged_attn<T16, false>, grid, kWarps * 32, smem, s, 0, a);
+  // the pool as one [rows, 64] matrix
+  const uint64_t rows = static_cast<uint64_t>(c->n_pages) * a.page_rows;
+  CUtensorMap map;
+  if (!encode_tma_2d(&map, Type16<T16>::kTma, c->pages, kHd, rows, kHd * 2, kHd, kTile)) return cudaErrorInvalidValue;
+  const bool wide = a.HB > 8;
+  const long long items = static_cast<long long>(c->n_seq) * a.n_kv * a.n_hb;
+  const bool solo = items <= num_sms() && static_cast<long long>(c->max_pages) * c->page_size <= kSoloTiles * kTile;
+  const int smem = solo ? kSoloWarps * kWarpBytes + 1024 : kWarps * kWarpBytes + 1024 + (c->n_seq + 1) * 4;
+  auto kern = solo ? (wide ? paged_attn_solo<T16, true> : paged_attn_solo<T16, false>)
+                   : (wide ? paged_attn<T16, true> : paged_attn<T16, false>);
+  static int configured[4][64] = {{0}};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int& done = configured[2 * solo + wide][dev];
+  if (!done) {
+    cudaError_t e = cudaFuncSetAttribute(
+        kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        solo ? kSoloWarps * kWarpBytes + 1024 : kWarps * kWarpBytes + 1024 + (kMaxPagedSeqs + 1) * 4);
+    if (e != cudaSuccess) return e;
+    // the joins use little shared memory but leave the SMs split as paged_attn
+    // has them: between two splits an SM has to run empty
+    e = cudaFuncSetAttribute(paged_join_many<T16>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    e = cudaFuncSetAttribute(paged_join_few<T16>, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    done = 1;
+  }
+  if (solo) return launch_pdl(kern, static_cast<unsigned>(items), kSoloWarps * 32, smem, s, 0, map, a);
+  cudaError_t e = launch_pdl(kern, num_sms() * kCtasPerSm, kWarps * 32, smem, s, 0, map, a);
   if (e != cudaSuccess) return e;
-  const unsigned joins = static_cast<unsigned>(c->n_seq) * a.n_kv * a.n_hb;
-  return launch_pdl(paged_join<T16>, joins, kJoinThreads, 0, s, 0, a);
+  if (items > num_sms()) {
+    const unsigned joins = static_cast<unsigned>((items + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
+    return launch_pdl(paged_join_many<T16>, joins, kJoinThreads, 0, s, 0, a);
+  }
+  int width = 1;
+  while (width < a.HB && width < 8) width *= 2;
+  return launch_pdl(paged_join_few<T16>, static_cast<unsigned>(items), kJoinFewThreads, 0, s, 0, a, width,
+                    kJoinFewThreads / 16 / width);
 }
 
 }  // namespace
@@ -559,8 +799,10 @@ size_t attention_paged_workspace(const gpt2_paged_cache* c, int n_head) {
 }
 
 bool attention_paged_fits(const gpt2_paged_cache* c, int n_head) {
-  // tiles of all items are counted in 32 bits, with room for one run more
+  // rows of the pool are TMA coordinates, and tiles of all items are counted,
+  // in 32 bits, the latter with room for one run more
   const int group = n_head / c->n_kv_head;
+  if (static_cast<double>(c->n_pages) * c->n_layer * 2 * c->n_kv_head * c->page_size >= 2147483648.0) return false;
   return static_cast<long long>(c->n_seq) * c->n_kv_head * head_blocks(group) *
              (static_cast<long long>(c->max_pages) * c->page_size / kTile) <
          (1ll << 30);

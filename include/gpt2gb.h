@@ -556,7 +556,8 @@ size_t gpt2_attention_paged_workspace_bytes(const gpt2_paged_cache *cache, int n
  *   v_new may point into one c_attn output); lse: NULL or fp32 [n_seq, n_head]:
  *   log2 sum_{p visible} 2^(score_scale log2(e) q . K), as
  *   gpt2_attention_causal_lse.  out must not overlap q, k_new or v_new.
- *   n_head a multiple of n_kv_head.
+ *   n_head a multiple of n_kv_head; n_pages * n_layer * 2 * n_kv_head *
+ *   page_size < 2^31.
  * Scores, softmax statistics and sums are fp32, and the probabilities enter
  * the product with V as the sum of two 16-bit numbers.  A sequence without a
  * visible position gets zeros and an lse of -inf; rows of slots with lens[b] < 0 are left as they

@@ -170,6 +170,49 @@ def test_windows(window, sinks, append):
     _go(Case([90, 200], window=window, sinks=sinks, append=append, page=32, drop_hidden=False, heads=12, kv_heads=4))
 
 
+WIDE = 4096  # positions of a table row: more than one CTA takes per item, so the work is split and joined
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("append", [True, False])
+@pytest.mark.parametrize("page", [16, 48, 256])
+@pytest.mark.parametrize("heads, kv_heads", [(2, 2), (12, 4), (20, 1)])
+def test_lengths_in_wide_tables(dtype, append, page, heads, kv_heads):
+    _go(Case(EDGES + [1000, 2, 2500], page=page, append=append, dtype=dtype, seed=page, max_pages=WIDE // page + 1,
+             heads=heads, kv_heads=kv_heads))
+
+
+@pytest.mark.parametrize("window, sinks", [(1, 1), (16, 4), (17, 17), (100, 1), (5, 1000), (700, 33)])
+@pytest.mark.parametrize("append", [True, False])
+def test_windows_in_wide_tables(window, sinks, append):
+    _go(Case(EDGES + [500, 3000], window=window, sinks=sinks, append=append, junk_entry=1 << 30, seed=window,
+             max_pages=WIDE // 16))
+
+
+def test_infinite_scores_and_missing_pages_in_wide_tables():
+    c = Case([40, 2000, 600], heads=2, kv_heads=2, seed=16, max_pages=WIDE // 16)
+    # two pages that are not there are left out, and so is a whole first half
+    c.table[2, :20] = c.n_pages
+    # sequence 1, head 0: every score -inf
+    c.qkv[1, :64] = 0.0
+    c.qkv[1, 0] = 1.0
+    at = torch.arange(2001, device="cuda")
+    rows = c.table[1].long()[at // 16], at % 16
+    c.pages[rows[0][:2000], 1, 0, 0, rows[1][:2000]] = 0.0
+    c.pages[rows[0][:2000], 1, 0, 0, rows[1][:2000], 0] = -math.inf
+    c.qkv[1, 128:192] = 0.0
+    c.qkv[1, 128] = -math.inf
+    c.run()
+    torch.cuda.synchronize()
+    assert G.gpt2_last_error()[0] == RANGE
+    assert (c.out[1, :64] == 0).all() and c.lse[1, 0] == -math.inf
+    ref = R.attention(c.q[2, 1].double().numpy(), c.k[2][320:, 1].double().numpy(), c.v[2][320:, 1].double().numpy(),
+                      0.125)
+    assert np.abs(c.out[2, 64:128].double().cpu().numpy() - ref[0]).max() < 0.01
+    assert abs(float(c.lse[2, 1]) - ref[1]) < 1e-3
+    c.check(rows=[0])
+
+
 @pytest.mark.parametrize("lens, heads, kv_heads", [([5000], 1, 1), ([5000], 12, 12), ([4097, 3, 2000], 4, 1),
                                                    ([20000], 2, 2), ([9000, 0, -1, 8999], 16, 1)])
 def test_long_lengths_are_split_and_joined(lens, heads, kv_heads):
