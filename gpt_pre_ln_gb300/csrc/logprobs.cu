@@ -17,252 +17,12 @@ namespace gpt2 {
 
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kGroups = kThreads / 4;  // threads whose maxima bound the n-th largest logit from below
-constexpr int kCand = 1024;            // candidates kept per row
-
 struct Cand {
   float v;
   int i;
 };
 // the order of the alternatives: larger value first, lower index on ties
 __device__ __forceinline__ bool ahead(const Cand& a, const Cand& b) { return a.v > b.v || (a.v == b.v && a.i < b.i); }
-
-template <typename T>
-struct Vec {
-  static constexpr int kN = 16 / sizeof(T);
-  float x[kN];
-};
-template <typename T>
-__device__ __forceinline__ Vec<T> load_vec(const T* row, int v, int V) {
-  Vec<T> r;
-  const uint4 u = *reinterpret_cast<const uint4*>(row + static_cast<long long>(v) * Vec<T>::kN);
-  if constexpr (sizeof(T) == 4) {
-    r.x[0] = __uint_as_float(u.x);
-    r.x[1] = __uint_as_float(u.y);
-    r.x[2] = __uint_as_float(u.z);
-    r.x[3] = __uint_as_float(u.w);
-  } else {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = Type16<T>::unpack2(w[i]);
-      r.x[2 * i] = f.x;
-      r.x[2 * i + 1] = f.y;
-    }
-  }
-  if ((v + 1) * Vec<T>::kN > V) {  // the row's padding
-#pragma unroll
-    for (int i = 0; i < Vec<T>::kN; ++i)
-      if (v * Vec<T>::kN + i >= V) r.x[i] = -INFINITY;
-  }
-  return r;
-}
-
-__device__ __forceinline__ float block_sum(float v, float* s) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (lane == 0) s[warp] = v;
-  __syncthreads();
-  float r = 0.f;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) r += s[w];
-  __syncthreads();
-  return r;
-}
-
-// The alternatives by top_n passes over the row in memory: for rows where more
-// logits reach the bound than are kept.  WARPS warps together (all of a CTA, or
-// one).
-template <typename T, int WARPS>
-__device__ __noinline__ void top_by_passes(const T* z, int V, int top_n, float m, float log_s, int32_t* ids, float* lps,
-                                           Cand* s_best) {
-  const int lane = threadIdx.x & 31, warp = WARPS > 1 ? threadIdx.x >> 5 : 0;
-  constexpr int kN = Vec<T>::kN;
-  const int vecs = (V + kN - 1) / kN;
-  Cand last{INFINITY, -1};
-  for (int k = 0; k < top_n; ++k) {
-    Cand best{-INFINITY, 0x7fffffff};
-#pragma unroll 4
-    for (int v = warp * 32 + lane; v < vecs; v += WARPS * 32) {
-      const Vec<T> x = load_vec(z, v, V);
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const Cand c{x.x[i] == x.x[i] ? x.x[i] : -INFINITY, v * kN + i};
-        if (c.i < V && ahead(last, c) && ahead(c, best)) best = c;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const Cand c{__shfl_xor_sync(0xffffffffu, best.v, o), __shfl_xor_sync(0xffffffffu, best.i, o)};
-      if (ahead(c, best)) best = c;
-    }
-    if constexpr (WARPS > 1) {
-      __syncthreads();
-      if (lane == 0) s_best[warp] = best;
-      __syncthreads();
-      for (int w = 0; w < WARPS; ++w)
-        if (ahead(s_best[w], best)) best = s_best[w];
-    }
-    last = best;
-    if (warp == 0 && lane == 0) {
-      ids[k] = best.i;
-      lps[k] = (to_f32<T>(z[best.i]) - m) - log_s;
-    }
-  }
-}
-
-// The alternatives from rank `at` on are the lowest ids among the logits equal
-// to `value` (-inf: also NaN, which ranks with it).  One warp.
-template <typename T>
-__device__ void top_equal(const T* z, int V, int top_n, int at, float value, float m, float log_s, int32_t* ids,
-                          float* lps) {
-  const int lane = threadIdx.x & 31;
-  for (int i0 = 0; i0 < V && at < top_n; i0 += 32) {
-    const float x = i0 + lane < V ? to_f32<T>(z[i0 + lane]) : 0.f;
-    const bool take = i0 + lane < V && (value == -INFINITY ? !(x > -INFINITY) : x == value);
-    const unsigned who = __ballot_sync(0xffffffffu, take);
-    const int k = at + __popc(who & ((1u << lane) - 1));
-    if (take && k < top_n) {
-      ids[k] = i0 + lane;
-      lps[k] = (x - m) - log_s;
-    }
-    at += __popc(who);
-  }
-}
-
-// One CTA per row.  Pass 1: the maximum, and the n-th largest of 128 disjoint
-// groups' maxima, a lower bound of the row's n-th largest logit.  Pass 2: the
-// sums against the maximum, and every logit at or above the bound as a
-// candidate; the candidates are ranked among themselves.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) token_logprobs(const T* __restrict__ logits, long long ld, int V,
-                                                           const int32_t* __restrict__ tokens,
-                                                           float* __restrict__ logprob, float* __restrict__ entropy,
-                                                           float* __restrict__ lse, int top_n,
-                                                           int32_t* __restrict__ top_ids,
-                                                           float* __restrict__ top_logprobs, unsigned* err) {
-  __shared__ float s_group[kGroups];
-  __shared__ float s_red[kThreads / 32];
-  __shared__ Cand s_cand[kCand];
-  __shared__ int s_count;
-  __shared__ float s_bound;
-  griddep_wait();
-  griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long row = blockIdx.x;
-  const T* z = logits + row * ld;
-  constexpr int kN = Vec<T>::kN;
-  const int vecs = (V + kN - 1) / kN;
-
-  float g = -INFINITY;
-  for (int v = tid; v < vecs; v += kThreads) {
-    const Vec<T> x = load_vec(z, v, V);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) g = fmaxf(g, x.x[i]);
-  }
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 1));
-  g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
-  if ((lane & 3) == 0) s_group[tid >> 2] = g;
-  if (tid == 0) s_count = 0;
-  __syncthreads();
-  float m = -INFINITY;
-  for (int i = 0; i < kGroups; i += 32) m = fmaxf(m, s_group[i + lane]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (top_n > 0 && tid < kGroups) {
-    const float mine = s_group[tid];
-    int rank = 0;
-    for (int i = 0; i < kGroups; ++i) {
-      const float o = s_group[i];
-      rank += (o > mine || (o == mine && i < tid)) ? 1 : 0;
-    }
-    if (rank == top_n - 1) s_bound = mine;
-  }
-  __syncthreads();
-  const float bound = top_n > 0 ? s_bound : INFINITY;
-
-  float sum = 0.f, dot = 0.f;
-  for (int v = tid; v < vecs; v += kThreads) {
-    const Vec<T> x = load_vec(z, v, V);
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      const float d = x.x[i] - m;
-      const float e = ex2_approx(d * 1.4426950408889634f);
-      sum += e;
-      dot = fmaf(e, fmaxf(d, -256.f), dot);  // e is 0 there; 0 times -inf would not be
-      if (top_n > 0 && x.x[i] >= bound && x.x[i] > -INFINITY) {
-        const int at = atomicAdd(&s_count, 1);
-        if (at < kCand) s_cand[at] = {x.x[i], v * kN + i};
-      }
-    }
-  }
-  sum = block_sum(sum, s_red);
-  dot = block_sum(dot, s_red);
-  const float log_s = logf(sum);
-  if (tid == 0) {
-    if (lse) lse[row] = m + log_s;
-    if (entropy) entropy[row] = log_s - dot / sum;
-    if (logprob) {
-      const int t = tokens[row];
-      if (t >= 0 && t < V) {
-        logprob[row] = (to_f32<T>(z[t]) - m) - log_s;
-      } else {
-        record_error(err, kErrRange, kSiteScoreToken);
-        logprob[row] = NAN;
-      }
-    }
-  }
-  if (top_n == 0) return;
-  const int found = s_count;  // (behind the barriers of block_sum)
-  int32_t* ids = top_ids + row * top_n;
-  float* lps = top_logprobs + row * top_n;
-  if (found <= kCand) {
-    for (int k = tid; k < found; k += kThreads) {
-      const Cand c = s_cand[k];
-      int rank = 0;
-      for (int i = 0; i < found; ++i) rank += ahead(s_cand[i], c) ? 1 : 0;
-      if (rank < top_n) {
-        ids[rank] = c.i;
-        lps[rank] = (c.v - m) - log_s;
-      }
-    }
-    // fewer than n: the bound was -inf, every other logit is -inf (or NaN,
-    // which ranks with it); the lowest indices among those follow
-    if (warp == 0 && found < top_n) top_equal(z, V, top_n, found, -INFINITY, m, log_s, ids, lps);
-    return;
-  }
-  // a great many logits at or above the bound: ties
-  top_by_passes<T, kThreads / 32>(z, V, top_n, m, log_s, ids, lps, s_cand);
-}
-
-// ------------------------------------------------------- rows kept on chip
-// The kernel for rows that fit the shared memory of a cluster: each row is
-// read from memory once.  A cluster of C CTAs (1, 2, 4 or 8) holds one row at
-// a time, each CTA a part of it and each of its 16 warps a slice of that,
-// fetched by the warp's own bulk copy.  Rows are taken one after another.  Per
-// row a warp (1) takes the maxima of its slice's lanes and hands on those of 4
-// groups of 8 lanes (fewer with several CTAs), (2) sums against its own
-// maximum and fetches its slice of the next row, (3) looks again (in L2) at the
-// few vectors of lanes whose maximum reaches the bound, for candidates, and
-// hands on its sums.  The bound, the top_n-th largest of 64 groups' maxima and
-// so no larger than the top_n-th largest logit, comes from one more warp (in
-// the cluster's first CTA); (3) waits until the warp has done (1) and (2) of
-// the next row, so that nobody waits for the bound while loads could run.  A
-// last warp joins the sums of a row in a fixed order and ranks its candidates,
-// beside the other warps' work.  What crosses between them is kept twice, row
-// by row in turn: row r is finished before the bound of row r + 2 is given
-// out, and nothing of row r + 2 but its maxima is written before that.
-//
-// Measured at 8192 x 50257 in bf16 with 20 alternatives: @@LP@@
-constexpr int kWarps = kThreads / 32;
-constexpr int kScoreThreads = kThreads + 64;   // and two warps that see to the rows' ends
-constexpr int kKeep = 512;                     // candidates per row
-constexpr int kPartBytes = 100 * 1024;         // two CTAs of this size share an SM
-constexpr int kPartBytesMax = 208 * 1024;      // one does
-constexpr int kMaxCluster = 8;
-constexpr int kFlood = 16;  // lanes of a warp at the bound that make it a row of ties
 
 // 16 bytes of logits as pairs of floats; as packed 16-bit pairs for maxima.
 template <typename T>
@@ -285,6 +45,13 @@ struct Row16 {
     const T2 m = __hmax2(__hmax2(as2(a.x), as2(a.y)), __hmax2(as2(a.z), as2(a.w)));
     const float2 f = Type16<T>::unpack2(bits(m));
     return fmaxf(f.x, f.y);
+  }
+  static __device__ __forceinline__ uint4 keep(uint4 a, int n) {  // the first n elements, 0 < n < 8
+    const uint4 l = lowest();
+    auto one = [&](uint32_t w, uint32_t low, int left) {
+      return left >= 2 ? w : left == 1 ? (w & 0xffffu) | (low & 0xffff0000u) : low;
+    };
+    return make_uint4(one(a.x, l.x, n), one(a.y, l.y, n - 2), one(a.z, l.z, n - 4), one(a.w, l.w, n - 6));
   }
   static __device__ __forceinline__ float2 two(uint32_t w) {
     if constexpr (kNarrow) return Type16<T>::unpack2(w);
@@ -323,6 +90,10 @@ struct Row16<float> {
     return fmaxf(fmaxf(__uint_as_float(a.x), __uint_as_float(a.y)),
                  fmaxf(__uint_as_float(a.z), __uint_as_float(a.w)));
   }
+  static __device__ __forceinline__ uint4 keep(uint4 a, int n) {  // the first n elements, 0 < n < 4
+    const uint4 l = lowest();
+    return make_uint4(a.x, n > 1 ? a.y : l.y, n > 2 ? a.z : l.z, l.w);
+  }
   static __device__ __forceinline__ void unpack(uint4 a, float (&x)[4]) {
     x[0] = __uint_as_float(a.x);
     x[1] = __uint_as_float(a.y);
@@ -340,35 +111,90 @@ struct Row16<float> {
   }
 };
 
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
-__device__ __forceinline__ void st_cluster(uint32_t addr, int v) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
-}
-__device__ __forceinline__ int add_cluster(uint32_t addr, int v) {
-  int old;
-  asm volatile("atom.relaxed.cluster.shared::cluster.add.s32 %0, [%1], %2;" : "=r"(old) : "r"(addr), "r"(v) : "memory");
-  return old;
-}
-// A bounded wait for a barrier that CTAs of the cluster share.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity) {
-  const unsigned long long t0 = globaltimer_ns();
-  while (true) {
-    for (int i = 0; i < 32; ++i) {
-      uint32_t ok;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}\n"
-          : "=r"(ok)
-          : "r"(bar), "r"(parity)
-          : "memory");
-      if (ok) return true;
+// The alternatives by top_n passes over the row in memory: for rows where more
+// logits reach the bound than are kept.  One warp.
+template <typename T>
+__device__ __noinline__ void top_by_passes(const T* z, int V, int top_n, float m, float log_s, int32_t* ids,
+                                           float* lps) {
+  using R = Row16<T>;
+  constexpr int kN = R::kN;
+  const int lane = threadIdx.x & 31, vecs = (V + kN - 1) / kN;
+  Cand last{INFINITY, -1};
+  for (int k = 0; k < top_n; ++k) {
+    Cand best{-INFINITY, 0x7fffffff};
+#pragma unroll 4
+    for (int v = lane; v < vecs; v += 32) {
+      float x[kN];
+      R::unpack(*reinterpret_cast<const uint4*>(z + static_cast<long long>(v) * kN), x);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const Cand c{x[i] == x[i] ? x[i] : -INFINITY, v * kN + i};
+        if (c.i < V && ahead(last, c) && ahead(c, best)) best = c;
+      }
     }
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      const Cand c{__shfl_xor_sync(0xffffffffu, best.v, o), __shfl_xor_sync(0xffffffffu, best.i, o)};
+      if (ahead(c, best)) best = c;
+    }
+    last = best;
+    if (lane == 0) {
+      ids[k] = best.i;
+      lps[k] = (to_f32<T>(z[best.i]) - m) - log_s;
+    }
   }
 }
+
+// The alternatives from rank `at` on are the lowest ids among the logits equal
+// to `value` (-inf: also NaN, which ranks with it).  One warp.
+template <typename T>
+__device__ void top_equal(const T* z, int V, int top_n, int at, float value, float m, float log_s, int32_t* ids,
+                          float* lps) {
+  const int lane = threadIdx.x & 31;
+  for (int i0 = 0; i0 < V && at < top_n; i0 += 32) {
+    const float x = i0 + lane < V ? to_f32<T>(z[i0 + lane]) : 0.f;
+    const bool take = i0 + lane < V && (value == -INFINITY ? !(x > -INFINITY) : x == value);
+    const unsigned who = __ballot_sync(0xffffffffu, take);
+    const int k = at + __popc(who & ((1u << lane) - 1));
+    if (take && k < top_n) {
+      ids[k] = i0 + lane;
+      lps[k] = (x - m) - log_s;
+    }
+    at += __popc(who);
+  }
+}
+
+// A CTA takes one row after another; each of its 16 warps takes a slice of the
+// row through a part of shared memory of its own, whole or, if it is long, in
+// chunks.  Of a chunk the warp takes the lanes' maxima, then the sums against
+// the largest logit it has seen (two passes over shared memory), and has its
+// place filled again by a bulk copy, with the next row's at the end.  So every
+// logit is read from memory once, and no warp waits for another to load.
+//
+// The alternatives: of each row a warp hands on the maxima of 4 groups of 8
+// lanes.  One more warp takes the top_n-th largest of the 64 groups' maxima,
+// which is no larger than the top_n-th largest logit, and gives it out as a
+// bound.  The warps look again (in L2) at the few vectors of lanes whose own
+// maximum reaches it, for candidates, and hand on their sums; they do so when
+// they are through with the next row, so that nobody waits for the bound while
+// loads could run.  A last warp joins the sums of a row in a fixed order and
+// ranks its candidates.  What crosses between the warps is kept twice, row by
+// row in turn: row r is finished before the bound of row r + 2 is given out,
+// and nothing of row r + 2 but its maxima is written before that.
+//
+// Measured at 8192 x 50257 in bf16 with 20 alternatives: 167 us, 4.9 TB/s (three
+// passes over memory and L2 took 283).  About 17 500 warp instructions a row
+// keep the issue slots 70% busy, and a slice's place lies empty from the end of
+// one copy to the end of the sums; two and three smaller places for each warp fill that gap
+// but take more instructions, chunk by chunk (203 and 229 us).
+constexpr int kWarps = 16;
+constexpr int kThreads = kWarps * 32;
+constexpr int kScoreThreads = kThreads + 64;  // and two warps that see to the rows' ends
+constexpr int kKeep = 512;                    // candidates per row
+constexpr int kFlood = 16;                    // lanes of a warp at the bound that make it a row of ties
+constexpr int kRingMany = 100 * 1024;         // two CTAs an SM
+constexpr int kRingFew = 200 * 1024;          // one, when there are no more rows than SMs
+
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
                "l"(src), "r"(bytes), "r"(bar)
@@ -387,32 +213,42 @@ struct ScoreArgs {
   unsigned* err;
   long long ld;
   int M, V, top_n;
-  int part, slice;  // vectors per CTA and per warp
+  int slice, chunk;  // vectors of a warp, and of one of its slots
 };
 
-// A warp's sums over its slice against its own maximum m (or 0 when there is
-// none): sum = sum e^(x - m), dot = sum e^(x - m) (x - m).
+// Sums against a maximum m (0 in its place when it is -inf): sum = sum
+// e^(x - m), dot = sum e^(x - m) (x - m).
 struct Sums {
   float m, sum, dot;
 };
 
+// The same sums against a larger maximum.
+__device__ __forceinline__ void raise(Sums& r, float m) {
+  if (r.m == m) return;
+  const float down = fmaxf(r.m - m, -1e4f), f = ex2_approx(down * 1.4426950408889634f);  // (0 at -1e4)
+  r.dot = fmaf(down, r.sum, r.dot) * f;
+  r.sum *= f;
+  r.m = m;
+}
+
+// Adds this lane's vectors of a chunk to its sums, which are against a maximum
+// not below any of them.
 template <typename T>
-__device__ __forceinline__ Sums slice_sums(const uint4* slice, int cnt, float m) {
+__device__ __forceinline__ void add_chunk(const uint4* chunk, int cnt, Sums& r) {
   using R = Row16<T>;
   constexpr int kN = R::kN;
   const int lane = threadIdx.x & 31;
   constexpr float kL2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-  Sums r{m, 0.f, 0.f};
-  if (fabsf(m) < 1e4f) {
+  if (fabsf(r.m) < 1e4f) {
     // t = x log2(e) - c in one rounding, c = m log2(e) rounded; what c lost is
     // put right in the sums
-    const float c = m * kL2e, lost = fmaf(m, -kL2e, c);  // t is too small by `lost`
+    const float c = r.m * kL2e, lost = fmaf(r.m, -kL2e, c);  // t is too small by `lost`
     const float2 neg = make_float2(-c, -c), l2e = make_float2(kL2e, kL2e);
     float2 sum = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
 #pragma unroll 2
     for (int v = lane; v < cnt; v += 32) {
       float2 x[kN / 2];
-      R::pairs(slice[v], x);
+      R::pairs(chunk[v], x);
 #pragma unroll
       for (int i = 0; i < kN / 2; ++i) {
         const float2 t = fma_f32x2(x[i], l2e, neg);
@@ -421,31 +257,28 @@ __device__ __forceinline__ Sums slice_sums(const uint4* slice, int cnt, float m)
         dot = fma_f32x2(e, t, dot);
       }
     }
-    const float f = fmaf(lost, kLn2, 1.f);  // 2^lost
-    r.sum = (sum.x + sum.y) * f;
-    r.dot = fmaf(lost, r.sum, (dot.x + dot.y) * f) * kLn2;
+    const float f = fmaf(lost, kLn2, 1.f), s = (sum.x + sum.y) * f;  // f = 2^lost
+    r.sum += s;
+    r.dot = fmaf(fmaf(lost, s, (dot.x + dot.y) * f), kLn2, r.dot);
   } else {  // a maximum far out (or none): `lost` is no small number, differences may overflow
-    const float ref = m == -INFINITY ? 0.f : m;
-    const T* x = reinterpret_cast<const T*>(slice);
-    for (int v = lane; v < cnt * kN; v += 32) {
-      const float d = to_f32<T>(x[v]) - ref;
-      const float e = ex2_approx(d * kL2e);
-      r.sum += e;
-      r.dot = fmaf(e, fmaxf(d, -256.f), r.dot);
+    const float ref = r.m == -INFINITY ? 0.f : r.m;
+    for (int v = lane; v < cnt; v += 32) {
+      float x[kN];
+      R::unpack(chunk[v], x);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const float d = x[i] - ref, e = ex2_approx(d * kL2e);
+        r.sum += e;
+        r.dot = fmaf(e, fmaxf(d, -256.f), r.dot);  // e is 0 there; 0 times -inf would not be
+      }
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
-    r.dot += __shfl_xor_sync(0xffffffffu, r.dot, o);
-  }
-  return r;
 }
 
 // Logits above `bound` anywhere in the row, as candidates; returns their
 // number.  One warp.
 template <typename T>
-__device__ __noinline__ int collect_above(const T* z, int V, float bound, Cand* s_cand, int* s_count) {
+__device__ __noinline__ int collect_above(const T* z, int V, float bound, Cand* s_cand, int* s_count, int keep) {
   using R = Row16<T>;
   constexpr int kN = R::kN;
   const int lane = threadIdx.x & 31, vecs = (V + kN - 1) / kN;
@@ -459,20 +292,217 @@ __device__ __noinline__ int collect_above(const T* z, int V, float bound, Cand* 
     for (int i = 0; i < kN; ++i)
       if (x[i] > bound && v * kN + i < V) {
         const int at = atomicAdd(s_count, 1);
-        if (at < kKeep) s_cand[at] = {x[i], v * kN + i};
+        if (at < keep) s_cand[at] = {x[i], v * kN + i};
       }
   }
   __syncwarp();
   return *s_count;
 }
 
-template <typename T, bool CLUSTER>
+// The outputs of a row from its sums r (against its maximum), and from its
+// candidates (s_count of them; at most `keep` are there), which are all logits
+// not below `bound`.  One warp.
+template <typename T>
+__device__ __forceinline__ void put_row(const ScoreArgs<T>& a, int row, const Sums& r, float z_tok, float bound,
+                                        Cand* s_cand, int* s_count, int keep) {
+  const int lane = threadIdx.x & 31;
+  const float m = r.m, log_s = m > -INFINITY ? logf(r.sum) : NAN;
+  if (lane == 0) {
+    if (a.lse) a.lse[row] = m + log_s;
+    if (a.entropy) a.entropy[row] = log_s - r.dot / r.sum;
+    if (a.logprob) a.logprob[row] = (z_tok - m) - log_s;
+  }
+  if (a.top_n == 0) return;
+  const T* z = a.logits + row * a.ld;
+  int32_t* ids = a.top_ids + static_cast<long long>(row) * a.top_n;
+  float* lps = a.top_logprobs + static_cast<long long>(row) * a.top_n;
+  int found = *s_count;
+  float rest = -INFINITY;  // what the list is filled up with
+  if (found > keep) {      // ties at the bound: those above it, then the lowest ids among the ties
+    __syncwarp();
+    found = collect_above(z, a.V, bound, s_cand, s_count, keep);
+    rest = bound;
+  }
+  if (found > keep) {
+    top_by_passes(z, a.V, a.top_n, m, log_s, ids, lps);
+  } else {
+    for (int k = lane; k < found; k += 32) {
+      const Cand c = s_cand[k];
+      int at = 0;
+#pragma unroll 4
+      for (int i = 0; i < found; ++i) at += ahead(s_cand[i], c) ? 1 : 0;
+      if (at < a.top_n) {
+        ids[at] = c.i;
+        lps[at] = (c.v - m) - log_s;
+      }
+    }
+    if (found < a.top_n) top_equal(z, a.V, a.top_n, found, rest, m, log_s, ids, lps);
+  }
+  __syncwarp();
+}
+
+// Short rows: one warp per row, a chunk of four vectors a lane in registers and
+// the next on its way.  Each lane keeps its own maximum and sums; the bound
+// comes from 64 groups' maxima (two a lane) by bisection, and what reaches it
+// is looked at again.  A row's end costs the CTA of the kernel below about 3.7
+// us: 8192 rows in bf16 take it 110 us at 8000 logits a row (here 68), 122 at
+// 14000 (here 93), 143 at 30000 (here 186).  A few rows of 8000 are better off
+// with a CTA each (64 rows: 7.9 us, here 19.7).
+constexpr int kShortBytes = 40 * 1024;  // of a row, when there are more rows than the other kernel holds
+constexpr int kShortAlways = 8 * 1024;  // under which that kernel's groups have no vector each
+constexpr int kShortWarps = 8;
+constexpr int kShortKeep = 128;
+template <typename T>
+__device__ __forceinline__ void add_vectors(const uint4 (&x)[4], Sums& r) {
+  using R = Row16<T>;
+  constexpr int kN = R::kN;
+  constexpr float kL2e = 1.4426950408889634f;
+  const float mc = R::reduce(R::vmax(R::vmax(x[0], x[1]), R::vmax(x[2], x[3])));
+  const float m = fmaxf(r.m, mc);
+  if (r.m == -INFINITY)
+    r.m = m;  // nothing but -inf (or NaN) so far: the sums stay
+  else
+    raise(r, m);
+  const float ref = m == -INFINITY ? 0.f : m;
+  if (__any_sync(0xffffffffu, m > 1e37f || (m < -6e4f && m > -INFINITY))) {
+    // differences may overflow, or -inf, raised, not be far enough below
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float e[kN];
+      R::unpack(x[k], e);
+#pragma unroll
+      for (int i = 0; i < kN; ++i) {
+        const float d = e[i] - ref, p = ex2_approx(d * kL2e);
+        r.sum += p;
+        r.dot = fmaf(p, fmaxf(d, -256.f), r.dot);
+      }
+    }
+    return;
+  }
+  const float2 neg = make_float2(-ref, -ref), l2e = make_float2(kL2e, kL2e);
+  float2 sum = make_float2(r.sum, 0.f), dot = make_float2(r.dot, 0.f);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    float2 v[kN / 2];
+    R::pairs(x[k], v);
+#pragma unroll
+    for (int i = 0; i < kN / 2; ++i) {
+      const float2 d = add_f32x2(v[i], neg), t = mul_f32x2(d, l2e);
+      const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+      sum = add_f32x2(sum, e);
+      dot = fma_f32x2(e, d, dot);
+    }
+  }
+  r.sum = sum.x + sum.y;
+  r.dot = dot.x + dot.y;
+}
+
+// Unsigned keys in the order of the floats.
+__device__ __forceinline__ unsigned key_of(float x) {
+  const unsigned u = __float_as_uint(x);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kShortWarps * 32, 4) score_short(const ScoreArgs<T> a) {
+  __shared__ Cand s_cand[kShortWarps][kShortKeep];
+  __shared__ int s_count[kShortWarps];
+  using R = Row16<T>;
+  constexpr int kN = R::kN;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int vecs = (a.V + kN - 1) / kN, pad = a.V % kN;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int step = gridDim.x * kShortWarps;
+  for (int row = blockIdx.x * kShortWarps + warp; row < a.M; row += step) {
+    const T* z = a.logits + row * a.ld;
+    const uint4* zv = reinterpret_cast<const uint4*>(z);
+    const int tok = a.logprob ? a.tokens[row] : 0;
+    auto load = [&](int c, uint4 (&x)[4]) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int v = c + 32 * k + lane;
+        x[k] = v < vecs ? zv[v] : R::lowest();
+        if (pad && v == vecs - 1) x[k] = R::keep(x[k], pad);  // what stands behind the vocabulary
+      }
+    };
+    Sums r{-INFINITY, 0.f, 0.f};
+    uint4 g0 = R::lowest(), g1 = R::lowest();
+    uint4 x[4], y[4];
+    load(0, x);
+    for (int c = 0; c < vecs; c += 128) {
+      if (c + 128 < vecs) load(c + 128, y);
+      g0 = R::vmax(g0, R::vmax(x[0], x[2]));
+      g1 = R::vmax(g1, R::vmax(x[1], x[3]));
+      add_vectors<T>(x, r);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = y[k];
+    }
+    const bool tok_ok = tok >= 0 && tok < a.V;
+    if (!tok_ok && lane == 0) record_error(a.err, kErrRange, kSiteScoreToken);
+    const float z_tok = tok_ok ? to_f32<T>(z[tok]) : NAN;
+    float m = r.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (r.m > -INFINITY) raise(r, m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
+      r.dot += __shfl_xor_sync(0xffffffffu, r.dot, o);
+    }
+    r.m = m;
+    float bound = -INFINITY;
+    if (a.top_n > 0) {
+      // a value that at least top_n groups reach, and few more than that
+      const float f0 = R::reduce(g0), f1 = R::reduce(g1);
+      const unsigned k0 = key_of(f0), k1 = key_of(f1);
+      unsigned low = key_of(-INFINITY), high = key_of(m) + 1;  // low: reached by top_n groups, high: by none
+      for (int i = 0; i < 32 && high - low > 1; ++i) {
+        const unsigned mid = low + (high - low) / 2;
+        const int n = __popc(__ballot_sync(0xffffffffu, k0 >= mid)) + __popc(__ballot_sync(0xffffffffu, k1 >= mid));
+        if (n >= a.top_n) {
+          low = mid;
+          if (n <= a.top_n + 2) break;
+        } else {
+          high = mid;
+        }
+      }
+      bound = low & 0x80000000u ? __uint_as_float(low & 0x7fffffffu) : __uint_as_float(~low);
+      const float least = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
+      if (lane == 0) s_count[warp] = 0;
+      __syncwarp();
+      unsigned who = __ballot_sync(0xffffffffu, f0 >= least), who1 = __ballot_sync(0xffffffffu, f1 >= least);
+      for (int h = 0; h < 2; ++h, who = who1) {
+        while (who) {
+          const int f = __ffs(who) - 1;
+          who &= who - 1;
+          for (int v = 32 * h + f + 64 * lane; v < vecs; v += 64 * 32) {  // that group's vectors
+            const uint4 u = zv[v];
+            if (R::reduce(u) < bound && v + 1 < vecs) continue;
+            float e[kN];
+            R::unpack(u, e);
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (e[i] >= least && v * kN + i < a.V) {
+                const int at = atomicAdd(&s_count[warp], 1);
+                if (at < kShortKeep) s_cand[warp][at] = {e[i], v * kN + i};
+              }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    __syncwarp();
+    put_row(a, row, r, z_tok, bound, s_cand[warp], &s_count[warp], kShortKeep);
+  }
+}
+
+template <typename T>
 __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T> a) {
-  extern __shared__ __align__(128) uint8_t s_row[];  // [kWarps][slice] vectors
-  __shared__ Sums s_sums[2][kMaxCluster * kWarps];
+  extern __shared__ __align__(128) uint8_t s_row[];  // [kWarps][chunk] vectors
+  __shared__ Sums s_sums[2][kWarps];
   __shared__ Cand s_cand[2][kKeep];
-  __shared__ float s_raw[2][kMaxCluster * kWarps];  // groups' maxima
-  __shared__ __align__(16) float s_group[64];
+  __shared__ __align__(16) float s_group[2][64];  // groups' maxima
   __shared__ int s_count[2];
   __shared__ float s_bound[2];
   // of even and of odd rows (a warp may be a row ahead of another, never two):
@@ -481,199 +511,175 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
   using R = Row16<T>;
   constexpr int kN = R::kN;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
-  const int C = CLUSTER ? static_cast<int>(cluster_nctarank()) : 1;
-  const int first = static_cast<int>(blockIdx.x) / C, step = static_cast<int>(gridDim.x) / C;
+  const int first = static_cast<int>(blockIdx.x), step = static_cast<int>(gridDim.x);
   const int vecs = (a.V + kN - 1) / kN;
-  const int per_warp = C >= 4 ? 1 : 4 / C;  // groups of a warp: 64 in all (128 with eight CTAs)
   if (tid == 0) {
     for (int w = 0; w < kWarps; ++w) mbar_init(smem_u32(&s_load[w]), 1);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&s_max[i]), C * kWarps);
+      mbar_init(smem_u32(&s_max[i]), kWarps);
       mbar_init(smem_u32(&s_bnd[i]), 1);
-      mbar_init(smem_u32(&s_set[i]), C * kWarps);
+      mbar_init(smem_u32(&s_set[i]), kWarps);
       mbar_init(smem_u32(&s_fin[i]), 1);
     }
     fence_barrier_init();
     s_count[0] = s_count[1] = 0;
   }
-  if (CLUSTER)
-    cluster_sync();
-  else
-    __syncthreads();
+  __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
 
   if (warp < kWarps) {
     // this warp's vectors of a row
-    const int v0 = rank * a.part + warp * a.slice;
-    const int cnt = max(0, min(min(a.slice, a.part - warp * a.slice), vecs - v0));
+    const int v0 = warp * a.slice;
+    const int cnt = max(0, min(a.slice, vecs - v0));
     const int pad = (a.V % kN) && cnt > 0 && v0 + cnt == vecs ? a.V % kN : 0;  // elements of the last vector
-    uint4* slice = reinterpret_cast<uint4*>(s_row) + warp * a.slice;
+    const int chunks = (cnt + a.chunk - 1) / a.chunk;
+    uint4* chunk = reinterpret_cast<uint4*>(s_row) + warp * a.chunk;
     const uint32_t bar = smem_u32(&s_load[warp]);
-    auto fetch = [&](int row) {
-      mbar_arrive_expect_tx(bar, cnt * 16);
-      bulk_load(smem_u32(slice), a.logits + row * a.ld + static_cast<long long>(v0) * kN, cnt * 16, bar);
+    int f_row = first, f_chunk = 0;  // the chunk to fetch next
+    auto fetch = [&] {               // lane 0
+      if (f_row >= a.M) return;
+      const int n = min(a.chunk, cnt - f_chunk * a.chunk);
+      mbar_arrive_expect_tx(bar, n * 16);
+      bulk_load(smem_u32(chunk), a.logits + f_row * a.ld + (static_cast<long long>(v0) + f_chunk * a.chunk) * kN,
+                n * 16, bar);
+      if (++f_chunk == chunks) {
+        f_chunk = 0;
+        f_row += step;
+      }
     };
-    if (lane == 0 && cnt > 0 && first < a.M) fetch(first);
-    int it = 0;
+    if (lane == 0 && cnt > 0) fetch();
+    int it = 0, parity = 0;
     bool ok = true;
-    float mine = -INFINITY;
+    float mine = -INFINITY;  // this lane's maximum
     Sums r{-INFINITY, 0.f, 0.f};
     auto arrive = [&](uint64_t* bars, int k) {
       __syncwarp();
-      if (lane == 0) {
-        const uint32_t b = smem_u32(&bars[k & 1]);
-        if (CLUSTER)
-          mbar_arrive_cluster(mapa_shared(b, 0));
-        else
-          mbar_arrive(b);
-      }
+      if (lane == 0) mbar_arrive(smem_u32(&bars[k & 1]));
     };
-    // (3) of the row before: candidates among what reaches its bound, and its
-    // sums.  `k`: the number of that row here.
+    auto warp_max = [](float m) {
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      return m;
+    };
+    // The maxima of the warp's four groups of lanes for the bound; returns the warp's.
+    auto hand_on = [&](int k, float m) {
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (lane % 8 == 0) s_group[k & 1][warp * 4 + lane / 8] = m;
+      arrive(s_max, k);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    };
+    // Of the row before: candidates among what reaches its bound, and its sums.
+    // `k`: the number of that row here.
     auto settle = [&](int row, int k, float mine, const Sums& r) {
       const int buf = k & 1;
-      const uint32_t bnd = smem_u32(&s_bnd[buf]);
-      ok = CLUSTER ? mbar_wait_cluster(bnd, (k >> 1) & 1) : mbar_wait(bnd, (k >> 1) & 1);
+      ok = mbar_wait(smem_u32(&s_bnd[buf]), (k >> 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
         if (lane == 0) record_error(a.err, kErrTimeout, kSiteScoreJoin);
         return;
       }
       const float bound = s_bound[buf];
+      const float least = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
       unsigned who = __ballot_sync(0xffffffffu, mine >= bound && mine > -INFINITY);
-      if (who) {
-        // the slice has gone: these few vectors come from L2
-        const uint4* z = reinterpret_cast<const uint4*>(a.logits + row * a.ld) + v0;
-        const uint32_t count = CLUSTER ? mapa_shared(smem_u32(&s_count[buf]), 0) : 0;
-        if (__popc(who) > kFlood) {
-          if (lane == 0) {
-            if (CLUSTER)
-              add_cluster(count, kKeep + 1);
-            else
-              atomicAdd(&s_count[buf], kKeep + 1);
-          }
-          who = 0;
-        }
-        while (who) {
-          const int f = __ffs(who) - 1;
-          who &= who - 1;
-          for (int v = f + 32 * lane; v < cnt; v += 32 * 32) {
-            const uint4 u = z[v];
-            if (v + 1 < cnt && R::reduce(u) < bound) continue;
-            float x[kN];
-            R::unpack(u, x);
+      if (__popc(who) > kFlood) {
+        if (lane == 0) atomicAdd(&s_count[buf], kKeep + 1);
+        who = 0;
+      }
+      // the chunks have gone: these few vectors come from L2
+      const uint4* z = reinterpret_cast<const uint4*>(a.logits + row * a.ld) + v0;
+      while (who) {
+        const int f = __ffs(who) - 1;
+        who &= who - 1;
+        for (int c = 0; c < cnt; c += a.chunk)  // that lane's vectors
+          for (int v = c + f + 32 * lane; v < min(cnt, c + a.chunk); v += 32 * 32) {
+          const uint4 u = z[v];
+          if (R::reduce(u) < bound && v + 1 < cnt) continue;
+          float x[kN];
+          R::unpack(u, x);
+          unsigned hit = 0;
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (x[i] >= bound && x[i] > -INFINITY && (v0 + v) * kN + i < a.V) {
-                const int id = (v0 + v) * kN + i;
-                if (CLUSTER) {
-                  const int at = add_cluster(count, 1);
-                  if (at < kKeep) {
-                    const uint32_t to = mapa_shared(smem_u32(&s_cand[buf][at]), 0);
-                    st_cluster(to, x[i]);
-                    st_cluster(to + 4, id);
-                  }
-                } else {
-                  const int at = atomicAdd(&s_count[buf], 1);
-                  if (at < kKeep) s_cand[buf][at] = {x[i], id};
-                }
-              }
+          for (int i = 0; i < kN; ++i) hit |= x[i] >= least ? 1u << i : 0u;
+          if (pad && v + 1 == cnt) hit &= (1u << pad) - 1;
+          while (hit) {
+            const int i = __ffs(hit) - 1;
+            hit &= hit - 1;
+            const int at = atomicAdd(&s_count[buf], 1);
+            if (at < kKeep) s_cand[buf][at] = {to_f32<T>(reinterpret_cast<const T*>(z + v)[i]), (v0 + v) * kN + i};
           }
-          __syncwarp();
         }
+        __syncwarp();
       }
-      if (lane == 0) {
-        if (CLUSTER) {
-          const uint32_t to = mapa_shared(smem_u32(&s_sums[buf][rank * kWarps + warp]), 0);
-          st_cluster(to, r.m);
-          st_cluster(to + 4, r.sum);
-          st_cluster(to + 8, r.dot);
-        } else {
-          s_sums[buf][warp] = r;
-        }
-      }
+      if (lane == 0) s_sums[buf][warp] = r;
       arrive(s_set, k);
     };
     for (int row = first; row < a.M; row += step, ++it) {
-      // ---- (1) maxima
-      uint4 mx = R::lowest();
-      if (cnt > 0) {
-        if (!mbar_wait(bar, it & 1)) {
-          if (lane == 0) record_error(a.err, kErrTimeout, kSiteScoreLoad);
-          (void)mbar_wait(bar, it & 1);  // the copy must not outlive the CTA
-          ok = false;
-        }
+      const float mine_was = mine;
+      const Sums r_was = r;
+      mine = -INFINITY;
+      r = Sums{-INFINITY, 0.f, 0.f};
+      for (int c = 0; c < chunks; ++c) {
+        ok = mbar_wait(bar, parity);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        if (pad) {  // what stands behind the vocabulary
-          T* last = reinterpret_cast<T*>(slice + cnt - 1);
+        parity ^= 1;
+        const int n = min(a.chunk, cnt - c * a.chunk);
+        if (pad && c + 1 == chunks) {  // what stands behind the vocabulary
+          T* last = reinterpret_cast<T*>(chunk + n - 1);
           if (lane >= pad && lane < kN) last[lane] = from_f32<T>(-INFINITY);
           __syncwarp();
         }
+        uint4 mx = R::lowest();
 #pragma unroll 4
-        for (int v = lane; v < cnt; v += 32) mx = R::vmax(mx, slice[v]);
-      }
-      const float mine_was = mine;
-      const Sums r_was = r;
-      mine = R::reduce(mx);
-      float m = mine;
-#pragma unroll
-      for (int o = 1; o <= 32; o <<= 1) {
-        if (o * per_warp == 32 && lane % o == 0) {  // m: the maximum of the o lanes from this one on
-          float* to = &s_raw[it & 1][(rank * kWarps + warp) * per_warp + lane / o];
-          if (CLUSTER)
-            st_cluster(mapa_shared(smem_u32(to), 0), m);
-          else
-            *to = m;
+        for (int v = lane; v < n; v += 32) mx = R::vmax(mx, chunk[v]);
+        mine = fmaxf(mine, R::reduce(mx));
+        const float m = c + 1 == chunks ? hand_on(it, mine) : warp_max(mine);
+        raise(r, m);
+        add_chunk<T>(chunk, n, r);
+        __syncwarp();
+        if (lane == 0) {
+          fence_proxy_async_smem();
+          fetch();
         }
-        if (o < 32) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       }
-      arrive(s_max, it);
-      // ---- (2) sums, and the next row's slice (the shuffles of the sums are
-      // behind every lane's reads of this one)
-      r = slice_sums<T>(slice, cnt, m);
-      if (lane == 0 && cnt > 0 && row + step < a.M) {
-        fence_proxy_async_smem();
-        fetch(row + step);
-      }
-      if (it > 0) settle(row - step, it - 1, mine_was, r_was);
       if (!ok) {
-        if (lane == 0 && cnt > 0 && row + step < a.M) (void)mbar_wait(bar, (it + 1) & 1);  // the copy in flight
+        if (lane == 0) record_error(a.err, kErrTimeout, kSiteScoreLoad);
         break;
       }
+      if (chunks == 0) hand_on(it, mine);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        r.sum += __shfl_xor_sync(0xffffffffu, r.sum, o);
+        r.dot += __shfl_xor_sync(0xffffffffu, r.dot, o);
+      }
+      if (it > 0) settle(row - step, it - 1, mine_was, r_was);
+      if (!ok) break;
     }
     if (ok && it > 0) settle(first + (it - 1) * step, it - 1, mine, r);
-  } else if (rank == 0) {
+    // (given up: the copy in flight must not outlive the CTA)
+    if (!ok && lane == 0 && cnt > 0) (void)mbar_wait(bar, parity);
+  } else {
     bool ok = true;
     auto arrived = [&](uint64_t* bars, int k) {  // every warp has come to row k
-      const uint32_t b = smem_u32(&bars[k & 1]);
-      ok = CLUSTER ? mbar_wait_cluster(b, (k >> 1) & 1) : mbar_wait(b, (k >> 1) & 1);
+      ok = mbar_wait(smem_u32(&bars[k & 1]), (k >> 1) & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok && lane == 0) record_error(a.err, kErrTimeout, kSiteScoreJoin);
       return ok;
     };
     if (warp == kWarps) {
       // ---- bounds
-      const int raw = C * kWarps * per_warp;
       for (int row = first, it = 0; row < a.M; row += step, ++it) {
         const int buf = it & 1;
         if (!arrived(s_max, it)) break;
         float bound = NAN;  // nothing reaches it
         if (a.top_n > 0) {
-          float x0 = s_raw[buf][lane], x1 = s_raw[buf][lane + 32];
-          if (raw > 64) {
-            x0 = fmaxf(x0, s_raw[buf][lane + 64]);
-            x1 = fmaxf(x1, s_raw[buf][lane + 96]);
-          }
-          s_group[lane] = x0;
-          s_group[lane + 32] = x1;
-          __syncwarp();
+          const float x0 = s_group[buf][lane], x1 = s_group[buf][lane + 32];
           int r0 = 0, r1 = 0;
 #pragma unroll 4
           for (int i = 0; i < 64; i += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(&s_group[i]);
+            const float4 o = *reinterpret_cast<const float4*>(&s_group[buf][i]);
             const float q[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -694,15 +700,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
           }
         }
         if (lane == 0) {
-          if (CLUSTER) {
-            for (int c = 0; c < C; ++c) {
-              st_cluster(mapa_shared(smem_u32(&s_bound[buf]), c), bound);
-              mbar_arrive_cluster(mapa_shared(smem_u32(&s_bnd[buf]), c));
-            }
-          } else {
-            s_bound[buf] = bound;
-            mbar_arrive(smem_u32(&s_bnd[buf]));
-          }
+          s_bound[buf] = bound;
+          mbar_arrive(smem_u32(&s_bnd[buf]));
         }
         __syncwarp();
       }
@@ -719,78 +718,28 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
         if (a.logprob && it + 1 < n) tok_next = a.tokens[row + step];
         if (!arrived(s_set, it)) break;
         float m = -INFINITY;
-        for (int i = lane; i < C * kWarps; i += 32) m = fmaxf(m, s_sums[buf][i].m);
+        if (lane < kWarps) m = s_sums[buf][lane].m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
         float s = 0.f, d = 0.f;
-        for (int i = lane; i < C * kWarps; i += 32) {
-          const Sums x = s_sums[buf][i];
-          if (x.m == -INFINITY) {
-            s += x.sum;  // 0, or NaN
-            continue;
-          }
-          const float down = fmaxf(x.m - m, -1e4f);  // (its factor is 0 there)
-          const float c = ex2_approx(down * 1.4426950408889634f);
-          s = fmaf(c, x.sum, s);
-          d = fmaf(c, fmaf(down, x.sum, x.dot), d);
+        if (lane < kWarps) {
+          Sums x = s_sums[buf][lane];
+          if (x.m > -INFINITY) raise(x, m);
+          s = x.sum;  // (of a warp with nothing but -inf: 0, or NaN)
+          d = x.dot;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           s += __shfl_xor_sync(0xffffffffu, s, o);
           d += __shfl_xor_sync(0xffffffffu, d, o);
         }
-        const float log_s = m > -INFINITY ? logf(s) : NAN;
-        if (lane == 0) {
-          if (a.lse) a.lse[row] = m + log_s;
-          if (a.entropy) a.entropy[row] = log_s - d / s;
-          if (a.logprob) a.logprob[row] = (z_tok - m) - log_s;
-        }
-        if (a.top_n > 0) {
-          const T* z = a.logits + row * a.ld;
-          int32_t* ids = a.top_ids + static_cast<long long>(row) * a.top_n;
-          float* lps = a.top_logprobs + static_cast<long long>(row) * a.top_n;
-          int found = s_count[buf];
-          float rest = -INFINITY;  // what the list is filled up with
-          if (found > kKeep) {     // ties at the bound: those above it, then the lowest ids among the ties
-            found = collect_above(z, a.V, s_bound[buf], s_cand[buf], &s_count[buf]);
-            rest = s_bound[buf];
-          }
-          if (found > kKeep) {
-            top_by_passes<T, 1>(z, a.V, a.top_n, m, log_s, ids, lps, nullptr);
-          } else {
-            for (int k = lane; k < found; k += 32) {
-              const Cand c = s_cand[buf][k];
-              int at = 0;
-#pragma unroll 4
-              for (int i = 0; i < found; ++i) at += ahead(s_cand[buf][i], c) ? 1 : 0;
-              if (at < a.top_n) {
-                ids[at] = c.i;
-                lps[at] = (c.v - m) - log_s;
-              }
-            }
-            if (found < a.top_n) top_equal(z, a.V, a.top_n, found, rest, m, log_s, ids, lps);
-          }
-          __syncwarp();
-          if (lane == 0) s_count[buf] = 0;  // next added to behind the bound of two rows on
-        }
+        put_row(a, row, Sums{m, s, d}, z_tok, s_bound[buf], s_cand[buf], &s_count[buf], kKeep);
+        if (lane == 0) s_count[buf] = 0;  // next added to behind the bound of two rows on
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_fin[buf]));
       }
     }
   }
-  __syncwarp();
-  if (CLUSTER) cluster_sync();  // no CTA leaves while another may still write to it
-}
-
-// CTAs per row: the fewest (1, 2, 4, 8) whose parts let two CTAs share an SM,
-// and with few rows as many as the SMs hold at two each.  0: the row does not
-// fit a cluster.
-inline int cluster_for(long long row_bytes, int64_t M) {
-  int c = 1;
-  while (c < kMaxCluster && row_bytes > static_cast<long long>(c) * kPartBytes) c *= 2;
-  if (row_bytes > static_cast<long long>(c) * kPartBytesMax) return 0;
-  while (c < kMaxCluster && M * c <= num_sms() && row_bytes > c * 16 * 1024) c *= 2;
-  return c;
 }
 
 template <typename T>
@@ -798,11 +747,6 @@ cudaError_t launch_t(const void* logits, int64_t ld, int64_t M, int V, const int
                      float* entropy, float* lse, int top_n, int32_t* top_ids, float* top_logprobs, cudaStream_t s) {
   constexpr int kN = Row16<T>::kN;
   const int vecs = (V + kN - 1) / kN;
-  const int C = cluster_for(16ll * vecs, M);
-  if (C == 0)
-    return launch_pdl(token_logprobs<T>, static_cast<unsigned>(M), kThreads, 0, s, 0, static_cast<const T*>(logits),
-                      static_cast<long long>(ld), V, tokens, logprob, entropy, lse, top_n, top_ids, top_logprobs,
-                      device_error_word());
   ScoreArgs<T> a;
   a.logits = static_cast<const T*>(logits);
   a.tokens = tokens;
@@ -816,22 +760,29 @@ cudaError_t launch_t(const void* logits, int64_t ld, int64_t M, int V, const int
   a.M = static_cast<int>(M);
   a.V = V;
   a.top_n = top_n;
-  a.part = (vecs + C - 1) / C;
-  a.slice = (a.part + kWarps - 1) / kWarps;
-  const size_t smem = static_cast<size_t>(kWarps) * a.slice * 16;
-  auto kern = C > 1 ? score_rows<T, true> : score_rows<T, false>;
-  static int configured[2][64] = {{0}};
+  const long long row_bytes = 16ll * vecs;
+  if (row_bytes < kShortAlways || (row_bytes <= kShortBytes && M > 2 * num_sms())) {
+    const int64_t most = 4ll * num_sms(), want = (M + kShortWarps - 1) / kShortWarps;
+    return launch_pdl(score_short<T>, static_cast<unsigned>(std::min(want, most)), kShortWarps * 32, 0, s, 0, a);
+  }
+  const int ring = M > num_sms() ? kRingMany : kRingFew;
+  a.slice = (vecs + kWarps - 1) / kWarps;
+  // one chunk, or several of much the same size in whole vectors of 32 lanes
+  const int most = ring / (kWarps * 16), parts = (a.slice + most / 32 * 32 - 1) / (most / 32 * 32);
+  a.chunk = a.slice <= most ? a.slice : ((a.slice + parts - 1) / parts + 31) / 32 * 32;
+  const size_t smem = static_cast<size_t>(kWarps) * a.chunk * 16;
+  auto kern = score_rows<T>;
+  static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!configured[C > 1][dev]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPartBytesMax + 256);
+  if (!configured[dev]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingFew);
     if (e != cudaSuccess) return e;
-    configured[C > 1][dev] = 1;
+    configured[dev] = 1;
   }
-  const long long fit = std::max(1, 2 * num_sms() / C);
-  const unsigned grid = static_cast<unsigned>(std::min<long long>(M, fit) * C);
-  return launch_pdl(kern, grid, kScoreThreads, smem, s, C > 1 ? C : 0, a);
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(M, 2 * num_sms()));
+  return launch_pdl(kern, grid, kScoreThreads, smem, s, 0, a);
 }
 
 }  // namespace

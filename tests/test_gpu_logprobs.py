@@ -92,18 +92,26 @@ def test_large_vocabularies(dtype, V):
     _check(_logits(2, V, dtype, seed=1), V, dtype, 20)
 
 
+@pytest.mark.parametrize("dtype, M, V", [("bf16", 1, 4088), ("bf16", 1, 4089), ("f32", 2, 2049), ("f32", 400, 10240),
+                                         ("f32", 400, 10241), ("bf16", 400, 20481), ("f16", 304, 9000),
+                                         ("f16", 305, 9000), ("bf16", 5000, 100), ("bf16", 200, 50257)])
+def test_each_side_of_the_kernels_borders(dtype, M, V):
+    """A warp per row, a CTA per row with one chunk or several, one CTA or two per SM."""
+    _check(_logits(M, V, dtype, seed=M), V, dtype, min(20, V))
+
+
 @pytest.mark.parametrize("M", [1, 17, 64, 700])
 def test_many_rows(M):
     _check(_logits(M, 5003, "bf16", seed=M), 5003, "bf16", 20)
     _check(_logits(M, 5003, "f32", seed=M, scale=20.0), 5003, "f32", 3)
 
 
+@pytest.mark.parametrize("V", [20011, 3001])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("kind", ["equal", "two values", "sorted", "falling", "one far ahead", "lowest but one",
                                   "lowest but a few", "inf but a few", "inf but one", "inf but thousands",
                                   "huge", "zeros of both signs", "strided"])
-def test_shapes_of_rows(kind, dtype):
-    V = 20011
+def test_shapes_of_rows(kind, dtype, V):
     z = _logits(3, V, dtype, seed=2)
     low = torch.finfo(DT[dtype][0]).min
     g = torch.Generator().manual_seed(1)
@@ -122,7 +130,7 @@ def test_shapes_of_rows(kind, dtype):
         z[:, :V] = low
         z[:, keep] = vals
     elif kind.startswith("inf"):
-        n = {"one": 1, "few": 9, "thousands": 3000}[kind.split()[-1]]
+        n = {"one": 1, "few": 9, "thousands": V // 7}[kind.split()[-1]]
         # thousands: a contiguous run, so that few of the threads hold any of them
         keep = torch.arange(100, 100 + n) if n > 9 else torch.randperm(V, generator=g)[:n]
         vals = z[:, keep].clone()
