@@ -275,6 +275,43 @@ __device__ __forceinline__ void add_chunk(const uint4* chunk, int cnt, Sums& r) 
   }
 }
 
+// Unsigned keys in the order of the floats (both zeros alike).
+__device__ __forceinline__ unsigned key_of(float x) {
+  const unsigned u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Leaves of the candidates those that reach a value which top_n of them do, and
+// not many more (but for ties); returns how many.  Ranking compares all with
+// all.  One warp, at most kKeep candidates, at least top_n.
+constexpr int kRanked = 64;
+__device__ __noinline__ int fewer(Cand* s_cand, int found, int top_n) {
+  const int lane = threadIdx.x & 31;
+  unsigned low = 0, high = 0xffffffffu;  // low: reached by top_n candidates, high: by fewer
+  while (high - low > 1) {
+    const unsigned mid = low + (high - low) / 2;
+    int n = 0;
+    for (int i = 0; i < found; i += 32)
+      n += __popc(__ballot_sync(0xffffffffu, i + lane < found && key_of(s_cand[i + lane].v) >= mid));
+    if (n >= top_n) {
+      low = mid;
+      if (n <= kRanked) break;
+    } else {
+      high = mid;
+    }
+  }
+  int kept = 0;
+  for (int i = 0; i < found; i += 32) {
+    const Cand c = i + lane < found ? s_cand[i + lane] : Cand{0.f, 0};
+    const bool stay = i + lane < found && key_of(c.v) >= low;
+    const unsigned who = __ballot_sync(0xffffffffu, stay);
+    if (stay) s_cand[kept + __popc(who & ((1u << lane) - 1))] = c;  // (never ahead of what is read)
+    kept += __popc(who);
+    __syncwarp();
+  }
+  return kept;
+}
+
 // Logits above `bound` anywhere in the row, as candidates; returns their
 // number.  One warp.
 template <typename T>
@@ -326,6 +363,7 @@ __device__ __forceinline__ void put_row(const ScoreArgs<T>& a, int row, const Su
   if (found > keep) {
     top_by_passes(z, a.V, a.top_n, m, log_s, ids, lps);
   } else {
+    if (found > kRanked) found = fewer(s_cand, found, a.top_n);
     for (int k = lane; k < found; k += 32) {
       const Cand c = s_cand[k];
       int at = 0;
@@ -351,7 +389,7 @@ __device__ __forceinline__ void put_row(const ScoreArgs<T>& a, int row, const Su
 constexpr int kShortBytes = 40 * 1024;  // of a row, when there are more rows than the other kernel holds
 constexpr int kShortAlways = 8 * 1024;  // under which that kernel's groups have no vector each
 constexpr int kShortWarps = 8;
-constexpr int kShortKeep = 128;
+constexpr int kShortKeep = 512;
 template <typename T>
 __device__ __forceinline__ void add_vectors(const uint4 (&x)[4], Sums& r) {
   using R = Row16<T>;
@@ -397,16 +435,11 @@ __device__ __forceinline__ void add_vectors(const uint4 (&x)[4], Sums& r) {
   r.dot = dot.x + dot.y;
 }
 
-// Unsigned keys in the order of the floats.
-__device__ __forceinline__ unsigned key_of(float x) {
-  const unsigned u = __float_as_uint(x);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kShortWarps * 32, 4) score_short(const ScoreArgs<T> a) {
   __shared__ Cand s_cand[kShortWarps][kShortKeep];
   __shared__ int s_count[kShortWarps];
+  __shared__ uint8_t s_who[kShortWarps][64];  // a row's groups at the bound
   using R = Row16<T>;
   constexpr int kN = R::kN;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -471,25 +504,25 @@ __global__ void __launch_bounds__(kShortWarps * 32, 4) score_short(const ScoreAr
       const float least = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
       if (lane == 0) s_count[warp] = 0;
       __syncwarp();
-      unsigned who = __ballot_sync(0xffffffffu, f0 >= least), who1 = __ballot_sync(0xffffffffu, f1 >= least);
-      for (int h = 0; h < 2; ++h, who = who1) {
-        while (who) {
-          const int f = __ffs(who) - 1;
-          who &= who - 1;
-          for (int v = 32 * h + f + 64 * lane; v < vecs; v += 64 * 32) {  // that group's vectors
-            const uint4 u = zv[v];
-            if (R::reduce(u) < bound && v + 1 < vecs) continue;
-            float e[kN];
-            R::unpack(u, e);
+      const unsigned who0 = __ballot_sync(0xffffffffu, f0 >= least), who1 = __ballot_sync(0xffffffffu, f1 >= least);
+      const int n0 = __popc(who0), below = (1u << lane) - 1;
+      if (who0 >> lane & 1) s_who[warp][__popc(who0 & below)] = static_cast<uint8_t>(lane);
+      if (who1 >> lane & 1) s_who[warp][n0 + __popc(who1 & below)] = static_cast<uint8_t>(32 + lane);
+      __syncwarp();
+      const int each = (vecs + 63) / 64;  // vectors of a group
+      for (int t = lane; t < (n0 + __popc(who1)) * each; t += 32) {
+        const int f = t / each, v = s_who[warp][f] + 64 * (t - f * each);
+        if (v >= vecs) continue;
+        const uint4 u = zv[v];
+        if (R::reduce(u) < bound && v + 1 < vecs) continue;
+        float e[kN];
+        R::unpack(u, e);
 #pragma unroll
-            for (int i = 0; i < kN; ++i)
-              if (e[i] >= least && v * kN + i < a.V) {
-                const int at = atomicAdd(&s_count[warp], 1);
-                if (at < kShortKeep) s_cand[warp][at] = {e[i], v * kN + i};
-              }
+        for (int i = 0; i < kN; ++i)
+          if (e[i] >= least && v * kN + i < a.V) {
+            const int at = atomicAdd(&s_count[warp], 1);
+            if (at < kShortKeep) s_cand[warp][at] = {e[i], v * kN + i};
           }
-          __syncwarp();
-        }
       }
     }
     __syncwarp();
@@ -505,6 +538,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
   __shared__ __align__(16) float s_group[2][64];  // groups' maxima
   __shared__ int s_count[2];
   __shared__ float s_bound[2];
+  __shared__ uint8_t s_who[kWarps][32];  // a warp's lanes at the bound
   // of even and of odd rows (a warp may be a row ahead of another, never two):
   // maxima there, bound given out, settled, finished
   __shared__ __align__(8) uint64_t s_load[kWarps], s_max[2], s_bnd[2], s_set[2], s_fin[2];
@@ -588,13 +622,16 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
         if (lane == 0) atomicAdd(&s_count[buf], kKeep + 1);
         who = 0;
       }
-      // the chunks have gone: these few vectors come from L2
-      const uint4* z = reinterpret_cast<const uint4*>(a.logits + row * a.ld) + v0;
-      while (who) {
-        const int f = __ffs(who) - 1;
-        who &= who - 1;
-        for (int c = 0; c < cnt; c += a.chunk)  // that lane's vectors
-          for (int v = c + f + 32 * lane; v < min(cnt, c + a.chunk); v += 32 * 32) {
+      if (who) {
+        // the chunks have gone: these lanes' vectors come from L2, all at once
+        if (who >> lane & 1) s_who[warp][__popc(who & ((1u << lane) - 1))] = static_cast<uint8_t>(lane);
+        __syncwarp();
+        const uint4* z = reinterpret_cast<const uint4*>(a.logits + row * a.ld) + v0;
+        const int per = (a.chunk + 31) / 32, each = per * chunks;  // vectors of a lane, in a chunk and in all
+        for (int t = lane; t < __popc(who) * each; t += 32) {
+          const int f = t / each, c = (t - f * each) / per;
+          const int in = s_who[warp][f] + 32 * (t - f * each - c * per), v = c * a.chunk + in;
+          if (in >= a.chunk || v >= cnt) continue;
           const uint4 u = z[v];
           if (R::reduce(u) < bound && v + 1 < cnt) continue;
           float x[kN];
@@ -610,7 +647,6 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
             if (at < kKeep) s_cand[buf][at] = {to_f32<T>(reinterpret_cast<const T*>(z + v)[i]), (v0 + v) * kN + i};
           }
         }
-        __syncwarp();
       }
       if (lane == 0) s_sums[buf][warp] = r;
       arrive(s_set, k);

@@ -18,6 +18,7 @@
 // are mma.sync m16n8k16 with the few query heads as rows: a tcgen05 tile would
 // be 128 rows, its operands shared by four warps, and the kernel has no use for
 // the rate.
+#include <algorithm>
 #include <type_traits>
 
 #include "common.cuh"
@@ -32,7 +33,7 @@ constexpr int kTile = 16;    // positions per tile; page sizes are multiples of 
 constexpr int kWarps = 4;    // warps per CTA, independent of one another
 constexpr int kCtasPerSm = 4;
 constexpr int kStages = 2;   // tiles per warp in flight or in use (3: 143 us instead of 137, see below)
-constexpr int kMinRun = 2;   // tiles per warp at least
+constexpr int kMinRun = 2;   // tiles per warp at least, and 4 where a piece of 9 or more heads weighs as much as one
 constexpr int kBoxBytes = kTile * kHd * 2;
 constexpr int kStageBytes = 2 * kBoxBytes;  // K, then V
 constexpr int kWarpBytes = kStages * kStageBytes;
@@ -476,8 +477,7 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   __syncthreads();
   const int total = carry;
   const int n_warps = gridDim.x * kWarps;
-  // (a run of fewer than kMinRun tiles would make more pieces than it saves time)
-  const int run = max((total + n_warps - 1) / n_warps, kMinRun);
+  const int run = max((total + n_warps - 1) / n_warps, WIDE ? 2 * kMinRun : kMinRun);
   if (blockIdx.x == 0) {
     for (int b = tid; b <= a.n_seq; b += kWarps * 32) a.plan[b] = s_base[b];
     if (tid == 0) a.plan[a.n_seq + 1] = run;
@@ -618,12 +618,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_many(const PagedArgs<
   }
 }
 
-// With few items each has many pieces: one CTA per item, `width` heads side by
-// side, and the `ways` groups of threads that are left take every ways-th
-// piece.
+// With few items each has many pieces: one CTA for `width` heads of an item
+// (blockIdx.y: which), side by side; the groups of threads that are left take
+// every ways-th piece.
 constexpr int kJoinFewThreads = 512;
 template <typename T16>
-__global__ void __launch_bounds__(kJoinFewThreads) paged_join_few(const PagedArgs<T16> a, int width, int ways) {
+__global__ void __launch_bounds__(kJoinFewThreads) paged_join_few(const PagedArgs<T16> a, int width) {
   __shared__ float4 s_o[kJoinFewThreads];
   __shared__ float2 s_ml[kJoinFewThreads];
   const int items = a.n_kv * a.n_hb;
@@ -635,21 +635,24 @@ __global__ void __launch_bounds__(kJoinFewThreads) paged_join_few(const PagedArg
   bool second;
   if (sp.nt < 0 || !pieces_of(a, b, item, sp, w0, w1, second)) return;
   const Item<T16> x = item_of(a, b, item, sp);
+  const int ways = kJoinFewThreads / 16 / width;
   const int tid = threadIdx.x, d4 = tid & 15, way = (tid >> 4) / width;
-  for (int h0 = 0; h0 < x.heads; h0 += width) {
-    const int hh = h0 + (tid >> 4) % width;
-    float M = -INFINITY, L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (hh < x.heads) gather(a, w0 + way, ways, w0, w1, second, hh, d4, acc, M, L);
-    s_o[tid] = acc;
-    s_ml[tid] = make_float2(M, L);
+  const int hh = blockIdx.y * width + (tid >> 4) % width;
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (hh < x.heads) gather(a, w0 + way, ways, w0, w1, second, hh, d4, acc, M, L);
+  s_o[tid] = acc;
+  s_ml[tid] = make_float2(M, L);
+  // pairwise, in an order that the number of threads alone gives
+  for (int k = ways >> 1; k > 0; k >>= 1) {
     __syncthreads();
-    if (way == 0 && hh < x.heads) {
-      for (int k = 1; k < ways; ++k) merge(acc, M, L, s_o[tid + 16 * width * k], s_ml[tid + 16 * width * k]);
-      put_joined(a, b, x.head0 + hh, d4, acc, M, L);
+    if (way < k) {
+      merge(acc, M, L, s_o[tid + 16 * width * k], s_ml[tid + 16 * width * k]);
+      s_o[tid] = acc;
+      s_ml[tid] = make_float2(M, L);
     }
-    __syncthreads();
   }
+  if (way == 0 && hh < x.heads) put_joined(a, b, x.head0 + hh, d4, acc, M, L);
 }
 
 // The same work with one CTA per item and nothing to join afterwards: 16 warps
@@ -752,7 +755,11 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   if (!encode_tma_2d(&map, Type16<T16>::kTma, c->pages, kHd, rows, kHd * 2, kHd, kTile)) return cudaErrorInvalidValue;
   const bool wide = a.HB > 8;
   const long long items = static_cast<long long>(c->n_seq) * a.n_kv * a.n_hb;
-  const bool solo = items <= num_sms() && static_cast<long long>(c->max_pages) * c->page_size <= kSoloTiles * kTile;
+  // positions that a query can see: of the window, of the sinks, and what
+  // shares a tile with either
+  long long most = static_cast<long long>(c->max_pages) * c->page_size;
+  if (window > 0) most = std::min(most, static_cast<long long>(window) + sinks + 3 * kTile);
+  const bool solo = items <= num_sms() && most <= kSoloTiles * kTile;
   const int smem = solo ? kSoloWarps * kWarpBytes + 1024 : kWarps * kWarpBytes + 1024 + (c->n_seq + 1) * 4;
   auto kern = solo ? (wide ? paged_attn_solo<T16, true> : paged_attn_solo<T16, false>)
                    : (wide ? paged_attn<T16, true> : paged_attn<T16, false>);
@@ -783,10 +790,10 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
     const unsigned joins = static_cast<unsigned>((items + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
     return launch_pdl(paged_join_many<T16>, joins, kJoinThreads, 0, s, 0, a);
   }
-  int width = 1;
-  while (width < a.HB && width < 8) width *= 2;
-  return launch_pdl(paged_join_few<T16>, static_cast<unsigned>(items), kJoinFewThreads, 0, s, 0, a, width,
-                    kJoinFewThreads / 16 / width);
+  int width = 1;  // as many CTAs as there are places for
+  while (width < 8 && items * ((a.HB + width - 1) / width) > 2 * num_sms()) width *= 2;
+  return launch_pdl(paged_join_few<T16>, dim3(static_cast<unsigned>(items), (a.HB + width - 1) / width),
+                    kJoinFewThreads, 0, s, 0, a, width);
 }
 
 }  // namespace

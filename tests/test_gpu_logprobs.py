@@ -106,7 +106,7 @@ def test_many_rows(M):
     _check(_logits(M, 5003, "f32", seed=M, scale=20.0), 5003, "f32", 3)
 
 
-@pytest.mark.parametrize("V", [20011, 3001])
+@pytest.mark.parametrize("V", [20011, 3001, 300])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("kind", ["equal", "two values", "sorted", "falling", "one far ahead", "lowest but one",
                                   "lowest but a few", "inf but a few", "inf but one", "inf but thousands",
@@ -140,8 +140,8 @@ def test_shapes_of_rows(kind, dtype, V):
         z[:, :V] = z[:, :V] * (-low / 64)
     elif kind == "zeros of both signs":
         z[:, :V] = -5.0
-        z[:, 100:200:2] = -0.0
-        z[:, 101:200:2] = 0.0
+        z[:, 1:280:2] = -0.0
+        z[:, 30:280:2] = 0.0
     else:  # the largest all in the columns that one thread reads
         z[:, 5:V:512] = 30.0
         z[:, 8:V:4096] = 31.0
