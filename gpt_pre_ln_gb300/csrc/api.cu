@@ -384,8 +384,8 @@ Acts carve_acts(void* ws, const gpt2_dims* d, int64_t M) {
 // The body of block `layer` (counted from 0) from `a = LN_1(x)` already
 // computed; x -> x_out.  With kv_layer (16-bit paths), the layer's K and V of
 // all B T positions are also written to cache slots 0..T-1 of a
-// [2, B, n_head, T_max, 64] layer; with paged, to positions lens[b] .. lens[b]
-// + T - 1 of that cache.
+// [2, B, n_head, T_max, 64] layer; with paged, to positions 0 .. T-1 of that
+// cache's sequences of length 0.
 int block_body(const gpt2_dims* d, const gpt2_block_weights* w, int layer, const float* x, float* x_out, int B, int T,
                const Acts& A, cudaStream_t s, void* kv_layer = nullptr, int T_max = 0,
                const gpt2_paged_cache* paged = nullptr) {
@@ -400,7 +400,7 @@ int block_body(const gpt2_dims* d, const gpt2_block_weights* w, int layer, const
   if (paged) {
     ProfScope prof("pages_write", 0.0, 2.0 * M * 2 * D * esize(dt), s);
     const char* k = static_cast<const char*>(A.qkv) + D * esize(dt);
-    GPT2_CUDA(launch_pages_write(paged, layer, k, k + D * esize(dt), 3 * D, T, nullptr, s));
+    GPT2_CUDA(launch_pages_write(paged, layer, k, k + D * esize(dt), 3 * D, T, nullptr, s, true));
   }
   GPT2_CUDA(attention(dt, A.qkv, A.o, B, T, H, score_scale(d, layer), s));
   GPT2_CUDA(linear(dt, A.o, w->w_o, w->b_o, x, A.h, M, D, D, D, false, GPT2_EPI_BIAS_RESIDUAL, GPT2_F32, s));

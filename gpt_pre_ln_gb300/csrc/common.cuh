@@ -44,6 +44,7 @@ enum ErrSite : unsigned {
   kSitePagedFull = 23,    // too few free pages
   kSiteScoreToken = 24,
   kSitePagedLoad = 27,
+  kSitePagedShared = 28,  // a write to a page that several sequences share
   kSiteScoreLoad = 25,
   kSiteScoreJoin = 26,
 };

@@ -187,8 +187,9 @@ cudaError_t launch_pages_fork(const gpt2_paged_cache* c, const int32_t* parents,
                               cudaStream_t s);
 cudaError_t launch_pages_reserve(const gpt2_paged_cache* c, const int32_t* n_new, void* ws, cudaStream_t s);
 cudaError_t launch_pages_compact(const gpt2_paged_cache* c, int32_t* n_used, void* ws, cudaStream_t s);
+// With from_zero rows of sequences whose length is not 0 are skipped.
 cudaError_t launch_pages_write(const gpt2_paged_cache* c, int layer, const void* k, const void* v, int64_t ldkv,
-                               int T, const int32_t* n_new, cudaStream_t s);
+                               int T, const int32_t* n_new, cudaStream_t s, bool from_zero = false);
 
 // Scores from stored logits (logprobs.cu; gpt2_token_logprobs in gpt2gb.h).
 constexpr int kMaxTopN = 32;

@@ -50,6 +50,7 @@ struct PagedArgs {
   int row0, page_rows;  // the pool as rows of 64: the layer's first row, rows per page
   const int32_t* table;
   const int32_t* lens;
+  const int32_t* refs;
   int* plan;       // base[n_seq + 1], then tiles per warp
   float* part_o;   // [2 * warps, HB, 64]
   float2* part_ml;  // [2 * warps, HB]: running maximum (log2 units) and sum
@@ -243,6 +244,14 @@ __device__ __forceinline__ bool attend(const PagedArgs<T16>& a, const Item<T16>&
   uint4 fresh = make_uint4(0, 0, 0, 0);
   const bool has_new = pos_new >= 0 && j0 + (cnt - 1) * step == x.sp.nt - 1;
   if (has_new && lane < 16) fresh = *(reinterpret_cast<const uint4*>(lane < 8 ? x.k_new : x.v_new) + (lane & 7));
+  bool store = has_new && x.hb == 0;
+  if (store) {  // not into a page that other sequences read
+    const int page = x.pages[pos_new / a.page_size];
+    if (page >= 0 && page < a.n_pages && a.refs[page] > 1) {
+      if (lane == 0) record_error(a.err, kErrRange, kSitePagedShared);
+      store = false;
+    }
+  }
   auto visible = [&](int p) { return p < n && (a.window <= 0 || p >= n - a.window || p < a.sinks); };
 
   for (int i = 0; i < cnt; ++i) {
@@ -265,7 +274,7 @@ __device__ __forceinline__ bool attend(const PagedArgs<T16>& a, const Item<T16>&
       const int at = pos_new - pos0;
       if (lane < 16) {
         *reinterpret_cast<uint4*>((lane < 8 ? kb : vb) + at * 128 + (((lane & 7) ^ (at & 7)) << 4)) = fresh;
-        if (x.hb == 0) {
+        if (store) {
           T16* to = a.pages + (static_cast<long long>(row - a.row0) + at + (lane < 8 ? 0 : a.n_kv * a.page_size)) * kHd;
           *reinterpret_cast<uint4*>(to + (lane & 7) * 8) = fresh;
         }
@@ -727,6 +736,7 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   a.row0 = layer * 2 * c->n_kv_head * c->page_size;
   a.table = c->table;
   a.lens = c->lens;
+  a.refs = c->refs;
   a.err = device_error_word();
   a.ldq = ldq;
   a.ldkv = ldkv;

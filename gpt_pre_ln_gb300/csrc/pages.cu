@@ -575,7 +575,8 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move(int32_t* table, lon
 
 // ---------------------------------------------------------------- write
 // Row b * T + t of k and v (n_kv heads of 64) to position lens[b] + t of
-// sequence b, for t < n_new[b] (all T when n_new is null).  ROWS rows per CTA,
+// sequence b, for t < n_new[b] (all T when n_new is null; with from_zero only of
+// sequences of length 0).  ROWS rows per CTA,
 // a thread's 16-byte pieces of all of them on their way at once: with 8, a head's
 // rows of one page go out as 1 KB together.
 constexpr int kWriteRows = 8;
@@ -584,8 +585,10 @@ __global__ void __launch_bounds__(512) pages_write(uint4* __restrict__ layer_pag
                                                    const uint4* __restrict__ k, const uint4* __restrict__ v,
                                                    long long ld_vecs, const int32_t* __restrict__ table,
                                                    const int32_t* __restrict__ lens,
+                                                   const int32_t* __restrict__ refs,
                                                    const int32_t* __restrict__ n_new, int T, long long rows, int n_kv,
-                                                   int page_size, int max_pages, int n_pages, unsigned* err) {
+                                                   int page_size, int max_pages, int n_pages, bool from_zero,
+                                                   unsigned* err) {
   __shared__ long long s_to[ROWS];  // first vector of the row's position in its page, -1: nowhere
   griddep_wait();
   griddep_launch_dependents();
@@ -596,15 +599,17 @@ __global__ void __launch_bounds__(512) pages_write(uint4* __restrict__ layer_pag
     if (row < rows) {
       const int b = static_cast<int>(row / T), t = static_cast<int>(row % T);
       const int len = lens[b];
-      if (len >= 0 && (!n_new || t < n_new[b])) {
+      if ((from_zero ? len == 0 : len >= 0) && (!n_new || t < n_new[b])) {
         const long long pos = static_cast<long long>(len) + t;
         if (pos < static_cast<long long>(max_pages) * page_size) {
           const int c = static_cast<int>(pos / page_size);
           const int page = table[static_cast<long long>(b) * max_pages + c];
-          if (page >= 0 && page < n_pages)
-            to = page * page_vecs + (pos - static_cast<long long>(c) * page_size) * 8;
-          else
+          if (page < 0 || page >= n_pages)
             record_error(err, kErrRange, kSitePagedPage);
+          else if (refs[page] > 1)
+            record_error(err, kErrRange, kSitePagedShared);
+          else
+            to = page * page_vecs + (pos - static_cast<long long>(c) * page_size) * 8;
         } else {
           record_error(err, kErrRange, kSitePagedLength);
         }
@@ -700,7 +705,7 @@ cudaError_t launch_pages_compact(const gpt2_paged_cache* c, int32_t* n_used, voi
 }
 
 cudaError_t launch_pages_write(const gpt2_paged_cache* c, int layer, const void* k, const void* v, int64_t ldkv,
-                               int T, const int32_t* n_new, cudaStream_t s) {
+                               int T, const int32_t* n_new, cudaStream_t s, bool from_zero) {
   const long long layer_vecs = 2ll * c->n_kv_head * c->page_size * 8;
   const int threads = std::min(512, (2 * c->n_kv_head * 8 + 31) / 32 * 32);
   const long long rows = static_cast<long long>(c->n_seq) * T;
@@ -710,8 +715,8 @@ cudaError_t launch_pages_write(const gpt2_paged_cache* c, int layer, const void*
   return launch_pdl(many ? pages_write<kWriteRows> : pages_write<1>, grid, threads, 0, s, 0,
                     static_cast<uint4*>(c->pages) + layer * layer_vecs, layer_vecs * c->n_layer,
                     static_cast<const uint4*>(k), static_cast<const uint4*>(v), static_cast<long long>(ldkv / 8),
-                    c->table, c->lens, n_new, T, rows, c->n_kv_head, c->page_size, c->max_pages, c->n_pages,
-                    device_error_word());
+                    c->table, c->lens, c->refs, n_new, T, rows, c->n_kv_head, c->page_size, c->max_pages, c->n_pages,
+                    from_zero, device_error_word());
 }
 
 }  // namespace gpt2

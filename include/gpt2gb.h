@@ -460,7 +460,9 @@ int gpt2_decode_step(const gpt2_dims *dims, const gpt2_model_weights *w, void *k
  * and lens -1; a new sequence begins with lens[b] = 0.  The state lives on the
  * device, so that a whole serving step (reserve, decode) can be captured into
  * a CUDA graph.  A struct whose table and lens point at a later slot, with a
- * smaller n_seq, is a cache of those slots alone.
+ * smaller n_seq, is a cache of those slots alone.  Calls on one cache belong
+ * on one stream, or in an order that events give: they read and write its
+ * state.
  *   page_size a multiple of 16 and at most 4096; n_seq at most 1024; max_pages
  *   is the length of a table row, with max_pages * page_size < 2^31.  16-bit
  *   types only (GPT2_ERR_UNSUPPORTED for GPT2_F32). */
@@ -531,8 +533,9 @@ int gpt2_pages_compact(const gpt2_paged_cache *cache, int32_t *n_used, void *ws,
  * to position lens[b] + t of sequence b, for t < n_new[b] (int32 [n_seq]
  * device; NULL: all T).  Rows of slots with lens[b] < 0 are skipped.  k and v
  * may point into a c_attn output [n_seq * T, 3D].  The pages must be there
- * and not shared (gpt2_pages_reserve); a position without a page is skipped
- * and GPT2_ERR_RANGE recorded.  n_seq * T < 2^31. */
+ * and not shared (gpt2_pages_reserve); a position without a page, or on one
+ * with refs above 1, is skipped and GPT2_ERR_RANGE recorded.
+ * n_seq * T < 2^31.  lens is not changed. */
 int gpt2_pages_write(const gpt2_paged_cache *cache, int layer, const void *k, const void *v, int64_t ldkv, int T,
                      const int32_t *n_new, gpt2_stream_t stream);
 
@@ -547,7 +550,8 @@ size_t gpt2_attention_paged_workspace_bytes(const gpt2_paged_cache *cache, int n
  * over the n = lens[b] cached positions and, when k_new and v_new are given,
  * the new token's own at position lens[b] (n = lens[b] + 1), which are also
  * stored in the cache there (its page must be there and not shared, see
- * gpt2_pages_reserve; lens is not changed).  window = 0: every position is
+ * gpt2_pages_reserve; with refs above 1 nothing is stored and GPT2_ERR_RANGE
+ * recorded; lens is not changed).  window = 0: every position is
  * visible; window > 0: those with p >= n - window or p < sinks.  Entries of
  * table rows for pages without a visible position are not read.
  *   q [n_seq, n_head * 64] with row stride ldq; k_new, v_new (both or neither)

@@ -253,10 +253,11 @@ def test_faults_are_reported():
     s.prefill(0, g.integers(0, 1000, (2, 10)))
     torch.cuda.synchronize()
     # a prompt into a sequence that already holds positions
-    before = s.lens.clone()
+    before, held = s.lens.clone(), s.pages.clone()
     G.gpt2_prefill_paged(s.cd, s.mw, G.paged_cache(s.pages, s.refs, s.table[:1], s.lens[:1]), _i32([[1, 2, 3]]), 3,
                          s.next[:1], None, 0, s.ws, s.ws.numel())
     assert G.gpt2_last_error()[0] == RANGE and torch.equal(s.lens, before)
+    assert torch.equal(s.pages.view(torch.int16), held.view(torch.int16))
     # a token out of range leaves its sequence alone
     nxt = s.next.clone()
     s.step(_i32([5, 1000, 0]))

@@ -283,7 +283,69 @@ def test_free_pages_are_taken_lowest_first_from_a_large_pool():
     assert x.table.cpu().tolist() == x.m.table and x.refs.cpu().tolist() == x.m.refs
 
 
-@pytest.mark.parametrize("n_pages, used", [(1, 0), (1, 1), (7, 3), (50, 49), (50, 50), (4097, 2000), (9000, 8500)])
+def test_reserve_of_many_entries():
+    """More entries than one CTA has threads: prompts of many pages, some of them shared and all rewritten."""
+    x = Both(1600, 16, 40, 64, layers=1, kv=1)
+    for b in range(20):
+        x.begin(b)
+    x.grow([500 + 7 * b if b < 20 else 0 for b in range(40)])
+    x.check()
+    x.fork(list(range(20)), list(range(20, 40)))
+    x.m.lens = [n - 300 if b % 3 else n for b, n in enumerate(x.m.lens)]  # cut back: shared pages behind the end
+    x.lens.copy_(_i32(x.m.lens))
+    x.grow([301 if b % 5 else 350 for b in range(40)])
+    x.check()
+    x.reserve([900 - n for n in x.m.lens], ok=False)  # too few pages left
+    x.check()
+
+
+def test_fork_of_many_rows():
+    """Tables beyond what one CTA takes: the cluster."""
+    x = Both(4000, 16, 300, 64, layers=1, kv=1)
+    for b in range(100):
+        x.begin(b)
+    x.grow([200 + b if b < 100 else 0 for b in range(300)])
+    g = np.random.default_rng(1)
+    x.fork([int(p) for p in g.integers(0, 120, 250)], [int(c) for c in g.permutation(300)[:250]])
+    x.check()
+    x.fork([int(p) for p in g.integers(0, 300, 300)], [int(c) for c in g.permutation(300)])
+    x.check()
+
+
+@pytest.mark.parametrize("T, kv", [(200, 3), (130, 1), (33, 70)])
+def test_writes_of_many_rows(T, kv):
+    """Several rows per CTA, ragged, across pages, and more heads than a CTA has threads for."""
+    x = Both(150, 16, 20, 30, layers=1, kv=kv)
+    for b in range(18):
+        x.begin(b)
+    x.grow([b % 7 for b in range(20)])
+    n = [min(T, (b * 37) % (T + 1)) if b % 4 else T for b in range(20)]
+    n = [c if b < 10 else 0 for b, c in enumerate(n)]
+    x.reserve(n)
+    x.append(n, T=T)
+    x.check()
+
+
+def test_writes_to_shared_pages_are_refused():
+    x = Both(20, 16, 3, 4)
+    x.begin(0)
+    x.grow([20, 0, 0])
+    x.fork([0], [1])
+    before = x.pages.clone()
+    rows = torch.ones(3 * 2, 3 * 64, dtype=torch.bfloat16, device="cuda")
+    G.gpt2_pages_write(x.cache, 1, rows, rows, 192, 2, _i32([2, 0, 0]))
+    assert G.gpt2_last_error()[0] == RANGE and torch.equal(x.pages, before)
+    need = G.gpt2_attention_paged_workspace_bytes(x.cache, 3)
+    ws, out = torch.empty(need, dtype=torch.uint8, device="cuda"), torch.zeros(3, 192, dtype=torch.bfloat16, device="cuda")
+    G.gpt2_attention_paged(x.cache, 1, rows, 192, rows, rows, 192, out, 192, None, 3, 0.125, 0, 0, ws, need)
+    assert G.gpt2_last_error()[0] == RANGE and torch.equal(x.pages, before)
+    x.reserve([1, 0, 0])
+    G.gpt2_pages_write(x.cache, 1, rows, rows, 192, 2, _i32([1, 0, 0]))
+    assert G.gpt2_last_error()[0] == 0
+
+
+@pytest.mark.parametrize("n_pages, used", [(1, 0), (1, 1), (7, 3), (50, 49), (50, 50), (4097, 2000), (9000, 8500), (16384, 9000), (16385, 9000),
+                                           (40000, 39990)])
 def test_compact(n_pages, used):
     page = 16
     g = np.random.default_rng(n_pages + used)
