@@ -107,7 +107,8 @@ __global__ void __launch_bounds__(256) pages_free(int32_t* table, int32_t* lens,
 // ---------------------------------------------------------------- fork
 // Row children[i] takes the pages that hold the positions of row parents[i]
 // (as all rows were before the call) and its length; what it named before
-// loses a reference.  One CTA, or with many entries one cluster of eight: each
+// loses a reference.  One CTA (5.5 us for 8 rows of 64 pages, the cluster 6.9),
+// or with many entries one cluster of eight: each
 // CTA owns a set of columns and reads them for every pair before it writes
 // any; the lengths are read by every CTA before the cluster's barrier and
 // written after it.
@@ -238,7 +239,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve(int32_t* table, co
   };
   if (total <= kPlanThreads) {
     // One entry per thread (a decode step, short prompts): everything stays in
-    // registers and shared memory, two rounds of loads in all.
+    // registers and shared memory, two rounds of loads in all (5.7 us for nine
+    // sequences; the general way below 8.9).
     const bool mine = tid < total;
     int b = 0, c = 0, p = -1, r = 0;
     if (mine) {
@@ -422,6 +424,8 @@ __global__ void __launch_bounds__(kPlanThreads) pages_reserve(int32_t* table, co
 // 128 contiguous bytes for each of the chunks = n_layer * 2 * n_kv_head
 // pieces of a page.  One warp per piece, four 16-byte loads of a lane in
 // flight.  No page is the source of one copy and the target of another.
+// Bound by HBM: 360 pages of 1.5 MB take 172 us, 6.6 TB/s, 98% of what a plain
+// copy reaches.
 constexpr int kCopyThreads = 256;
 __device__ __forceinline__ void copy_rows(uint4* pages, int n, const int3* copies, int chunks, int page_size) {
   const int lane = threadIdx.x & 31;
@@ -576,9 +580,10 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move(int32_t* table, lon
 // ---------------------------------------------------------------- write
 // Row b * T + t of k and v (n_kv heads of 64) to position lens[b] + t of
 // sequence b, for t < n_new[b] (all T when n_new is null; with from_zero only of
-// sequences of length 0).  ROWS rows per CTA,
-// a thread's 16-byte pieces of all of them on their way at once: with 8, a head's
-// rows of one page go out as 1 KB together.
+// sequences of length 0).  ROWS rows per CTA, a thread's 16-byte pieces of all
+// of them on their way at once: with 8, a head's rows of one page go out as 1 KB
+// together.  Bound by HBM: 16 prompts of 512 to 1023 tokens at 25 heads take
+// 26 us, 5.7 TB/s (one row per CTA 40 us, four 27, sixteen 35).
 constexpr int kWriteRows = 8;
 template <int ROWS>
 __global__ void __launch_bounds__(512) pages_write(uint4* __restrict__ layer_pages, long long page_vecs,
@@ -690,7 +695,7 @@ cudaError_t launch_pages_compact(const gpt2_paged_cache* c, int32_t* n_used, voi
   w.counts = reinterpret_cast<int*>(p + per_page);
   cudaError_t e;
   if (c->n_pages <= kPlanThreads * kScanPer) {
-    // (one CTA's scan: 6 us instead of 9 for the two launches)
+    // (6 us alone, 8.5 as two launches)
     e = launch_pdl(compact_rank, 1, kPlanThreads, 0, s, 0, c->refs, c->n_pages, c->page_size, n_used, true, w);
   } else {
     const int blocks = scan_blocks(c);
