@@ -171,9 +171,9 @@ __device__ void top_equal(const T* z, int V, int top_n, int at, float value, flo
 // place filled again by a bulk copy, with the next row's at the end.  So every
 // logit is read from memory once, and no warp waits for another to load.
 //
-// The alternatives: of each row a warp hands on the maxima of 4 groups of 8
-// lanes.  One more warp takes the top_n-th largest of the 64 groups' maxima,
-// which is no larger than the top_n-th largest logit, and gives it out as a
+// The alternatives: of each row the lanes hand on their maxima.  One more warp
+// finds, by bisection, a value that at least top_n of the 512 reach and few more;
+// it is no larger than the top_n-th largest logit, and is given out as a
 // bound.  The warps look again (in L2) at the few vectors of lanes whose own
 // maximum reaches it, for candidates, and hand on their sums; they do so when
 // they are through with the next row, so that nobody waits for the bound while
@@ -191,7 +191,7 @@ constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kScoreThreads = kThreads + 64;  // and two warps that see to the rows' ends
 constexpr int kKeep = 512;                    // candidates per row
-constexpr int kFlood = 16;                    // lanes of a warp at the bound that make it a row of ties
+constexpr int kFlood = 96;                    // lanes at the bound that make it a row of ties
 constexpr int kRingMany = 100 * 1024;         // two CTAs an SM
 constexpr int kRingFew = 200 * 1024;          // one, when there are no more rows than SMs
 
@@ -535,9 +535,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
   extern __shared__ __align__(128) uint8_t s_row[];  // [kWarps][chunk] vectors
   __shared__ Sums s_sums[2][kWarps];
   __shared__ Cand s_cand[2][kKeep];
-  __shared__ __align__(16) float s_group[2][64];  // groups' maxima
+  __shared__ float s_lane[2][kThreads];  // the lanes' maxima
   __shared__ int s_count[2];
-  __shared__ float s_bound[2];
+  __shared__ float s_bound[2], s_real[2];  // what the warps compare with, and what it is
   __shared__ uint8_t s_who[kWarps][32];  // a warp's lanes at the bound
   // of even and of odd rows (a warp may be a row ahead of another, never two):
   // maxima there, bound given out, settled, finished
@@ -596,14 +596,9 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
       for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
       return m;
     };
-    // The maxima of the warp's four groups of lanes for the bound; returns the warp's.
-    auto hand_on = [&](int k, float m) {
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (lane % 8 == 0) s_group[k & 1][warp * 4 + lane / 8] = m;
+    auto hand_on = [&](int k, float m) {  // the lanes' maxima, for the bound
+      s_lane[k & 1][tid] = m;
       arrive(s_max, k);
-      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-      return fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
     };
     // Of the row before: candidates among what reaches its bound, and its sums.
     // `k`: the number of that row here.
@@ -617,11 +612,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
       }
       const float bound = s_bound[buf];
       const float least = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
-      unsigned who = __ballot_sync(0xffffffffu, mine >= bound && mine > -INFINITY);
-      if (__popc(who) > kFlood) {
-        if (lane == 0) atomicAdd(&s_count[buf], kKeep + 1);
-        who = 0;
-      }
+      const unsigned who = __ballot_sync(0xffffffffu, mine >= bound && mine > -INFINITY);
       if (who) {
         // the chunks have gone: these lanes' vectors come from L2, all at once
         if (who >> lane & 1) s_who[warp][__popc(who & ((1u << lane) - 1))] = static_cast<uint8_t>(lane);
@@ -671,7 +662,8 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
 #pragma unroll 4
         for (int v = lane; v < n; v += 32) mx = R::vmax(mx, chunk[v]);
         mine = fmaxf(mine, R::reduce(mx));
-        const float m = c + 1 == chunks ? hand_on(it, mine) : warp_max(mine);
+        if (c + 1 == chunks) hand_on(it, mine);
+        const float m = warp_max(mine);
         raise(r, m);
         add_chunk<T>(chunk, n, r);
         __syncwarp();
@@ -709,23 +701,35 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
       for (int row = first, it = 0; row < a.M; row += step, ++it) {
         const int buf = it & 1;
         if (!arrived(s_max, it)) break;
+        // a value that at least top_n lanes' maxima reach, and few more than that
         float bound = NAN;  // nothing reaches it
+        bool flood = false;
         if (a.top_n > 0) {
-          const float x0 = s_group[buf][lane], x1 = s_group[buf][lane + 32];
-          int r0 = 0, r1 = 0;
-#pragma unroll 4
-          for (int i = 0; i < 64; i += 4) {
-            const float4 o = *reinterpret_cast<const float4*>(&s_group[buf][i]);
-            const float q[4] = {o.x, o.y, o.z, o.w};
+          unsigned key[kWarps], low = 0xffffffffu, high = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              r0 += (q[e] > x0 || (q[e] == x0 && i + e < lane)) ? 1 : 0;
-              r1 += (q[e] > x1 || (q[e] == x1 && i + e < lane + 32)) ? 1 : 0;
+          for (int i = 0; i < kWarps; ++i) {
+            key[i] = key_of(s_lane[buf][i * 32 + lane]);
+            low = min(low, key[i]);
+            high = max(high, key[i]);
+          }
+          low = __reduce_min_sync(0xffffffffu, low);  // all of them reach it
+          high = __reduce_max_sync(0xffffffffu, high) + 1;  // none does
+          int n = kThreads;
+          while (high - low > 1 && n > a.top_n + 2) {
+            const unsigned mid = low + (high - low) / 2;
+            int c = 0;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) c += key[i] >= mid ? 1 : 0;
+            c = __reduce_add_sync(0xffffffffu, c);
+            if (c >= a.top_n) {
+              low = mid;
+              n = c;
+            } else {
+              high = mid;
             }
           }
-          const unsigned b0 = __ballot_sync(0xffffffffu, r0 == a.top_n - 1);
-          const unsigned b1 = __ballot_sync(0xffffffffu, r1 == a.top_n - 1);
-          bound = b0 ? __shfl_sync(0xffffffffu, x0, __ffs(b0) - 1) : __shfl_sync(0xffffffffu, x1, __ffs(b1) - 1);
+          bound = low & 0x80000000u ? __uint_as_float(low & 0x7fffffffu) : __uint_as_float(~low);
+          flood = n > kFlood;
         }
         if (it > 1) {  // what row it - 2 left in the buffers has been used
           ok = mbar_wait(smem_u32(&s_fin[buf]), ((it >> 1) - 1) & 1);
@@ -736,7 +740,10 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
           }
         }
         if (lane == 0) {
-          s_bound[buf] = bound;
+          // ties by the hundred: nothing is to be collected, the row's end sees to it
+          s_bound[buf] = flood ? NAN : bound;
+          s_real[buf] = bound;
+          if (flood) s_count[buf] = kKeep + 1;
           mbar_arrive(smem_u32(&s_bnd[buf]));
         }
         __syncwarp();
@@ -769,7 +776,7 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
           s += __shfl_xor_sync(0xffffffffu, s, o);
           d += __shfl_xor_sync(0xffffffffu, d, o);
         }
-        put_row(a, row, Sums{m, s, d}, z_tok, s_bound[buf], s_cand[buf], &s_count[buf], kKeep);
+        put_row(a, row, Sums{m, s, d}, z_tok, s_real[buf], s_cand[buf], &s_count[buf], kKeep);
         if (lane == 0) s_count[buf] = 0;  // next added to behind the bound of two rows on
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&s_fin[buf]));
