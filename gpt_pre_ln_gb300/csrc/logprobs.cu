@@ -182,11 +182,14 @@ __device__ void top_equal(const T* z, int V, int top_n, int at, float value, flo
 // row in turn: row r is finished before the bound of row r + 2 is given out,
 // and nothing of row r + 2 but its maxima is written before that.
 //
-// Measured at 8192 x 50257 in bf16 with 20 alternatives: 167 us, 4.9 TB/s (three
-// passes over memory and L2 took 283).  About 17 500 warp instructions a row
-// keep the issue slots 70% busy, and a slice's place lies empty from the end of
-// one copy to the end of the sums; two and three smaller places for each warp fill that gap
-// but take more instructions, chunk by chunk (203 and 229 us).
+// Measured at 8192 x 50257 in bf16 with 20 alternatives: 159 us, 5.2 TB/s (three
+// passes over memory and L2 took 283).  About 16 700 warp instructions a row
+// keep two thirds of the issue slots busy, and a warp's place lies empty from
+// the end of one copy to the end of the sums; two and three smaller places for
+// each warp fill that gap but take more instructions, chunk by chunk (203 and
+// 229 us).  Likely tokens that stand together are one warp's to look at again:
+// logits that fall by 1e-3 an id take 293 us.  Rows dealt out to the warps in
+// pieces of 512 bytes would take 195 for those, and 169 where nothing falls.
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kScoreThreads = kThreads + 64;  // and two warps that see to the rows' ends

@@ -70,14 +70,15 @@ struct Span {
 };
 template <typename T16>
 __device__ __forceinline__ Span span_of(const PagedArgs<T16>& a, int b, bool record) {
-  const int len = a.lens[b];
-  const int n = len + (a.k_new ? 1 : 0);
-  Span s{n, 0, 0, -1};
+  const int len = a.lens[b], more = a.k_new ? 1 : 0;
+  Span s{0, 0, 0, -1};
   if (len < 0) return s;
-  if (n > a.max_pages * a.page_size) {
+  if (len > a.max_pages * a.page_size - more) {
     if (record) record_error(a.err, kErrRange, kSitePagedLength);
     return s;
   }
+  const int n = len + more;
+  s.n = n;
   const int te = (n + kTile - 1) / kTile;
   if (a.window > 0 && n > a.window) {
     const int first = n - a.window;
@@ -734,6 +735,7 @@ template <typename T16>
 cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_t ldq, const void* k_new,
                      const void* v_new, int64_t ldkv, void* out, int64_t ldo, float* lse, int n_head,
                      float score_scale, int window, int sinks, void* ws, cudaStream_t s) {
+  const int sms = num_sms();
   PagedArgs<T16> a;
   a.q = static_cast<const T16*>(q);
   a.k_new = static_cast<const T16*>(k_new);
@@ -767,7 +769,7 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   a.plan = reinterpret_cast<int*>(base);
   base += align256((static_cast<size_t>(c->n_seq) + 2) * 4);
   a.part_ml = reinterpret_cast<float2*>(base);
-  base += align256(2ull * max_warps() * a.HB * sizeof(float2));
+  base += align256(2ull * sms * kCtasPerSm * kWarps * a.HB * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(base);
   // the pool as one [rows, 64] matrix
   const uint64_t rows = static_cast<uint64_t>(c->n_pages) * a.page_rows;
@@ -779,7 +781,7 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   // shares a tile with either
   long long most = static_cast<long long>(c->max_pages) * c->page_size;
   if (window > 0) most = std::min(most, static_cast<long long>(window) + sinks + 3 * kTile);
-  const bool solo = items <= num_sms() && most <= kSoloTiles * kTile;
+  const bool solo = items <= sms && most <= kSoloTiles * kTile;
   const int smem = solo ? kSoloWarps * kWarpBytes + 1024 : kWarps * kWarpBytes + 1024 + (c->n_seq + 1) * 4;
   auto kern = solo ? (wide ? paged_attn_solo<T16, true> : paged_attn_solo<T16, false>)
                    : (wide ? paged_attn<T16, true> : paged_attn<T16, false>);
@@ -804,14 +806,14 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
     done = 1;
   }
   if (solo) return launch_pdl(kern, static_cast<unsigned>(items), kSoloWarps * 32, smem, s, 0, map, a);
-  cudaError_t e = launch_pdl(kern, num_sms() * kCtasPerSm, kWarps * 32, smem, s, 0, map, a);
+  cudaError_t e = launch_pdl(kern, sms * kCtasPerSm, kWarps * 32, smem, s, 0, map, a);
   if (e != cudaSuccess) return e;
-  if (items > num_sms()) {
+  if (items > sms) {
     const unsigned joins = static_cast<unsigned>((items + kJoinThreads / 32 - 1) / (kJoinThreads / 32));
     return launch_pdl(paged_join_many<T16>, joins, kJoinThreads, 0, s, 0, a);
   }
   int width = 1;  // as many CTAs as there are places for
-  while (width < 8 && items * ((a.HB + width - 1) / width) > 2 * num_sms()) width *= 2;
+  while (width < 8 && items * ((a.HB + width - 1) / width) > 2 * sms) width *= 2;
   return launch_pdl(paged_join_few<T16>, dim3(static_cast<unsigned>(items), (a.HB + width - 1) / width),
                     kJoinFewThreads, 0, s, 0, a, width);
 }

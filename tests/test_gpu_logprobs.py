@@ -110,7 +110,8 @@ def test_many_rows(M):
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("kind", ["equal", "two values", "sorted", "falling", "one far ahead", "lowest but one",
                                   "lowest but a few", "inf but a few", "inf but one", "inf but thousands",
-                                  "huge", "zeros of both signs", "strided"])
+                                  "huge", "zeros of both signs", "strided", "low ids ahead",
+                                  "low ids far ahead"])
 def test_shapes_of_rows(kind, dtype, V):
     z = _logits(3, V, dtype, seed=2)
     low = torch.finfo(DT[dtype][0]).min
@@ -138,6 +139,8 @@ def test_shapes_of_rows(kind, dtype, V):
         z[:, keep] = vals
     elif kind == "huge":
         z[:, :V] = z[:, :V] * (-low / 64)
+    elif kind.startswith("low ids"):
+        z[:, :V] -= (torch.arange(V, device="cuda") * (0.1 if "far" in kind else 0.001)).to(z.dtype)
     elif kind == "zeros of both signs":
         z[:, :V] = -5.0
         z[:, 1:280:2] = -0.0

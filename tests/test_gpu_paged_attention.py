@@ -296,6 +296,15 @@ def test_bad_pages_and_lengths_are_reported_and_the_rest_is_right():
     assert np.abs(c.out[1, :64].double().cpu().numpy() - ref).max() < 0.02
 
 
+def test_lengths_far_out_of_range_are_reported():
+    c = Case([40, 50], heads=2, kv_heads=2, seed=17)
+    c.lens[1] = 2 ** 31 - 1
+    c.run()
+    c.check(rows=[0])
+    assert (c.out[1] == 7.0).all()
+    assert G.gpt2_last_error()[0] == RANGE
+
+
 def test_view_of_later_slots():
     c = Case([40, 50, 60], heads=2, kv_heads=2, seed=10)
     c.cache = G.paged_cache(c.pages, c.refs, c.table[1:], c.lens[1:])
