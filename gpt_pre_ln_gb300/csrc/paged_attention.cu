@@ -468,8 +468,6 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   Ring ring = ring_of<T16>(&map, s_tiles, s_bar, warp);
   if (lane == 0) tma_prefetch_desc(&map);
-  // (no early launch of the join: its CTAs, waiting in the places of ours that
-  // are through, cost a window case of 128 sequences 169 us instead of 143)
   griddep_wait();
   const int items = a.n_kv * a.n_hb;
   // base[b] = tiles of all items of sequences before b
@@ -525,6 +523,9 @@ __global__ void __launch_bounds__(kWarps * 32, kCtasPerSm)
     const Item<T16> x = item_of(a, lo, item, sp);
     Acc acc;
     if (!attend<T16, WIDE>(a, x, j0, 1, cnt, ring, acc)) return;
+    // the join may come now; earlier, its CTAs, waiting in the places of ours
+    // that are through, cost a window case of 128 sequences 169 us instead of 137
+    if (t + cnt >= t_end) griddep_launch_dependents();
     if (cnt == sp.nt) {
 #pragma unroll
       for (int g = 0; g < (WIDE ? 2 : 1); ++g) {

@@ -269,3 +269,23 @@ def test_faults_are_reported():
     s.step(_i32([5, 6, 0]), reserve=False)
     assert G.gpt2_last_error()[0] == RANGE
     assert s.lens.cpu().tolist() == [128, 11, -1]
+
+
+def test_more_rows_than_the_few_row_gemm_takes():
+    """130 slots, three of them in use: the tiled GEMMs and the argmax over stored logits."""
+    s = Server(130, n_pages=40, max_pages=4)
+    g = np.random.default_rng(8)
+    first, last = g.integers(0, 1000, (1, 18)), g.integers(0, 1000, (2, 31))
+    s.prefill(7, first)
+    s.prefill(128, last)
+    seqs = {7: list(first[0]), 128: list(last[0]), 129: list(last[1])}
+    for _ in range(3):
+        tok = s.next.clone()
+        for k in seqs:
+            seqs[k].append(int(tok[k]))
+        s.step(tok)
+        got = s.got()
+        for k, t in seqs.items():
+            assert _rel(got[k], _ref_last(s, t)) < 1e-2
+            assert int(s.next[k]) == int(np.argmax(got[k]))
+    assert int((s.lens >= 0).sum()) == 3 and int(s.next[0]) == -1
