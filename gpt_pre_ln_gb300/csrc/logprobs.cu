@@ -182,14 +182,15 @@ __device__ void top_equal(const T* z, int V, int top_n, int at, float value, flo
 // row in turn: row r is finished before the bound of row r + 2 is given out,
 // and nothing of row r + 2 but its maxima is written before that.
 //
-// Measured at 8192 x 50257 in bf16 with 20 alternatives: 159 us, 5.2 TB/s (three
-// passes over memory and L2 took 283).  About 16 700 warp instructions a row
+// Measured at 8192 x 50257 in bf16 with 20 alternatives: 153 us, 5.4 TB/s (three
+// passes over memory and L2 took 283).  Some 16 000 warp instructions a row
 // keep two thirds of the issue slots busy, and a warp's place lies empty from
 // the end of one copy to the end of the sums; two and three smaller places for
 // each warp fill that gap but take more instructions, chunk by chunk (203 and
-// 229 us).  Likely tokens that stand together are one warp's to look at again:
-// logits that fall by 1e-3 an id take 293 us.  Rows dealt out to the warps in
-// pieces of 512 bytes would take 195 for those, and 169 where nothing falls.
+// 229 us).  Without the second look at the candidates it would be 131.  Likely
+// tokens that stand together are one warp's to look at again: logits that fall
+// by 1e-3 an id take 300 us.  Rows dealt out to the warps in pieces of 512
+// bytes took 195 for those, and 169 where nothing falls.
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kScoreThreads = kThreads + 64;  // and two warps that see to the rows' ends
@@ -541,7 +542,6 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
   __shared__ float s_lane[2][kThreads];  // the lanes' maxima
   __shared__ int s_count[2];
   __shared__ float s_bound[2], s_real[2];  // what the warps compare with, and what it is
-  __shared__ uint8_t s_who[kWarps][32];  // a warp's lanes at the bound
   // of even and of odd rows (a warp may be a row ahead of another, never two):
   // maxima there, bound given out, settled, finished
   __shared__ __align__(8) uint64_t s_load[kWarps], s_max[2], s_bnd[2], s_set[2], s_fin[2];
@@ -615,32 +615,30 @@ __global__ void __launch_bounds__(kScoreThreads, 2) score_rows(const ScoreArgs<T
       }
       const float bound = s_bound[buf];
       const float least = fmaxf(bound, -3.402823466e38f);  // (-inf is no candidate)
-      const unsigned who = __ballot_sync(0xffffffffu, mine >= bound && mine > -INFINITY);
-      if (who) {
-        // the chunks have gone: these lanes' vectors come from L2, all at once
-        if (who >> lane & 1) s_who[warp][__popc(who & ((1u << lane) - 1))] = static_cast<uint8_t>(lane);
-        __syncwarp();
-        const uint4* z = reinterpret_cast<const uint4*>(a.logits + row * a.ld) + v0;
-        const int per = (a.chunk + 31) / 32, each = per * chunks;  // vectors of a lane, in a chunk and in all
-        for (int t = lane; t < __popc(who) * each; t += 32) {
-          const int f = t / each, c = (t - f * each) / per;
-          const int in = s_who[warp][f] + 32 * (t - f * each - c * per), v = c * a.chunk + in;
-          if (in >= a.chunk || v >= cnt) continue;
-          const uint4 u = z[v];
-          if (R::reduce(u) < bound && v + 1 < cnt) continue;
-          float x[kN];
-          R::unpack(u, x);
-          unsigned hit = 0;
+      unsigned who = __ballot_sync(0xffffffffu, mine >= bound && mine > -INFINITY);
+      // the chunks have gone: the vectors of these lanes come from L2, half a
+      // warp for each lane
+      const uint4* z = reinterpret_cast<const uint4*>(a.logits + row * a.ld) + v0;
+      while (who) {
+        const int f0 = __ffs(who) - 1;
+        who &= who - 1;
+        const int f1 = who ? __ffs(who) - 1 : cnt;  // (cnt: none)
+        who &= who - 1;
+        const int f = lane < 16 ? f0 : f1;
+        for (int c = 0; c < cnt; c += a.chunk)
+          for (int v = c + f + 32 * (lane & 15); v < min(cnt, c + a.chunk); v += 32 * 16) {
+            const uint4 u = z[v];
+            if (R::reduce(u) < bound && v + 1 < cnt) continue;
+            float x[kN];
+            R::unpack(u, x);
 #pragma unroll
-          for (int i = 0; i < kN; ++i) hit |= x[i] >= least ? 1u << i : 0u;
-          if (pad && v + 1 == cnt) hit &= (1u << pad) - 1;
-          while (hit) {
-            const int i = __ffs(hit) - 1;
-            hit &= hit - 1;
-            const int at = atomicAdd(&s_count[buf], 1);
-            if (at < kKeep) s_cand[buf][at] = {to_f32<T>(reinterpret_cast<const T*>(z + v)[i]), (v0 + v) * kN + i};
+            for (int i = 0; i < kN; ++i)
+              if (x[i] >= least && (v + 1 < cnt || !pad || i < pad)) {
+                const int at = atomicAdd(&s_count[buf], 1);
+                if (at < kKeep) s_cand[buf][at] = {x[i], (v0 + v) * kN + i};
+              }
           }
-        }
+        __syncwarp();
       }
       if (lane == 0) s_sums[buf][warp] = r;
       arrive(s_set, k);
