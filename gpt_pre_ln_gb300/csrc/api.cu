@@ -511,7 +511,7 @@ struct DecodeGroup {
     const int D = d->d_model;
     ProfScope prof("decode_embed_layernorm", 8.0 * nb * D, static_cast<double>(nb) * D * 10.0, s);
     return launch_decode_embed_ln(d->dtype, tokens, past_len, w->wte, w->wpe, w->blocks[0].ln1_g,
-                                  w->blocks[0].ln1_b, A.x, A.a, nb, D, d->vocab, d->n_pos, T_max, d->eps, valid, s, paged != nullptr);
+                                  w->blocks[0].ln1_b, A.x, A.a, nb, D, d->vocab, d->n_pos, T_max, d->eps, valid, s, paged);
   }
 
   cudaError_t layer(int l) {
@@ -635,7 +635,7 @@ int prefill(const gpt2_dims* dims, const gpt2_model_weights* w, const int32_t* t
   GPT2_TRY(forward_to_lnf(dims, w, tokens, B, T, A, s, kv_cache, T_max, false, paged));
   {
     ProfScope prof("prefill_last_rows", 0.0, 8.0 * B * D, s);
-    GPT2_CUDA(launch_prefill_last_rows(A.x, B, T, D, x_last, valid, past_len, s, paged != nullptr));
+    GPT2_CUDA(launch_prefill_last_rows(A.x, B, T, D, x_last, valid, past_len, s, paged));
   }
   GPT2_CUDA(layernorm(x_last, w->lnf_g, w->lnf_b, a_last, B, D, dims->eps, GPT2_F32, dt, s));
   if (B <= kMaxRowsGemm) {

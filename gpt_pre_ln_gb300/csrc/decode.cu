@@ -25,14 +25,20 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// One warp per sequence: valid[b] = position and token in range;
-// x = wte[token] + wpe[pos]; y = LN(x).
+// Entry c of sequence b's table row names a page that this sequence alone holds.
+__device__ __forceinline__ bool own_page(const gpt2_paged_cache& cache, int b, int c) {
+  const int page = cache.table[static_cast<long long>(b) * cache.max_pages + c];
+  return page >= 0 && page < cache.n_pages && cache.refs[page] <= 1;
+}
+
+// One warp per sequence: valid[b] = position and token in range (paged: and a
+// page of its own there); x = wte[token] + wpe[pos]; y = LN(x).
 template <typename T16>
 __global__ void decode_embed_ln(const int32_t* __restrict__ tokens, const int32_t* __restrict__ past_len,
                                 const T16* __restrict__ wte, const T16* __restrict__ wpe,
                                 const T16* __restrict__ gamma, const T16* __restrict__ beta, float* __restrict__ x,
                                 T16* __restrict__ y, int B, int D, int V, int n_pos, int T_max, float eps,
-                                int* __restrict__ valid, bool idle_slots, unsigned* err) {
+                                int* __restrict__ valid, const gpt2_paged_cache paged, unsigned* err) {
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
@@ -41,11 +47,13 @@ __global__ void decode_embed_ln(const int32_t* __restrict__ tokens, const int32_
   const int pos = past_len[b];
   const int tok = tokens[b];
   const bool pos_ok = pos >= 0 && pos < n_pos && pos < T_max;
+  const bool page_ok = !paged.table || !pos_ok || own_page(paged, b, pos / paged.page_size);
   const bool tok_ok = tok >= 0 && tok < V;
   if (lane == 0) {
-    valid[b] = (pos_ok && tok_ok) ? 1 : 0;
-    const bool idle = idle_slots && pos == -1;
+    valid[b] = (pos_ok && page_ok && tok_ok) ? 1 : 0;
+    const bool idle = paged.table && pos == -1;
     if (!pos_ok && !idle) record_error(err, kErrRange, kSiteDecodePos);
+    if (!page_ok) record_error(err, kErrRange, kSitePagedPage);
     if (!tok_ok && !idle) record_error(err, kErrRange, kSiteDecodeToken);
   }
   const bool ok = pos_ok && tok_ok;
@@ -370,11 +378,11 @@ __global__ void kv_from_qkv(const T16* __restrict__ qkv, T16* __restrict__ kv_la
 }
 
 // After the prompt: x_last[b] = x[b T + T - 1] (the residual stream of each
-// sequence's last position), valid[b] = 1, past_len[b] = T (with from_zero
-// only where past_len[b] was 0).
+// sequence's last position), valid[b] = 1, past_len[b] = T (paged: only
+// where past_len[b] was 0 and the T positions have pages of their own).
 __global__ void prefill_last_rows(const float* __restrict__ x, int T, int D, float* __restrict__ x_last,
-                                  int* __restrict__ valid, int32_t* __restrict__ past_len, bool from_zero,
-                                  unsigned* err) {
+                                  int* __restrict__ valid, int32_t* __restrict__ past_len,
+                                  const gpt2_paged_cache paged, unsigned* err) {
   griddep_wait();
   griddep_launch_dependents();
   const int b = blockIdx.x;
@@ -382,13 +390,18 @@ __global__ void prefill_last_rows(const float* __restrict__ x, int T, int D, flo
   for (int i = threadIdx.x * 4; i < D; i += blockDim.x * 4)
     *reinterpret_cast<float4*>(x_last + static_cast<long long>(b) * D + i) =
         *reinterpret_cast<const float4*>(src + i);
+  bool missing = false;
+  if (paged.table)
+    for (int c = threadIdx.x; c < (T + paged.page_size - 1) / paged.page_size; c += blockDim.x)
+      missing |= !own_page(paged, b, c);
+  missing = __syncthreads_or(missing);
   if (threadIdx.x == 0) {
-    const bool ok = !from_zero || past_len[b] == 0;
-    valid[b] = ok ? 1 : 0;
-    if (ok)
+    const bool empty = !paged.table || past_len[b] == 0;
+    valid[b] = empty && !missing ? 1 : 0;
+    if (empty && !missing)
       past_len[b] = T;
     else
-      record_error(err, kErrRange, kSitePagedLength);
+      record_error(err, kErrRange, empty ? kSitePagedPage : kSitePagedLength);
   }
 }
 
@@ -407,28 +420,29 @@ cudaError_t launch_kv_from_qkv(gpt2_dtype dt, const void* qkv, void* kv_layer, i
 }
 
 cudaError_t launch_prefill_last_rows(const float* x, int B, int T, int D, float* x_last, int* valid,
-                                     int32_t* past_len, cudaStream_t stream, bool from_zero) {
-  return launch_pdl(prefill_last_rows, B, 256, 0, stream, 0, x, T, D, x_last, valid, past_len, from_zero,
-                    device_error_word());
+                                     int32_t* past_len, cudaStream_t stream, const gpt2_paged_cache* paged) {
+  return launch_pdl(prefill_last_rows, B, 256, 0, stream, 0, x, T, D, x_last, valid, past_len,
+                    paged ? *paged : gpt2_paged_cache{}, device_error_word());
 }
 
 cudaError_t launch_decode_embed_ln(gpt2_dtype dt, const int32_t* tokens, const int32_t* past_len, const void* wte,
                                    const void* wpe, const void* gamma, const void* beta, float* x, void* y, int B,
                                    int D, int V, int n_pos, int T_max, float eps, int* valid, cudaStream_t stream,
-                                   bool idle_slots) {
+                                   const gpt2_paged_cache* paged) {
   const int warps = 4;
   const dim3 grid((B + warps - 1) / warps), block(warps * 32);
   unsigned* err = device_error_word();
+  const gpt2_paged_cache cache = paged ? *paged : gpt2_paged_cache{};
   if (dt == GPT2_F16) {
     using T = __half;
     return launch_pdl(decode_embed_ln<T>, grid, block, 0, stream, 0, tokens, past_len, static_cast<const T*>(wte),
                       static_cast<const T*>(wpe), static_cast<const T*>(gamma), static_cast<const T*>(beta), x,
-                      static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, idle_slots, err);
+                      static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, cache, err);
   }
   using T = __nv_bfloat16;
   return launch_pdl(decode_embed_ln<T>, grid, block, 0, stream, 0, tokens, past_len, static_cast<const T*>(wte),
                     static_cast<const T*>(wpe), static_cast<const T*>(gamma), static_cast<const T*>(beta), x,
-                    static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, idle_slots, err);
+                    static_cast<T*>(y), B, D, V, n_pos, T_max, eps, valid, cache, err);
 }
 
 namespace {

@@ -132,13 +132,13 @@ cudaError_t launch_attention_backward_tc(gpt2_dtype dt, const void* qkv, const v
 cudaError_t launch_attention_f32(const float* qkv, float* out, int B, int T, int n_head, float score_scale,
                                  cudaStream_t stream);
 
-// Decode-step kernels (16-bit paths; dt GPT2_BF16 or GPT2_F16).  With
-// idle_slots a past_len of -1 is a slot without a sequence: not valid, and no
-// error.
+// Decode-step kernels (16-bit paths; dt GPT2_BF16 or GPT2_F16).  With a paged
+// cache a past_len of -1 is a slot without a sequence: not valid, and no error;
+// a sequence whose next position has no page of its own is not valid (an error).
 cudaError_t launch_decode_embed_ln(gpt2_dtype dt, const int32_t* tokens, const int32_t* past_len, const void* wte,
                                    const void* wpe, const void* gamma, const void* beta, float* x, void* y, int B,
                                    int D, int V, int n_pos, int T_max, float eps, int* valid, cudaStream_t stream,
-                                   bool idle_slots = false);
+                                   const gpt2_paged_cache* paged = nullptr);
 // Rows 0..B-1 of qkv / out / past_len / valid are sequences b_cache0 ..
 // b_cache0 + B - 1 of a cache laid out for B_cache sequences.
 cudaError_t launch_decode_attention(gpt2_dtype dt, const void* qkv, void* kv_layer, void* out, const int32_t* past_len,
@@ -149,10 +149,10 @@ cudaError_t launch_decode_attention(gpt2_dtype dt, const void* qkv, void* kv_lay
 cudaError_t launch_kv_from_qkv(gpt2_dtype dt, const void* qkv, void* kv_layer, int B, int T, int n_head, int T_max,
                                cudaStream_t stream);
 // x_last[b] = x[b T + T - 1] (fp32 [B, D]), valid[b] = 1, past_len[b] = T.
-// With from_zero a sequence whose past_len is not 0 is not valid (an error)
-// and keeps its past_len.
+// With a paged cache a sequence whose past_len is not 0, or that lacks pages of
+// its own for T positions, is not valid (an error) and keeps its past_len.
 cudaError_t launch_prefill_last_rows(const float* x, int B, int T, int D, float* x_last, int* valid,
-                                     int32_t* past_len, cudaStream_t stream, bool from_zero = false);
+                                     int32_t* past_len, cudaStream_t stream, const gpt2_paged_cache* paged = nullptr);
 // past_len may be null in the two argmax launchers (no increment).
 cudaError_t launch_argmax_rows(const float* logits, int64_t ld, int B, int V, const int* valid, int32_t* next_tokens,
                                int32_t* past_len, cudaStream_t stream);

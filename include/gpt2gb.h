@@ -575,8 +575,9 @@ int gpt2_attention_paged(const gpt2_paged_cache *cache, int layer, const void *q
 
 /* gpt2_prefill into a paged cache of n_seq sequences with n_kv_head = n_head:
  * every sequence must have lens[b] = 0 and pages for T positions
- * (gpt2_pages_reserve); sets lens[b] = T.  A sequence with another length is
- * left as it was and GPT2_ERR_RANGE recorded.  tokens [n_seq, T]; the other
+ * (gpt2_pages_reserve); sets lens[b] = T.  A sequence with another length, or
+ * without pages of its own for all T, keeps its lens and next_tokens and
+ * GPT2_ERR_RANGE is recorded; its row of logits_opt is not defined.  tokens [n_seq, T]; the other
  * arguments as gpt2_prefill.  The prompt's own attention is causal over all of
  * it (no window). */
 size_t gpt2_prefill_paged_workspace_bytes(const gpt2_dims *dims, const gpt2_paged_cache *cache, int T);
@@ -588,7 +589,10 @@ int gpt2_prefill_paged(const gpt2_dims *dims, const gpt2_model_weights *w, const
  * of each sequence, its page reserved before (gpt2_pages_reserve with n_new =
  * 1), attention as gpt2_attention_paged with `window` and `sinks`; lens[b] +=
  * 1.  Slots with lens[b] = -1 are skipped: their next_tokens stay, and their
- * row of logits_opt is not defined. */
+ * row of logits_opt is not defined.  The same holds, with GPT2_ERR_RANGE
+ * recorded, for a sequence whose position or token is out of range or whose
+ * position has no page of its own (the pool had run short): it may take the
+ * step again once there is one. */
 size_t gpt2_decode_step_paged_workspace_bytes(const gpt2_dims *dims, const gpt2_paged_cache *cache);
 int gpt2_decode_step_paged(const gpt2_dims *dims, const gpt2_model_weights *w, const gpt2_paged_cache *cache,
                            int window, int sinks, const int32_t *tokens, int32_t *next_tokens, float *logits_opt,

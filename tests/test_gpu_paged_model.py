@@ -289,3 +289,54 @@ def test_more_rows_than_the_few_row_gemm_takes():
             assert _rel(got[k], _ref_last(s, t)) < 1e-2
             assert int(s.next[k]) == int(np.argmax(got[k]))
     assert int((s.lens >= 0).sum()) == 3 and int(s.next[0]) == -1
+
+
+def test_a_pool_that_runs_short_leaves_its_sequences():
+    """A sequence without a page for its next position takes no step, the others do; once there is a page it takes
+    the step with the result it would have had."""
+    s, full = Server(3, n_pages=5), Server(3)
+    g = np.random.default_rng(9)
+    a, b, c = g.integers(0, 1000, (1, 32)), g.integers(0, 1000, (1, 20)), g.integers(0, 1000, (1, 5))
+    for x in (s, full):
+        x.prefill(0, a)
+        x.prefill(1, b)
+        x.prefill(2, c)
+    G.gpt2_pages_free(s.cache, _i32([2]), 1)
+    G.gpt2_pages_fork(s.cache, _i32([1]), _i32([2]), 1)  # shares b's pages: sequence 2 may not write either
+    torch.cuda.synchronize()
+    assert G.gpt2_last_error()[0] == 0
+    assert int((s.refs == 0).sum()) == 1
+    s.reserve([1, 1, 1])  # two entries want another page, one is free
+    assert G.gpt2_last_error()[0] == RANGE
+    tok = _i32([3, 4, 4])
+    before = s.next.clone()
+    s.step(tok, reserve=False)
+    torch.cuda.synchronize()
+    assert G.gpt2_last_error()[0] == RANGE
+    assert s.lens.cpu().tolist() == [32, 20, 20] and torch.equal(s.next, before)
+    G.gpt2_pages_free(s.cache, _i32([2]), 1)
+    s.reserve([0, 1, 0])
+    s.step(tok, reserve=False)  # sequence 0 still has none, sequence 1 steps
+    assert G.gpt2_last_error()[0] == RANGE
+    assert s.lens.cpu().tolist() == [32, 21, -1] and int(s.next[0]) == int(before[0])
+    s.step(tok)
+    torch.cuda.synchronize()
+    assert G.gpt2_last_error()[0] == 0 and s.lens.cpu().tolist() == [33, 22, -1]
+    full.step(tok)
+    got, ref = s.got()[0], full.got()[0]
+    assert np.array_equal(got, ref) and int(s.next[0]) == int(full.next[0])
+    assert _rel(got, _ref_last(s, list(a[0]) + [3])) < 1e-2
+
+
+def test_a_prompt_without_its_pages_is_not_taken():
+    s = Server(2, n_pages=3)
+    g = np.random.default_rng(10)
+    prompt = g.integers(0, 1000, (2, 20))
+    s.prefill(0, prompt)  # four pages wanted
+    assert G.gpt2_last_error()[0] == RANGE
+    assert s.lens.cpu().tolist() == [0, 0] and s.next.cpu().tolist() == [-1, -1] and int(s.refs.sum()) == 0
+    s.reserve([20, 0])
+    G.gpt2_prefill_paged(s.cd, s.mw, s.cache, _i32(prompt.tolist()), 20, s.next, s.logits, 1000, s.ws, s.ws.numel())
+    assert G.gpt2_last_error()[0] == RANGE
+    assert s.lens.cpu().tolist() == [20, 0] and int(s.next[1]) == -1
+    assert _rel(s.got()[0], _ref_last(s, list(prompt[0]))) < 1e-2
