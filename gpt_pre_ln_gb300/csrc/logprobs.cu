@@ -183,7 +183,7 @@ __device__ void top_equal(const T* z, int V, int top_n, int at, float value, flo
 // and nothing of row r + 2 but its maxima is written before that.
 //
 // Measured at 8192 x 50257 in bf16 with 20 alternatives: 153 us, 5.4 TB/s (three
-// passes over memory and L2 took 283).  Some 16 000 warp instructions a row
+// passes over memory and L2 took 283).  16 200 warp instructions a row
 // keep two thirds of the issue slots busy, and a warp's place lies empty from
 // the end of one copy to the end of the sums; two and three smaller places for
 // each warp fill that gap but take more instructions, chunk by chunk (203 and
