@@ -513,9 +513,11 @@ int gpt2_pages_fork(const gpt2_paged_cache *cache, const int32_t *parents, const
  * become -1 and their pages lose a reference.  With keep_first = keep_last = 0
  * the whole sequence goes and lens becomes -1.  Otherwise pages that hold one
  * of the first keep_first or of the last keep_last positions stay, as do pages
- * that reach behind lens, and lens does not change: with keep_first = sinks
- * and keep_last = window - 1 nothing that a later query under that window sees
- * is given back.  0 <= n <= n_seq. */
+ * that reach behind lens, and lens does not change.  Behind a sliding window
+ * call it with keep_first = sinks and keep_last = max(window - 1, 1): nothing
+ * that a later query under that window sees is given back.  (A window of 1
+ * sees the new token alone, so that no cached position has to stay, but 0
+ * and 0 would end the sequence.)  0 <= n <= n_seq. */
 int gpt2_pages_free(const gpt2_paged_cache *cache, const int32_t *seqs, int n, int keep_first, int keep_last,
                     gpt2_stream_t stream);
 
