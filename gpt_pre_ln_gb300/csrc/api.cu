@@ -1605,7 +1605,8 @@ int gpt2_token_logprobs(const void* logits, int64_t ld, gpt2_dtype logits_t, int
                         float* top_logprobs, gpt2_stream_t stream) {
   if (!valid_dtype(logits_t)) return GPT2_ERR_ARG;
   if (M < 0 || V <= 0 || ld < V || top_n < 0 || top_n > V) return GPT2_ERR_ARG;
-  if (M >= (1ll << 30) || V > INT_MAX - 16 || top_n > kMaxTopN || (ld * static_cast<int64_t>(esize(logits_t))) % 16 != 0) return GPT2_ERR_UNSUPPORTED;
+  if (M >= (1ll << 30) || V > kMaxScoreVocab || top_n > kMaxTopN) return GPT2_ERR_UNSUPPORTED;
+  if ((ld * static_cast<int64_t>(esize(logits_t))) % 16 != 0) return GPT2_ERR_UNSUPPORTED;
   if ((tokens == nullptr) != (logprob == nullptr)) return GPT2_ERR_ARG;
   if (top_n == 0) top_ids = nullptr, top_logprobs = nullptr;
   if (top_n > 0 && (!top_ids || !top_logprobs)) return GPT2_ERR_ARG;

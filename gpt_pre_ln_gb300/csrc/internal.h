@@ -193,6 +193,11 @@ cudaError_t launch_pages_write(const gpt2_paged_cache* c, int layer, const void*
 
 // Scores from stored logits (logprobs.cu; gpt2_token_logprobs in gpt2gb.h).
 constexpr int kMaxTopN = 32;
+// A row whose likely tokens stand together in a few threads' parts is ranked by
+// one warp in top_n + 1 passes over it, 95 ns a logit for 32 alternatives (fp32),
+// and the row after next waits for that: 0.2 s at this vocabulary, a tenth of
+// what a wait may take.
+constexpr int kMaxScoreVocab = 1 << 21;
 cudaError_t launch_token_logprobs(const void* logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V,
                                   const int32_t* tokens, float* logprob, float* entropy, float* lse, int top_n,
                                   int32_t* top_ids, float* top_logprobs, cudaStream_t s);

@@ -601,8 +601,8 @@ int gpt2_decode_step_paged(const gpt2_dims *dims, const gpt2_model_weights *w, c
                            int64_t ld, void *ws, size_t ws_bytes, gpt2_stream_t stream);
 
 /* Scores of tokens from stored logits z [M, ld] of type logits_t (any of the
- * three; M < 2^30, V <= ld, ld times the element size a multiple of 16 bytes), as
- * gpt2_forward_logits or a decode step leaves them.  Per row, each of the
+ * three; M < 2^30, V <= ld, V <= 2^21, ld times the element size a multiple of
+ * 16 bytes), as gpt2_forward_logits or a decode step leaves them.  Per row, each of the
  * outputs that is given (at least one):
  *   lse[m] = log sum_v e^(z_v); logprob[m] = z_t - lse with t = tokens[m]
  *   (int32 [M] device; an id outside [0, V) gives NaN and GPT2_ERR_RANGE);
