@@ -384,7 +384,7 @@ __device__ __forceinline__ void put_row(const ScoreArgs<T>& a, int row, const Su
 }
 
 // Short rows: one warp per row, a chunk of four vectors a lane in registers and
-// the next on its way.  Each lane keeps its own maximum and sums; the bound
+// the next on its way.  Each lane keeps sums against a maximum of its own; the bound
 // comes from 64 groups' maxima (two a lane) by bisection, and what reaches it
 // is looked at again.  A row's end costs the CTA of the kernel below about 3.7
 // us: 8192 rows in bf16 take it 110 us at 8000 logits a row (here 68), 122 at
@@ -394,19 +394,30 @@ constexpr int kShortBytes = 40 * 1024;  // of a row, when there are more rows th
 constexpr int kShortAlways = 8 * 1024;  // under which that kernel's groups have no vector each
 constexpr int kShortWarps = 8;
 constexpr int kShortKeep = 512;
+// Adds four vectors to this lane's sums, which are against a reference r.m that
+// the largest logit so far passes by less than 1 (-inf: nothing but -inf or NaN
+// so far).  A chunk's sums begin at 0, so that behind a large term the small ones
+// add up first: a lane's terms pass through kN * 2 + 1 additions of their chunk
+// and one of each chunk, V / 1024 (16 bits) or V / 512 (fp32) of them, where one
+// running sum would be V / 64 additions long and lose what is below half its last
+// place each time.  When the reference moves, what is there shrinks by e at
+// least, and the exponentials' errors with it: all those moves together cost less
+// than two.
 template <typename T>
 __device__ __forceinline__ void add_vectors(const uint4 (&x)[4], Sums& r) {
   using R = Row16<T>;
   constexpr int kN = R::kN;
   constexpr float kL2e = 1.4426950408889634f;
-  const float mc = R::reduce(R::vmax(R::vmax(x[0], x[1]), R::vmax(x[2], x[3])));
-  const float m = fmaxf(r.m, mc);
-  if (r.m == -INFINITY)
-    r.m = m;  // nothing but -inf (or NaN) so far: the sums stay
-  else
-    raise(r, m);
-  const float ref = m == -INFINITY ? 0.f : m;
-  if (__any_sync(0xffffffffu, m > 1e37f || (m < -6e4f && m > -INFINITY))) {
+  const float m = R::reduce(R::vmax(R::vmax(x[0], x[1]), R::vmax(x[2], x[3])));
+  if (m > r.m + 1.f) {
+    if (r.m == -INFINITY)
+      r.m = m;  // the sums stay
+    else
+      raise(r, m);
+  }
+  const float ref = r.m == -INFINITY ? 0.f : r.m;
+  float2 sum = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
+  if (__any_sync(0xffffffffu, r.m > 1e37f || (r.m < -6e4f && r.m > -INFINITY))) {
     // differences may overflow, or -inf, raised, not be far enough below
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -415,28 +426,28 @@ __device__ __forceinline__ void add_vectors(const uint4 (&x)[4], Sums& r) {
 #pragma unroll
       for (int i = 0; i < kN; ++i) {
         const float d = e[i] - ref, p = ex2_approx(d * kL2e);
-        r.sum += p;
-        r.dot = fmaf(p, fmaxf(d, -256.f), r.dot);
+        float &to = i & 1 ? sum.y : sum.x, &dots = i & 1 ? dot.y : dot.x;
+        to += p;
+        dots = fmaf(p, fmaxf(d, -256.f), dots);
       }
     }
-    return;
-  }
-  const float2 neg = make_float2(-ref, -ref), l2e = make_float2(kL2e, kL2e);
-  float2 sum = make_float2(r.sum, 0.f), dot = make_float2(r.dot, 0.f);
+  } else {
+    const float2 neg = make_float2(-ref, -ref), l2e = make_float2(kL2e, kL2e);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float2 v[kN / 2];
-    R::pairs(x[k], v);
+    for (int k = 0; k < 4; ++k) {
+      float2 v[kN / 2];
+      R::pairs(x[k], v);
 #pragma unroll
-    for (int i = 0; i < kN / 2; ++i) {
-      const float2 d = add_f32x2(v[i], neg), t = mul_f32x2(d, l2e);
-      const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
-      sum = add_f32x2(sum, e);
-      dot = fma_f32x2(e, d, dot);
+      for (int i = 0; i < kN / 2; ++i) {
+        const float2 d = add_f32x2(v[i], neg), t = mul_f32x2(d, l2e);
+        const float2 e = make_float2(ex2_approx(t.x), ex2_approx(t.y));
+        sum = add_f32x2(sum, e);
+        dot = fma_f32x2(e, d, dot);
+      }
     }
   }
-  r.sum = sum.x + sum.y;
-  r.dot = dot.x + dot.y;
+  r.sum += sum.x + sum.y;
+  r.dot += dot.x + dot.y;
 }
 
 template <typename T>
@@ -478,7 +489,8 @@ __global__ void __launch_bounds__(kShortWarps * 32, 4) score_short(const ScoreAr
     const bool tok_ok = tok >= 0 && tok < a.V;
     if (!tok_ok && lane == 0) record_error(a.err, kErrRange, kSiteScoreToken);
     const float z_tok = tok_ok ? to_f32<T>(z[tok]) : NAN;
-    float m = r.m;
+    const float f0 = R::reduce(g0), f1 = R::reduce(g1);  // the groups' maxima
+    float m = fmaxf(f0, f1);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     if (r.m > -INFINITY) raise(r, m);
@@ -491,7 +503,6 @@ __global__ void __launch_bounds__(kShortWarps * 32, 4) score_short(const ScoreAr
     float bound = -INFINITY;
     if (a.top_n > 0) {
       // a value that at least top_n groups reach, and few more than that
-      const float f0 = R::reduce(g0), f1 = R::reduce(g1);
       const unsigned k0 = key_of(f0), k1 = key_of(f1);
       unsigned low = key_of(-INFINITY), high = key_of(m) + 1;  // low: reached by top_n groups, high: by none
       for (int i = 0; i < 32 && high - low > 1; ++i) {
