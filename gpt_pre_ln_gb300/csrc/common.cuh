@@ -43,10 +43,10 @@ enum ErrSite : unsigned {
   kSitePagedRow = 22,     // a sequence out of range, or named twice
   kSitePagedFull = 23,    // too few free pages
   kSiteScoreToken = 24,
-  kSitePagedLoad = 27,
-  kSitePagedShared = 28,  // a write to a page that several sequences share
   kSiteScoreLoad = 25,
   kSiteScoreJoin = 26,
+  kSitePagedLoad = 27,
+  kSitePagedShared = 28,  // a write to a page that several sequences share
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per wait

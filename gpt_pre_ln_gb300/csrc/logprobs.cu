@@ -190,7 +190,10 @@ __device__ void top_equal(const T* z, int V, int top_n, int at, float value, flo
 // 229 us).  Without the second look at the candidates it would be 131.  Likely
 // tokens that stand together are one warp's to look at again: logits that fall
 // by 1e-3 an id take 300 us.  Rows dealt out to the warps in pieces of 512
-// bytes took 195 for those, and 169 where nothing falls.
+// bytes took 195 for those, and 169 where nothing falls.  Rows in which fewer
+// than top_n lanes hold anything but -inf have a bound of -inf, which all lanes
+// reach; they go the way of ties, by one warp over the row once more: 3.3 ms
+// with all but 10 logits of a row masked (0.16 ms for 5 alternatives of those).
 constexpr int kWarps = 16;
 constexpr int kThreads = kWarps * 32;
 constexpr int kScoreThreads = kThreads + 64;  // and two warps that see to the rows' ends
@@ -389,7 +392,8 @@ __device__ __forceinline__ void put_row(const ScoreArgs<T>& a, int row, const Su
 // is looked at again.  A row's end costs the CTA of the kernel below about 3.7
 // us: 8192 rows in bf16 take it 110 us at 8000 logits a row (here 68), 122 at
 // 14000 (here 93), 143 at 30000 (here 186).  A few rows of 8000 are better off
-// with a CTA each (64 rows: 7.9 us, here 19.7).
+// with a CTA each (64 rows: 7.9 us, here 19.7).  Bound by issue: 4880 warp
+// instructions a row of 8000, 1540 a row of 1000, of which some 1060 for its end.
 constexpr int kShortBytes = 40 * 1024;  // of a row, when there are more rows than the other kernel holds
 constexpr int kShortAlways = 8 * 1024;  // under which that kernel's groups have no vector each
 constexpr int kShortWarps = 8;

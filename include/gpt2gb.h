@@ -463,9 +463,10 @@ int gpt2_decode_step(const gpt2_dims *dims, const gpt2_model_weights *w, void *k
  * smaller n_seq, is a cache of those slots alone.  Calls on one cache belong
  * on one stream, or in an order that events give: they read and write its
  * state.
- *   page_size a multiple of 16 and at most 4096; n_seq at most 1024; max_pages
- *   is the length of a table row, with max_pages * page_size < 2^31.  16-bit
- *   types only (GPT2_ERR_UNSUPPORTED for GPT2_F32). */
+ *   page_size a multiple of 16 and at most 4096; n_seq and n_kv_head at most
+ *   1024, n_layer at most 4096; max_pages is the length of a table row, with
+ *   max_pages * page_size and n_seq * max_pages < 2^31.  16-bit types only.
+ *   What is beyond these gets GPT2_ERR_UNSUPPORTED. */
 typedef struct {
   void *pages;
   int32_t *refs;  /* [n_pages] */
@@ -479,7 +480,8 @@ typedef struct {
  * are not looked at). */
 size_t gpt2_paged_cache_bytes(const gpt2_paged_cache *cache);
 
-/* Workspace of gpt2_pages_reserve and gpt2_pages_compact. */
+/* Workspace of gpt2_pages_reserve and gpt2_pages_compact: 256-byte aligned, one
+ * for each of the calls (on different caches) that may run at the same time. */
 size_t gpt2_pages_workspace_bytes(const gpt2_paged_cache *cache);
 
 /* Makes room for n_new[b] more positions of every sequence b (int32 [n_seq]
@@ -562,8 +564,9 @@ size_t gpt2_attention_paged_workspace_bytes(const gpt2_paged_cache *cache, int n
  *   v_new may point into one c_attn output); lse: NULL or fp32 [n_seq, n_head]:
  *   log2 sum_{p visible} 2^(score_scale log2(e) q . K), as
  *   gpt2_attention_causal_lse.  out must not overlap q, k_new or v_new.
- *   n_head a multiple of n_kv_head; n_pages * n_layer * 2 * n_kv_head *
- *   page_size < 2^31.
+ *   n_head a multiple of n_kv_head and at most 1024; n_pages * n_layer * 2 *
+ *   n_kv_head * page_size < 2^31; n_seq * n_kv_head * ceil(n_head / n_kv_head /
+ *   16) * max_pages * page_size < 2^34.
  * Scores, softmax statistics and sums are fp32, and the probabilities enter
  * the product with V as the sum of two 16-bit numbers.  A sequence without a
  * visible position gets zeros and an lse of -inf; rows of slots with lens[b] < 0 are left as they
@@ -590,7 +593,8 @@ int gpt2_prefill_paged(const gpt2_dims *dims, const gpt2_model_weights *w, const
 /* gpt2_decode_step over a paged cache (n_kv_head = n_head): position lens[b]
  * of each sequence, its page reserved before (gpt2_pages_reserve with n_new =
  * 1), attention as gpt2_attention_paged with `window` and `sinks`; lens[b] +=
- * 1.  Slots with lens[b] = -1 are skipped: their next_tokens stay, and their
+ * 1.  The model's positions are absolute and end at dims->n_pos, whatever the
+ * window is.  Slots with lens[b] = -1 are skipped: their next_tokens stay, and their
  * row of logits_opt is not defined.  The same holds, with GPT2_ERR_RANGE
  * recorded, for a sequence whose position or token is out of range or whose
  * position has no page of its own (the pool had run short): it may take the
