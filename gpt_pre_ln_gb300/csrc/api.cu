@@ -410,6 +410,10 @@ int block_body(const gpt2_dims* d, const gpt2_block_weights* w, int layer, const
   return GPT2_OK;
 }
 
+// An array of 4-byte elements on its boundary; null passes the first.
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+bool given4(const void* p) { return p && aligned4(p); }
+
 // `data`: also the pointers that every call on the cache needs.
 int check_paged(const gpt2_paged_cache* c, bool data) {
   if (!c) return GPT2_ERR_ARG;
@@ -426,7 +430,7 @@ int check_paged(const gpt2_paged_cache* c, bool data) {
   if (!data) return GPT2_OK;
   const void* ps[4] = {c->pages, c->refs, c->table, c->lens};
   for (const void* p : ps)
-    if (!p || (reinterpret_cast<uintptr_t>(p) & 3u)) return GPT2_ERR_ARG;
+    if (!given4(p)) return GPT2_ERR_ARG;
   return aligned16(c->pages) ? GPT2_OK : GPT2_ERR_ARG;
 }
 
@@ -1449,7 +1453,7 @@ int gpt2_pages_reserve(const gpt2_paged_cache* cache, const int32_t* n_new, void
                        gpt2_stream_t stream) {
   GPT2_TRY(check_paged(cache, true));
   if (cache->n_seq == 0) return GPT2_OK;
-  if (!n_new) return GPT2_ERR_ARG;
+  if (!given4(n_new)) return GPT2_ERR_ARG;
   GPT2_TRY(check_ws(ws, ws_bytes, pages_workspace(cache)));
   ProfScope prof("pages_reserve", 0.0, 0.0, cs(stream));
   return cuda_status(launch_pages_reserve(cache, n_new, ws, cs(stream)));
@@ -1460,7 +1464,7 @@ int gpt2_pages_fork(const gpt2_paged_cache* cache, const int32_t* parents, const
   GPT2_TRY(check_paged(cache, true));
   if (n < 0 || n > cache->n_seq) return GPT2_ERR_ARG;
   if (n == 0) return GPT2_OK;
-  if (!parents || !children) return GPT2_ERR_ARG;
+  if (!given4(parents) || !given4(children)) return GPT2_ERR_ARG;
   ProfScope prof("pages_fork", 0.0, 0.0, cs(stream));
   return cuda_status(launch_pages_fork(cache, parents, children, n, cs(stream)));
 }
@@ -1470,7 +1474,7 @@ int gpt2_pages_free(const gpt2_paged_cache* cache, const int32_t* seqs, int n, i
   GPT2_TRY(check_paged(cache, true));
   if (n < 0 || n > cache->n_seq || keep_first < 0 || keep_last < 0) return GPT2_ERR_ARG;
   if (n == 0) return GPT2_OK;
-  if (!seqs) return GPT2_ERR_ARG;
+  if (!given4(seqs)) return GPT2_ERR_ARG;
   ProfScope prof("pages_free", 0.0, 0.0, cs(stream));
   return cuda_status(launch_pages_free(cache, seqs, n, keep_first, keep_last, cs(stream)));
 }
@@ -1478,7 +1482,7 @@ int gpt2_pages_free(const gpt2_paged_cache* cache, const int32_t* seqs, int n, i
 int gpt2_pages_compact(const gpt2_paged_cache* cache, int32_t* n_used, void* ws, size_t ws_bytes,
                        gpt2_stream_t stream) {
   GPT2_TRY(check_paged(cache, true));
-  if (!n_used) return GPT2_ERR_ARG;
+  if (!given4(n_used)) return GPT2_ERR_ARG;
   GPT2_TRY(check_ws(ws, ws_bytes, pages_workspace(cache)));
   ProfScope prof("pages_compact", 0.0, 0.0, cs(stream));
   return cuda_status(launch_pages_compact(cache, n_used, ws, cs(stream)));
@@ -1491,7 +1495,7 @@ int gpt2_pages_write(const gpt2_paged_cache* cache, int layer, const void* k, co
   if (static_cast<int64_t>(cache->n_seq) * T > INT_MAX) return GPT2_ERR_ARG;
   if (ldkv % 8 != 0) return GPT2_ERR_UNSUPPORTED;
   if (cache->n_seq == 0 || T == 0) return GPT2_OK;
-  if (!k || !v || !aligned16(k) || !aligned16(v)) return GPT2_ERR_ARG;
+  if (!k || !v || !aligned16(k) || !aligned16(v) || !aligned4(n_new)) return GPT2_ERR_ARG;
   const double rows = static_cast<double>(cache->n_seq) * T;
   ProfScope prof("pages_write", 0.0, rows * cache->n_kv_head * 512.0, cs(stream));
   return cuda_status(launch_pages_write(cache, layer, k, v, ldkv, T, n_new, cs(stream)));
@@ -1516,7 +1520,7 @@ int gpt2_attention_paged(const gpt2_paged_cache* cache, int layer, const void* q
   if (!attention_paged_fits(cache, n_head)) return GPT2_ERR_UNSUPPORTED;
   if (cache->n_seq == 0) return GPT2_OK;
   if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new)) return GPT2_ERR_ARG;
-  if (reinterpret_cast<uintptr_t>(lse) & 3u) return GPT2_ERR_ARG;
+  if (!aligned4(lse)) return GPT2_ERR_ARG;
   GPT2_TRY(check_ws(ws, ws_bytes, attention_paged_workspace(cache, n_head)));
   // the lengths live on the device: the work of this kernel is left to the
   // caller, who knows them
@@ -1540,7 +1544,7 @@ int gpt2_prefill_paged(const gpt2_dims* dims, const gpt2_model_weights* w, const
   if (T < 0 || static_cast<int64_t>(B) * T > INT_MAX) return GPT2_ERR_ARG;
   if (B == 0) return GPT2_OK;
   if (T < 1 || T > dims->n_pos || T > cache->max_pages * cache->page_size) return GPT2_ERR_ARG;
-  if (!tokens || !next_tokens) return GPT2_ERR_ARG;
+  if (!given4(tokens) || !given4(next_tokens)) return GPT2_ERR_ARG;
   if (logits_opt && (ld < dims->vocab || !aligned16(logits_opt))) return GPT2_ERR_ARG;
   if (logits_opt && ld % 4 != 0) return GPT2_ERR_UNSUPPORTED;
   GPT2_TRY(check_ws(ws, ws_bytes, gpt2_prefill_paged_workspace_bytes(dims, cache, T)));
@@ -1564,7 +1568,7 @@ int gpt2_decode_step_paged(const gpt2_dims* dims, const gpt2_model_weights* w, c
   if (window < 0 || sinks < 0) return GPT2_ERR_ARG;
   if (!attention_paged_fits(cache, dims->n_head)) return GPT2_ERR_UNSUPPORTED;
   if (B == 0) return GPT2_OK;
-  if (!tokens || !next_tokens) return GPT2_ERR_ARG;
+  if (!given4(tokens) || !given4(next_tokens)) return GPT2_ERR_ARG;
   if (logits_opt && (ld < dims->vocab || !aligned16(logits_opt))) return GPT2_ERR_ARG;
   if (logits_opt && ld % 4 != 0) return GPT2_ERR_UNSUPPORTED;
   GPT2_TRY(check_ws(ws, ws_bytes, gpt2_decode_step_paged_workspace_bytes(dims, cache)));
@@ -1611,6 +1615,9 @@ int gpt2_token_logprobs(const void* logits, int64_t ld, gpt2_dtype logits_t, int
   if (top_n == 0) top_ids = nullptr, top_logprobs = nullptr;
   if (top_n > 0 && (!top_ids || !top_logprobs)) return GPT2_ERR_ARG;
   if (!logprob && !entropy && !lse && top_n == 0) return GPT2_ERR_ARG;
+  const void* ps[6] = {tokens, logprob, entropy, lse, top_ids, top_logprobs};
+  for (const void* p : ps)
+    if (!aligned4(p)) return GPT2_ERR_ARG;
   if (M == 0) return GPT2_OK;
   if (!logits || !aligned16(logits)) return GPT2_ERR_ARG;
   ProfScope prof("token_logprobs", 6.0 * M * V, static_cast<double>(M) * V * esize(logits_t), cs(stream));

@@ -466,7 +466,9 @@ int gpt2_decode_step(const gpt2_dims *dims, const gpt2_model_weights *w, void *k
  *   page_size a multiple of 16 and at most 4096; n_seq and n_kv_head at most
  *   1024, n_layer at most 4096; max_pages is the length of a table row, with
  *   max_pages * page_size and n_seq * max_pages < 2^31.  16-bit types only.
- *   What is beyond these gets GPT2_ERR_UNSUPPORTED. */
+ *   What is beyond these gets GPT2_ERR_UNSUPPORTED.  int32 and fp32 arrays of
+ *   these calls stand on 4-byte boundaries, pages, q, k, v and out on 16
+ *   (GPT2_ERR_ARG). */
 typedef struct {
   void *pages;
   int32_t *refs;  /* [n_pages] */
@@ -614,7 +616,8 @@ int gpt2_decode_step_paged(const gpt2_dims *dims, const gpt2_model_weights *w, c
  *   nothing); top_ids, top_logprobs [M, top_n]: the top_n most likely tokens
  *   and their log probabilities, larger first, lowest id first on ties (a NaN
  *   ranks as -inf).
- * All outputs are fp32 (ids int32); sums in fp32 in a fixed order.  tokens and
+ * All outputs are fp32 (ids int32), on 4-byte boundaries as tokens are, logits
+ * on 16; sums in fp32 in a fixed order.  tokens and
  * logprob go together, as do top_ids and top_logprobs (top_n = 0 without
  * them).  0 <= top_n <= min(32, V).  A row with a NaN or +inf, or with
  * nothing but -inf, has no distribution: its sums and log probabilities are
