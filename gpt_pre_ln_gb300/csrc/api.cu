@@ -427,6 +427,9 @@ int check_paged(const gpt2_paged_cache* c, bool data) {
   if (static_cast<int64_t>(c->max_pages) * c->page_size > INT_MAX ||
       static_cast<int64_t>(c->n_seq) * c->max_pages > INT_MAX)
     return GPT2_ERR_UNSUPPORTED;
+  // (the product of all of them may pass 64 bits; 256 bytes a position, head and layer)
+  if (static_cast<double>(c->n_pages) * c->n_layer * c->n_kv_head * c->page_size >= 72057594037927936.0 /* 2^56 */)
+    return GPT2_ERR_UNSUPPORTED;
   if (!data) return GPT2_OK;
   const void* ps[4] = {c->pages, c->refs, c->table, c->lens};
   for (const void* p : ps)

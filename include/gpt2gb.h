@@ -465,7 +465,8 @@ int gpt2_decode_step(const gpt2_dims *dims, const gpt2_model_weights *w, void *k
  * state.
  *   page_size a multiple of 16 and at most 4096; n_seq and n_kv_head at most
  *   1024, n_layer at most 4096; max_pages is the length of a table row, with
- *   max_pages * page_size and n_seq * max_pages < 2^31.  16-bit types only.
+ *   max_pages * page_size and n_seq * max_pages < 2^31; the pool smaller than
+ *   2^64 bytes.  16-bit types only.
  *   What is beyond these gets GPT2_ERR_UNSUPPORTED.  int32 and fp32 arrays of
  *   these calls stand on 4-byte boundaries, pages, q, k, v and out on 16
  *   (GPT2_ERR_ARG). */

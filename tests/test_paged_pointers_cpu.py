@@ -1,6 +1,7 @@
 """Pointers that the paged-cache and scoring calls may not follow are refused
 on the host: an int32 or fp32 array off its 4-byte boundary is a misaligned
-access on the GPU.  Nothing is launched (no GPU needed)."""
+access on the GPU.  So are pools whose bytes do not fit 64 bits.  Nothing is
+launched (no GPU needed)."""
 import ctypes
 
 import pytest
@@ -49,3 +50,11 @@ def test_scores(L, which):
     p[which] = ODD
     assert L.gpt2_token_logprobs(256, 1000, G.F32, 4, 1000, p["tok"], p["lp"], p["ent"], p["lse"], 5, p["ids"],
                                  p["tlp"], None) == ARG
+
+
+@pytest.mark.parametrize("n_pages, fits", [(1 << 20, True), (1 << 22, False), (2 ** 31 - 1, False)])
+def test_pools_beyond_64_bits(L, n_pages, fits):
+    """4096 layers of 1024 heads, pages of 4096: 2^42 bytes each."""
+    c = G.PagedCache(256, 256, 256, 256, n_pages, 4096, 4096, 1024, 4, 8, G.BF16)
+    assert G.gpt2_paged_cache_bytes(c) == (n_pages << 42 if fits else 0)
+    assert L.gpt2_pages_fork(ctypes.byref(c), None, None, 0, None) == (0 if fits else 2)
