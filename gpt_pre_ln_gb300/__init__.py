@@ -27,7 +27,10 @@ __all__ = [
     "gpt2_paged_cache_bytes", "gpt2_pages_workspace_bytes", "gpt2_pages_reserve", "gpt2_pages_fork",
     "gpt2_pages_free", "gpt2_pages_compact", "gpt2_pages_write", "gpt2_attention_paged_workspace_bytes",
     "gpt2_attention_paged", "gpt2_prefill_paged_workspace_bytes", "gpt2_prefill_paged",
-    "gpt2_decode_step_paged_workspace_bytes", "gpt2_decode_step_paged", "gpt2_token_logprobs", "gpt2_profile_begin",
+    "gpt2_decode_step_paged_workspace_bytes", "gpt2_decode_step_paged", "gpt2_token_logprobs",
+    "gpt2_attention_paged_draft_workspace_bytes", "gpt2_attention_paged_draft",
+    "gpt2_draft_step_paged_workspace_bytes", "gpt2_draft_step_paged", "gpt2_draft_accept", "gpt2_sample_tokens",
+    "gpt2_profile_begin",
     "gpt2_profile_end", "gpt2_profile_read", "ProfileEntry",
 ]
 
@@ -147,6 +150,14 @@ _SIGS = {
     "gpt2_decode_step_paged": (_I32, [ctypes.POINTER(Dims), ctypes.POINTER(ModelWeights), ctypes.POINTER(PagedCache),
                                       _I32, _I32, _VP, _VP, _VP, _I64, _VP, _SZ, _VP]),
     "gpt2_token_logprobs": (_I32, [_VP, _I64, _I32, _I64, _I32, _VP, _VP, _VP, _VP, _I32, _VP, _VP, _VP]),
+    "gpt2_attention_paged_draft_workspace_bytes": (_SZ, [ctypes.POINTER(PagedCache), _I32, _I32]),
+    "gpt2_attention_paged_draft": (_I32, [ctypes.POINTER(PagedCache), _I32, _VP, _I64, _VP, _VP, _I64, _VP, _I64, _VP,
+                                          _I32, _VP, _VP, _I32, _F, _I32, _I32, _VP, _SZ, _VP]),
+    "gpt2_draft_step_paged_workspace_bytes": (_SZ, [ctypes.POINTER(Dims), ctypes.POINTER(PagedCache), _I32]),
+    "gpt2_draft_step_paged": (_I32, [ctypes.POINTER(Dims), ctypes.POINTER(ModelWeights), ctypes.POINTER(PagedCache),
+                                     _I32, _VP, _VP, _VP, _I32, _I32, _VP, _I64, _I32, _VP, _SZ, _VP]),
+    "gpt2_draft_accept": (_I32, [ctypes.POINTER(PagedCache), _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "gpt2_sample_tokens": (_I32, [_VP, _I64, _I32, _I64, _I32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
     "gpt2_mlp_noalloc_max_scratch_bytes": (_SZ, []),
     "gpt2_mlp_noalloc": (_I32, [_VP, _VP, _VP, _VP, _VP, _VP, _VP, _I64, _I32, _I32, _I32, _VP]),
     "gpt2_profile_begin": (_I32, [_I32]),
@@ -438,6 +449,41 @@ def gpt2_token_logprobs(logits, ld, logits_t, M, V, tokens, logprob, entropy, ls
     _check(lib().gpt2_token_logprobs(_ptr(logits), ld, logits_t, M, V, _ptr(tokens), _ptr(logprob), _ptr(entropy),
                                      _ptr(lse), top_n, _ptr(top_ids), _ptr(top_logprobs), _stream(stream)),
            "gpt2_token_logprobs")
+
+
+def gpt2_attention_paged_draft_workspace_bytes(cache: PagedCache, T: int, n_head: int) -> int:
+    return lib().gpt2_attention_paged_draft_workspace_bytes(ctypes.byref(cache), T, n_head)
+
+
+def gpt2_attention_paged_draft(cache: PagedCache, layer, q, ldq, k, v, ldkv, out, ldo, lse, T, parents, n_draft,
+                               n_head, score_scale, window, sinks, ws, ws_bytes, stream=None):
+    _check(lib().gpt2_attention_paged_draft(ctypes.byref(cache), layer, _ptr(q), ldq, _ptr(k), _ptr(v), ldkv,
+                                            _ptr(out), ldo, _ptr(lse), T, _ptr(parents), _ptr(n_draft), n_head,
+                                            score_scale, window, sinks, _ptr(ws), ws_bytes, _stream(stream)),
+           "gpt2_attention_paged_draft")
+
+
+def gpt2_draft_step_paged_workspace_bytes(dims: Dims, cache: PagedCache, T: int) -> int:
+    return lib().gpt2_draft_step_paged_workspace_bytes(ctypes.byref(dims), ctypes.byref(cache), T)
+
+
+def gpt2_draft_step_paged(dims: Dims, w: ModelWeights, cache: PagedCache, T, tokens, parents, n_draft, window, sinks,
+                          logits, ld, logits_t, ws, ws_bytes, stream=None):
+    _check(lib().gpt2_draft_step_paged(ctypes.byref(dims), ctypes.byref(w), ctypes.byref(cache), T, _ptr(tokens),
+                                       _ptr(parents), _ptr(n_draft), window, sinks, _ptr(logits), ld, logits_t,
+                                       _ptr(ws), ws_bytes, _stream(stream)), "gpt2_draft_step_paged")
+
+
+def gpt2_draft_accept(cache: PagedCache, T, tokens, parents, n_draft, chosen, path, n_kept, next_tokens, stream=None):
+    _check(lib().gpt2_draft_accept(ctypes.byref(cache), T, _ptr(tokens), _ptr(parents), _ptr(n_draft), _ptr(chosen),
+                                   _ptr(path), _ptr(n_kept), _ptr(next_tokens), _stream(stream)), "gpt2_draft_accept")
+
+
+def gpt2_sample_tokens(logits, ld, logits_t, M, V, temperature, top_k, top_p, min_p, uniform, tokens, logprob=None,
+                       stream=None):
+    _check(lib().gpt2_sample_tokens(_ptr(logits), ld, logits_t, M, V, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                                    _ptr(min_p), _ptr(uniform), _ptr(tokens), _ptr(logprob), _stream(stream)),
+           "gpt2_sample_tokens")
 
 
 def gpt2_profile_begin(max_launches: int):

@@ -1607,6 +1607,131 @@ int gpt2_decode_step_paged(const gpt2_dims* dims, const gpt2_model_weights* w, c
   });
 }
 
+size_t gpt2_attention_paged_draft_workspace_bytes(const gpt2_paged_cache* cache, int T, int n_head) {
+  if (check_paged(cache, false) != GPT2_OK || n_head <= 0 || n_head > 1024 || n_head % cache->n_kv_head != 0 ||
+      T < 1 || T > kMaxDraft)
+    return 0;
+  return attention_draft_workspace(cache, T, n_head);
+}
+
+int gpt2_attention_paged_draft(const gpt2_paged_cache* cache, int layer, const void* q, int64_t ldq, const void* k,
+                               const void* v, int64_t ldkv, void* out, int64_t ldo, float* lse, int T,
+                               const int32_t* parents, const int32_t* n_draft, int n_head, float score_scale,
+                               int window, int sinks, void* ws, size_t ws_bytes, gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (layer < 0 || layer >= cache->n_layer || n_head <= 0 || window < 0 || sinks < 0 || T < 0) return GPT2_ERR_ARG;
+  if (!std::isfinite(score_scale) || !(score_scale > 0.f)) return GPT2_ERR_ARG;
+  if (n_head % cache->n_kv_head != 0 || n_head > 1024 || T > kMaxDraft) return GPT2_ERR_UNSUPPORTED;
+  if ((k == nullptr) != (v == nullptr)) return GPT2_ERR_ARG;
+  const int64_t width = 64ll * n_head, kv_width = 64ll * cache->n_kv_head;
+  if (ldq < width || ldo < width || (k && ldkv < kv_width)) return GPT2_ERR_ARG;
+  if (ldq % 8 != 0 || ldo % 8 != 0 || (k && ldkv % 8 != 0)) return GPT2_ERR_UNSUPPORTED;
+  if (cache->n_seq == 0 || T == 0) return GPT2_OK;
+  if (!attention_draft_fits(cache, T, n_head)) return GPT2_ERR_UNSUPPORTED;
+  if (!q || !out || !aligned16(q) || !aligned16(out) || !aligned16(k) || !aligned16(v)) return GPT2_ERR_ARG;
+  if (!aligned4(lse) || !aligned4(parents) || !aligned4(n_draft)) return GPT2_ERR_ARG;
+  GPT2_TRY(check_ws(ws, ws_bytes, attention_draft_workspace(cache, T, n_head)));
+  // the lengths live on the device: the work of this kernel is left to the
+  // caller, who knows them
+  ProfScope prof("draft_attn", 0.0, 0.0, cs(stream));
+  return cuda_status(launch_attention_draft(cache, layer, q, ldq, k, v, ldkv, out, ldo, lse, T, parents, n_draft,
+                                            n_head, score_scale, window, sinks, ws, cs(stream)));
+}
+
+int gpt2_draft_accept(const gpt2_paged_cache* cache, int T, const int32_t* tokens, const int32_t* parents,
+                      const int32_t* n_draft, const int32_t* chosen, int32_t* path, int32_t* n_kept,
+                      int32_t* next_tokens, gpt2_stream_t stream) {
+  GPT2_TRY(check_paged(cache, true));
+  if (T < 0) return GPT2_ERR_ARG;
+  if (T > kMaxDraft) return GPT2_ERR_UNSUPPORTED;
+  if (cache->n_seq == 0 || T == 0) return GPT2_OK;
+  if (!given4(tokens) || !given4(chosen) || !given4(path) || !given4(n_kept) || !given4(next_tokens))
+    return GPT2_ERR_ARG;
+  if (!aligned4(parents) || !aligned4(n_draft)) return GPT2_ERR_ARG;
+  ProfScope prof("draft_accept", 0.0, 0.0, cs(stream));
+  return cuda_status(launch_draft_accept(cache, T, tokens, parents, n_draft, chosen, path, n_kept, next_tokens,
+                                         cs(stream)));
+}
+
+size_t gpt2_draft_step_paged_workspace_bytes(const gpt2_dims* dims, const gpt2_paged_cache* cache, int T) {
+  if (check_dims(dims, true) != GPT2_OK || !is16(dims->dtype) || check_paged(cache, false) != GPT2_OK ||
+      dims->n_head % cache->n_kv_head != 0 || dims->n_head > 1024 || T < 1 || T > kMaxDraft)
+    return 0;
+  return acts_bytes(dims, static_cast<int64_t>(cache->n_seq) * T) + attention_draft_workspace(cache, T, dims->n_head);
+}
+
+int gpt2_draft_step_paged(const gpt2_dims* dims, const gpt2_model_weights* w, const gpt2_paged_cache* cache, int T,
+                          const int32_t* tokens, const int32_t* parents, const int32_t* n_draft, int window,
+                          int sinks, void* logits, int64_t ld, gpt2_dtype logits_t, void* ws, size_t ws_bytes,
+                          gpt2_stream_t stream) {
+  GPT2_TRY(check_model(dims, w));
+  if (!is16(dims->dtype)) return GPT2_ERR_UNSUPPORTED;
+  GPT2_TRY(check_paged_model(dims, cache));
+  if (window < 0 || sinks < 0 || T < 0 || !valid_dtype(logits_t) || ld < dims->vocab) return GPT2_ERR_ARG;
+  if (T > kMaxDraft || (logits_t != GPT2_F32 && logits_t != dims->dtype)) return GPT2_ERR_UNSUPPORTED;
+  if (ld * static_cast<int64_t>(esize(logits_t)) % 16 != 0) return GPT2_ERR_UNSUPPORTED;
+  const int B = cache->n_seq;
+  if (B == 0 || T == 0) return GPT2_OK;
+  if (!attention_draft_fits(cache, T, dims->n_head)) return GPT2_ERR_UNSUPPORTED;
+  if (!given4(tokens) || !aligned4(parents) || !aligned4(n_draft)) return GPT2_ERR_ARG;
+  if (!logits || !aligned16(logits)) return GPT2_ERR_ARG;
+  GPT2_TRY(check_ws(ws, ws_bytes, gpt2_draft_step_paged_workspace_bytes(dims, cache, T)));
+  KeyBuilder kb;
+  kb.add(7).dims(dims).model(w, dims->n_layer).paged(cache).add(T).ptr(tokens).ptr(parents).ptr(n_draft).add(window)
+      .add(sinks).ptr(logits).add(ld).add(logits_t).ptr(ws);
+  return run_graphed(kb, cs(stream), [&](cudaStream_t s) -> int {
+    const gpt2_dtype dt = dims->dtype;
+    const int64_t M = static_cast<int64_t>(B) * T;
+    const int D = dims->d_model, F = dims->d_ff, H = dims->n_head;
+    Acts A = carve_acts(ws, dims, M);
+    void* attn_ws = static_cast<char*>(ws) + acts_bytes(dims, M);
+    {
+      ProfScope prof("draft_embed", 0.0, static_cast<double>(M) * D * 8.0, s);
+      GPT2_CUDA(launch_draft_embed(dt, cache, T, tokens, parents, n_draft, w->wte, w->wpe, A.x, D, dims->vocab,
+                                   dims->n_pos, s));
+    }
+    for (int l = 0; l < dims->n_layer; ++l) {
+      const gpt2_block_weights* bw = &w->blocks[l];
+      GPT2_CUDA(layernorm(A.x, bw->ln1_g, bw->ln1_b, A.a, M, D, dims->eps, GPT2_F32, dt, s));
+      GPT2_CUDA(linear(dt, A.a, bw->w_qkv, bw->b_qkv, nullptr, A.qkv, M, 3 * D, D, 3 * D, false, GPT2_EPI_BIAS, dt,
+                       s));
+      {
+        ProfScope prof("draft_attn", 0.0, 0.0, s);
+        const char* q = static_cast<const char*>(A.qkv);
+        GPT2_CUDA(launch_attention_draft(cache, l, q, 3 * D, q + D * 2, q + D * 4, 3 * D, A.o, D, nullptr, T, parents,
+                                         n_draft, H, score_scale(dims, l), window, sinks, attn_ws, s));
+      }
+      GPT2_CUDA(linear(dt, A.o, bw->w_o, bw->b_o, A.x, A.h, M, D, D, D, false, GPT2_EPI_BIAS_RESIDUAL, GPT2_F32, s));
+      GPT2_CUDA(layernorm(A.h, bw->ln2_g, bw->ln2_b, A.a, M, D, dims->eps, GPT2_F32, dt, s));
+      GPT2_CUDA(linear(dt, A.a, bw->w_fc, bw->b_fc, nullptr, A.g, M, F, D, F, false, mlp_epilogue(dims), dt, s));
+      GPT2_CUDA(linear(dt, A.g, bw->w_proj, bw->b_proj, A.h, A.x, M, D, F, D, false, GPT2_EPI_BIAS_RESIDUAL, GPT2_F32,
+                       s));
+    }
+    GPT2_CUDA(layernorm(A.x, w->lnf_g, w->lnf_b, A.a, M, D, dims->eps, GPT2_F32, dt, s));
+    GPT2_CUDA(linear(dt, A.a, w->wte, nullptr, nullptr, logits, M, dims->vocab, D, ld, true, GPT2_EPI_NONE, logits_t,
+                     s));
+    return GPT2_OK;
+  });
+}
+
+int gpt2_sample_tokens(const void* logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V,
+                       const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                       const float* uniform, int32_t* tokens, float* logprob, gpt2_stream_t stream) {
+  if (!valid_dtype(logits_t)) return GPT2_ERR_ARG;
+  if (M < 0 || V <= 0 || ld < V) return GPT2_ERR_ARG;
+  if (M >= (1ll << 30) || V > kMaxScoreVocab) return GPT2_ERR_UNSUPPORTED;
+  if ((ld * static_cast<int64_t>(esize(logits_t))) % 16 != 0) return GPT2_ERR_UNSUPPORTED;
+  const void* ps[5] = {temperature, top_k, top_p, min_p, logprob};
+  for (const void* p : ps)
+    if (!aligned4(p)) return GPT2_ERR_ARG;
+  if (M == 0) return GPT2_OK;
+  if (!given4(uniform) || !given4(tokens)) return GPT2_ERR_ARG;
+  if (!logits || !aligned16(logits)) return GPT2_ERR_ARG;
+  ProfScope prof("sample_tokens", 6.0 * M * V, static_cast<double>(M) * V * esize(logits_t), cs(stream));
+  return cuda_status(launch_sample_tokens(logits, ld, logits_t, M, V, temperature, top_k, top_p, min_p, uniform,
+                                          tokens, logprob, cs(stream)));
+}
+
 int gpt2_token_logprobs(const void* logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V, const int32_t* tokens,
                         float* logprob, float* entropy, float* lse, int top_n, int32_t* top_ids,
                         float* top_logprobs, gpt2_stream_t stream) {

@@ -191,6 +191,30 @@ cudaError_t launch_pages_compact(const gpt2_paged_cache* c, int32_t* n_used, voi
 cudaError_t launch_pages_write(const gpt2_paged_cache* c, int layer, const void* k, const void* v, int64_t ldkv,
                                int T, const int32_t* n_new, cudaStream_t s, bool from_zero = false);
 
+// Drafted tokens over the paged cache (paged_draft.cu, draft.cu): attention of
+// a tree of up to kMaxDraft tokens per sequence, the embedding of such trees
+// (x [n_seq * T, D] = wte + wpe at len + depth, zeros for rows without a token),
+// and the path that stays.
+constexpr int kMaxDraft = 64;
+bool attention_draft_fits(const gpt2_paged_cache* c, int T, int n_head);
+size_t attention_draft_workspace(const gpt2_paged_cache* c, int T, int n_head);
+cudaError_t launch_attention_draft(const gpt2_paged_cache* c, int layer, const void* q, int64_t ldq, const void* k,
+                                   const void* v, int64_t ldkv, void* out, int64_t ldo, float* lse, int T,
+                                   const int32_t* parents, const int32_t* n_draft, int n_head, float score_scale,
+                                   int window, int sinks, void* ws, cudaStream_t s);
+cudaError_t launch_draft_embed(gpt2_dtype dt, const gpt2_paged_cache* c, int T, const int32_t* tokens,
+                               const int32_t* parents, const int32_t* n_draft, const void* wte, const void* wpe,
+                               float* x, int D, int V, int n_pos, cudaStream_t s);
+cudaError_t launch_draft_accept(const gpt2_paged_cache* c, int T, const int32_t* tokens, const int32_t* parents,
+                                const int32_t* n_draft, const int32_t* chosen, int32_t* path, int32_t* n_kept,
+                                int32_t* next_tokens, cudaStream_t s);
+
+// Tokens drawn from stored logits (sample.cu; gpt2_sample_tokens in gpt2gb.h).
+cudaError_t launch_sample_tokens(const void* logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V,
+                                 const float* temperature, const int32_t* top_k, const float* top_p,
+                                 const float* min_p, const float* uniform, int32_t* tokens, float* logprob,
+                                 cudaStream_t s);
+
 // Scores from stored logits (logprobs.cu; gpt2_token_logprobs in gpt2gb.h).
 constexpr int kMaxTopN = 32;
 // A row whose likely tokens stand together in a few threads' parts is ranked by

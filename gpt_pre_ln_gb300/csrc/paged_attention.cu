@@ -24,10 +24,9 @@
 // of 32000 positions in bf16 (524 MB) take 115 us with 16 heads on 1, 170 with 25
 // and 289 with 40 (two and three blocks); of 4000 (66 MB, within L2) 29, 35 and 57.
 #include <algorithm>
-#include <type_traits>
 
-#include "common.cuh"
 #include "internal.h"
+#include "paged.cuh"
 
 namespace gpt2 {
 
@@ -94,33 +93,6 @@ __device__ __forceinline__ Span span_of(const PagedArgs<T16>& a, int b, bool rec
   return s;
 }
 
-template <typename T16>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-  if constexpr (std::is_same<T16, __half>::value)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-  else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// (p rounded, what that lost) in 16 bits, so that their sum carries p to 16
-// bits (bf16) or 22 bits (fp16).  In bf16 that moves 2 of 1000 output elements, those
-// next to a border, to the neighbouring bf16 number (fp32 sums in another order
-// move 0.3); the error against 64 bits stays that of the result's own rounding,
-// 1.7e-3.  A third bf16 part left 0.3 to 1.1 and cost 2.4% under a window at 25 heads.
-template <typename T16>
-__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  hi = Type16<T16>::pack2(x, y);
-  const float2 h = Type16<T16>::unpack2(hi);
-  lo = Type16<T16>::pack2(x - h.x, y - h.y);
-}
-
 // A warp's ring of tiles.
 struct Ring {
   const CUtensorMap* map;
@@ -164,11 +136,6 @@ __device__ __forceinline__ Item<T16> item_of(const PagedArgs<T16>& a, int b, int
   x.v_new = a.k_new ? a.v_new + b * a.ldkv + x.kvh * kHd : nullptr;
   return x;
 }
-
-// fp16 probabilities are carried 2^12 times larger: their smallest step is then
-// 2^-36 of the row's largest and not 2^-24.
-template <typename T16>
-constexpr float kShift = std::is_same<T16, __half>::value ? 12.f : 0.f;
 
 // Attention of an item's query heads over its tiles j0, j0 + step, ... (cnt of
 // them) by one warp.  False if a wait ran out.
@@ -426,19 +393,6 @@ __device__ __forceinline__ void put_piece(const Acc& acc, int heads, float* dst,
     }
     if (j == 0) ml[hh] = make_float2(acc.m[g] - kShift<T16>, acc.l[g]);
   }
-}
-
-// Adds a piece (its 4 values x, its m and l) to (acc, M, L).
-__device__ __forceinline__ void merge(float4& acc, float& M, float& L, const float4& x, const float2& ml) {
-  if (ml.y == 0.f) return;  // nothing in it but scores of -inf
-  const float mn = fmaxf(M, ml.x);
-  const float c0 = M == mn ? 1.f : ex2_approx(M - mn), c1 = ml.x == mn ? 1.f : ex2_approx(ml.x - mn);
-  M = mn;
-  L = L * c0 + ml.y * c1;
-  acc.x = acc.x * c0 + x.x * c1;
-  acc.y = acc.y * c0 + x.y * c1;
-  acc.z = acc.z * c0 + x.z * c1;
-  acc.w = acc.w * c0 + x.w * c1;
 }
 
 template <typename T16>

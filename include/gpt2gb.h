@@ -627,6 +627,120 @@ int gpt2_token_logprobs(const void *logits, int64_t ld, gpt2_dtype logits_t, int
                         float *logprob, float *entropy, float *lse, int top_n, int32_t *top_ids,
                         float *top_logprobs, gpt2_stream_t stream);
 
+/* ---------------------------------------------------------- drafted tokens
+ * One step of speculative decoding over a paged cache: a cheap model or
+ * heuristic drafts tokens, this model looks at all of them at once, and the
+ * path that its own choices confirm stays:
+ *   gpt2_pages_reserve (n_new = drafted tokens of each sequence),
+ *   gpt2_draft_step_paged (or gpt2_attention_paged_draft per layer),
+ *   gpt2_sample_tokens on the n_seq * T rows of logits, gpt2_draft_accept.
+ * Sequence b has n = min(n_draft[b], T) of them (int32 [n_seq] device; NULL:
+ * T), at most 64; rows of sequences with lens[b] < 0, and rows t >= n, are not
+ * looked at, and in the outputs left as they were.  They form a tree: token t
+ * follows token parents[b * T + t], which is < t, or with -1 the cached
+ * positions (int32 [n_seq, T] device; NULL: each token follows the one
+ * before).  A parent outside -1 .. t - 1 counts as -1 and GPT2_ERR_RANGE is
+ * recorded.  The token at depth d (0 without a parent) is at position
+ * lens[b] + d; its K and V stand in the cache where position lens[b] + t
+ * would, until gpt2_draft_accept moves them. */
+
+/* Workspace of gpt2_attention_paged_draft (depends on the current device; 0 if
+ * an argument is out of range). */
+size_t gpt2_attention_paged_draft_workspace_bytes(const gpt2_paged_cache *cache, int T, int n_head);
+
+/* gpt2_attention_paged for drafted tokens (T = 1: one new token):
+ *   out[b, t, h*64 + d] = sum_{p visible to t} softmax_p(score_scale
+ *   q[b, t, h] . K[b, p, g]) V[b, p, g, d],   g = h / (n_head / n_kv_head)
+ * over the lens[b] cached positions, the drafted tokens that t follows,
+ * directly or through others, and itself.  window = 0: all of these are
+ * visible; window > 0: those at a position > lens[b] + depth(t) - window or
+ * < sinks.  Entries of table rows for pages without a place that some token of
+ * the sequence sees are not read.
+ *   q [n_seq * T, n_head * 64] with row stride ldq; k, v (both or neither)
+ *   [n_seq * T, n_kv_head * 64] with row stride ldkv: the drafted tokens' own,
+ *   which are also stored in the cache (their pages must be there and not
+ *   shared, see gpt2_pages_reserve; on a page with refs above 1 they are not
+ *   stored and GPT2_ERR_RANGE is recorded; lens is not changed); without them
+ *   the cache has them already (gpt2_pages_write).  out [n_seq * T, n_head * 64]
+ *   with row stride ldo; lse: NULL or fp32 [n_seq * T, n_head], as
+ *   gpt2_attention_paged.  Types, strides and alignment as there; out must not
+ *   overlap q, k or v.
+ *   1 <= T <= 64 (0 is a no-op); n_head a multiple of n_kv_head and at most
+ *   1024; n_pages * n_layer * 2 * n_kv_head * page_size < 2^31; n_seq *
+ *   n_kv_head * T * (n_head / n_kv_head) / 8 * max_pages * page_size < 2^34.
+ * Numerics as gpt2_attention_paged.  A value that is not finite at a place
+ * that a token does not see changes nothing for it.  A token that sees nothing
+ * but scores of -inf, or no place at all, gets zeros and an lse of -inf.  Places
+ * on a page that the table does not name are left out, and a sequence whose
+ * drafted tokens do not fit its table row is skipped; both record
+ * GPT2_ERR_RANGE.  Results do not depend on timing.  ws:
+ * gpt2_attention_paged_draft_workspace_bytes bytes, 256-byte aligned; calls
+ * that may run at the same time need one each. */
+int gpt2_attention_paged_draft(const gpt2_paged_cache *cache, int layer, const void *q, int64_t ldq, const void *k,
+                               const void *v, int64_t ldkv, void *out, int64_t ldo, float *lse, int T,
+                               const int32_t *parents, const int32_t *n_draft, int n_head, float score_scale,
+                               int window, int sinks, void *ws, size_t ws_bytes, gpt2_stream_t stream);
+
+/* The model over drafted tokens (n_kv_head = n_head): token tokens[b * T + t]
+ * (int32 [n_seq, T] device) at position lens[b] + depth(t), its pages reserved
+ * before; attention as gpt2_attention_paged_draft, K and V stored; logits
+ * [n_seq * T, ld] of every token, of type logits_t (GPT2_F32 or dims->dtype;
+ * ld >= vocab, ld times the element size a multiple of 16 bytes).  lens is not
+ * changed.  Rows without a token are not defined.  Nor are those of a token out of
+ * range or at a position >= n_pos, and of the tokens that follow it
+ * (GPT2_ERR_RANGE is recorded): such a token should not be accepted.
+ *   16-bit paths; ws of gpt2_draft_step_paged_workspace_bytes bytes, 256-byte
+ *   aligned. */
+size_t gpt2_draft_step_paged_workspace_bytes(const gpt2_dims *dims, const gpt2_paged_cache *cache, int T);
+int gpt2_draft_step_paged(const gpt2_dims *dims, const gpt2_model_weights *w, const gpt2_paged_cache *cache, int T,
+                          const int32_t *tokens, const int32_t *parents, const int32_t *n_draft, int window,
+                          int sinks, void *logits, int64_t ld, gpt2_dtype logits_t, void *ws, size_t ws_bytes,
+                          gpt2_stream_t stream);
+
+/* Keeps the drafted tokens that the model's choices confirm.  tokens and
+ * chosen: int32 [n_seq, T] device, the drafted tokens and the one chosen behind
+ * each.  The path starts at token 0 (chosen in the step before, so that it
+ * stays in any case) and goes on to the lowest child u of its end t with
+ * tokens[u] = chosen[t], until there is none.  Then path[b, j] is its j-th
+ * token, -1 behind its end (int32 [n_seq, T]); n_kept[b] its length;
+ * next_tokens[b] the token chosen behind its end (int32 [n_seq] each); in
+ * every layer the K and V of token path[b, j] are at position lens[b] + j; and
+ * lens[b] grows by n_kept[b].  Positions behind the new length are free for
+ * the next step; pages stay reserved.
+ * A sequence that lacks a page of its own for a position that it keeps, or whose
+ * drafted tokens do not fit its table row, keeps its lens and its rows of path
+ * and next_tokens; n_kept[b] is 0 and GPT2_ERR_RANGE is recorded.  Outputs must not overlap inputs.  0 <= T <= 64. */
+int gpt2_draft_accept(const gpt2_paged_cache *cache, int T, const int32_t *tokens, const int32_t *parents,
+                      const int32_t *n_draft, const int32_t *chosen, int32_t *path, int32_t *n_kept,
+                      int32_t *next_tokens, gpt2_stream_t stream);
+
+/* Draws a token per row of stored logits z [M, ld] (types and sizes as
+ * gpt2_token_logprobs) with given random numbers.  Row m keeps the first
+ * tokens in the order of falling z (lowest id first on ties), as many as each
+ * of these allows, and one at least:
+ *   top_k[m] > 0: the first top_k[m];
+ *   top_p[m] < 1: of those, the ones before which the kept tokens' weight is
+ *     less than top_p[m] times the weight of all of those, where token v weighs
+ *     w_v = e^((z_v - max z) / temperature[m]);
+ *   min_p[m] > 0: those with w_v >= min_p[m];
+ * and temperature[m] = 0 keeps the first alone.  tokens[m] is the lowest kept
+ * id for which the weights of the kept ids up to it add up to more than
+ * uniform[m] times the weight of all kept ones; logprob[m] (NULL or fp32 [M])
+ * the logarithm of its share of that weight.  temperature, top_p, min_p: NULL
+ * (1, 1 and 0 for every row) or fp32 [M] device, top_k: NULL (0) or int32 [M]
+ * device, uniform: fp32 [M] device.  Temperatures other than 0 below 2^-100 count as 2^-100,
+ * those above 2^100 as 2^100.
+ *   The choice is that of exact arithmetic on the given numbers, up to about
+ * 2^-40 of a row's weight, and does not depend on timing.  Log
+ * probabilities are fp32, within 1e-5.
+ *   A row with a NaN or +inf, or with nothing but -inf, gets token -1 and logprob
+ * NaN.  So does, with GPT2_ERR_RANGE recorded, a row with a temperature that is
+ * negative or not finite, top_k < 0, top_p < 0, min_p outside [0, 1], uniform
+ * outside [0, 1), or a NaN among them. */
+int gpt2_sample_tokens(const void *logits, int64_t ld, gpt2_dtype logits_t, int64_t M, int V,
+                       const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                       const float *uniform, int32_t *tokens, float *logprob, gpt2_stream_t stream);
+
 /* ------------------------------------------------------------ profiling
  * Per-kernel timing of the calls made between gpt2_profile_begin() and
  * gpt2_profile_end(): the library records a CUDA event on the launching
