@@ -49,6 +49,7 @@ enum ErrSite : unsigned {
   kSitePagedShared = 28,  // a write to a page that several sequences share
   kSiteDraftParent = 29,  // a drafted token that does not stand behind its parent
   kSiteSampleRow = 30,    // a row's settings are out of range
+  kSiteSampleLoad = 31,
 };
 
 constexpr unsigned long long kWaitLimitNs = 2000000000ull;  // 2 s per wait

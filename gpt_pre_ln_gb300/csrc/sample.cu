@@ -9,17 +9,18 @@
 // same order.  The token is where the running sum of the kept weights, in the
 // order of the ids, passes uniform times their sum.
 //
-// An id is right or wrong: a sum in fp32 is off by 1e-7 of itself at best, which is
-// more than many a token's share.  So every sum is kept with a bound of its
-// error; where a decision lies within it, the row is done once more with weights
-// and sums of two floats each (2^-36 of the row's weight at worst, 2^-42 as a
-// rule).
+// An id is right or wrong: a sum of fp32 weights is off by 5e-7 of itself, which
+// is more than many a token's share.  So where a decision lies within that bound,
+// the row is done once more with weights and sums of two floats each (2^-36 of the
+// row's weight at worst, 2^-42 as a rule): 1 to 4 rows of 100, at three times the
+// time.
 //
 // One CTA per row, which it reads once into shared memory (rows that do not fit
-// are read from global memory, where they stay in L2) and goes over there: the
-// maximum; with top-k or top-p a histogram and the elements around the border,
-// which are ranked; the sums of the warps' parts of the row; and the part that
-// the random number falls into.
+// are read from global memory, where they stay in L2) and goes over there: for
+// the maximum; with top-p for a histogram of the weights, and a finer one around
+// the border; for the weights' sums; and over the part that the random number
+// falls into.  Where the kept tokens are few (top-k, or top-p of a sharp row) they
+// are listed instead, and the rest is done on the list, in two floats at once.
 #include <algorithm>
 #include <type_traits>
 
@@ -52,16 +53,32 @@ __device__ __forceinline__ Two add(Two a, Two b) {
   two_sum(a.hi, b.hi, s, e);
   return norm(s, e + (a.lo + b.lo));
 }
-__device__ __forceinline__ double value(Two a) { return static_cast<double>(a.hi) + a.lo; }
-__device__ __forceinline__ Two shfl_xor(Two a, int o) {
-  return {__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)};
+__device__ __forceinline__ Two times(Two a, float b) {
+  const float h = a.hi * b;
+  return norm(h, fmaf(a.hi, b, -h) + a.lo * b);
 }
-__device__ __forceinline__ Two shfl_up(Two a, int o) {
-  return {__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+__device__ __forceinline__ bool less(Two a, Two b) { return a.hi < b.hi || (a.hi == b.hi && a.lo < b.lo); }
+__device__ __forceinline__ float minus(Two a, Two b) { return (a.hi - b.hi) + (a.lo - b.lo); }
+__device__ __forceinline__ Two shfl(Two a, int from) {
+  return {__shfl_sync(0xffffffffu, a.hi, from), __shfl_sync(0xffffffffu, a.lo, from)};
 }
+// (loops stay loops in what follows wherever they are not the time of a pass: a
+// row goes through the code once, and what it runs for the first time it waits for)
 __device__ __forceinline__ Two warp_add(Two a) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a = add(a, shfl_xor(a, o));
+#pragma unroll 1
+  for (int o = 16; o > 0; o >>= 1)
+    a = add(a, Two{__shfl_xor_sync(0xffffffffu, a.hi, o), __shfl_xor_sync(0xffffffffu, a.lo, o)});
+  return a;
+}
+__device__ __forceinline__ Two warp_incl(Two a) {  // running sum over the lanes
+  const int lane = threadIdx.x & 31;
+#pragma unroll 1
+  for (int o = 1; o < 32; o <<= 1) {
+    const Two u{__shfl_up_sync(0xffffffffu, a.hi, o), __shfl_up_sync(0xffffffffu, a.lo, o)};
+    const Two both = add(u, a);  // (by all lanes: no branch)
+    a.hi = lane >= o ? both.hi : a.hi;
+    a.lo = lane >= o ? both.lo : a.lo;
+  }
   return a;
 }
 
@@ -92,28 +109,40 @@ __device__ const float2 kExp2[65] = {
 };
 
 // The row's scale: t = (z - max) log2(e) / temperature = (z/2 - max/2) c (half
-// of each, so that the difference of any two is a number).
+// of each, so that the difference of any two is a number).  c_lo > 0, so that a z
+// of -inf gives a t of -inf.
 struct Scale {
   float half_max, c_hi, c_lo;
 };
-
-// w = 2^t to fp32 accuracy: t is off by three roundings, the exponential by 2^-22.
-__device__ __forceinline__ float weight1(const Scale& s, float z, float& t) {
-  t = (0.5f * z - s.half_max) * s.c_hi;
-  return ex2_approx(t);
+// (the same roundings in both: bins are compared by it)
+__device__ __forceinline__ float exponent(const Scale& s, float z) {
+  const float d = __fmaf_rn(z, 0.5f, -s.half_max);
+  return __fmaf_rn(d, s.c_hi, __fmul_rn(d, s.c_lo));
 }
-constexpr float kErrExp = 4.5e-7f;   // 2^-22, and three roundings of a sum of eight
-constexpr float kErrArg = 1.25e-7f;  // per unit of |t|: 3 * 2^-24 * ln 2
+__device__ __forceinline__ float2 splat(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 exponent2(const Scale& s, float2 z) {
+  const float2 d = fma_f32x2(z, splat(0.5f), splat(-s.half_max));
+  return fma_f32x2(d, splat(s.c_hi), mul_f32x2(d, splat(s.c_lo)));
+}
+// Bound of the error of a sum of fp32 weights 2^t, of itself: 2^-22 of the
+// exponential and four roundings of sums (those of a vector's elements; sums of
+// vectors are kept in two floats), and 2 * 2^-24 ln 2 |t| for the roundings of t,
+// whose mean over the weights is at most log2(V / sum): that is what their entropy
+// leaves.
+__device__ __forceinline__ float error_of(float sum, int V) {
+  return sum * (4.8e-7f + 8.4e-8f * fmaxf(log2f(static_cast<float>(V) / sum), 0.f)) + 1e-30f;
+}
 
-// The same to about 2^-45 of itself: t as two floats, 2^t = 2^n 2^(k/64) e^x with
-// the integer n, the nearest k and |x| <= ln 2 / 128, whose series ends with x^5.
-// Weights below 2^-100 count as 0.
+// The same to about 2^-45 of itself: 2^t = 2^n 2^(k/64) e^x with the integer n, the
+// nearest k and |x| <= ln 2 / 128, whose series ends with x^5.  Weights below 2^-100
+// count as 0.
 __device__ __forceinline__ Two weight2(const Scale& s, const float2* table, float z) {
   const float a = 0.5f * z;
   float d, d_lo;
   two_sum(a, -s.half_max, d, d_lo);
   const float t = d * s.c_hi;
-  if (!(t > -100.f)) return {0.f, 0.f};
+  // (below 2^-36 of the largest weight fp32 will do; below 2^-100 they count as 0)
+  if (!(t > -36.f)) return {t > -100.f ? ex2_approx(fmaf(d, s.c_lo, t)) : 0.f, 0.f};
   const float t_lo = fmaf(d, s.c_hi, -t) + fmaf(d, s.c_lo, d_lo * s.c_hi);
   const float n = rintf(t), f = t - n, k = rintf(64.f * f), g = fmaf(k, -0.015625f, f);
   constexpr float kLn2Hi = 0.6931471824645996f, kLn2Lo = -1.9046542121259336e-09f;  // ln 2
@@ -142,28 +171,46 @@ __device__ __forceinline__ uint32_t key_of(float z) {
 __device__ __forceinline__ float z_of(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
-__device__ __forceinline__ unsigned long long place_of(uint32_t key, int id) {
-  return (static_cast<unsigned long long>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
+using Place = unsigned long long;
+__device__ __forceinline__ Place place_at(uint32_t key, int id) {
+  return (static_cast<Place>(key) << 32) | (0xffffffffu - static_cast<uint32_t>(id));
 }
-// 16 bytes of a row
+__device__ __forceinline__ Place place_of(float z, int id) { return place_at(key_of(z), id); }
+__device__ __forceinline__ int id_of(Place p) { return static_cast<int>(0xffffffffu - static_cast<uint32_t>(p)); }
+__device__ __forceinline__ float z_of(Place p) { return z_of(static_cast<uint32_t>(p >> 32)); }
+
+// The last element of the order that stays.
+struct Cut {
+  float z;
+  int id;
+  __device__ __forceinline__ bool keeps(float x, int i) const { return x > z || (x == z && i <= id); }
+  __device__ __forceinline__ Place place() const { return place_of(z, id); }
+};
+__device__ __forceinline__ Cut cut_at(Place p) { return {z_of(p), id_of(p)}; }
+
+// 16 bytes of a row, as pairs
 template <typename T>
 struct Vec {
   static constexpr int kN = 16 / static_cast<int>(sizeof(T));
-  static __device__ __forceinline__ void unpack(const uint4& u, float (&z)[kN]) {
+  static __device__ __forceinline__ void unpack(const uint4& u, float2 (&z)[kN / 2]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
     if constexpr (sizeof(T) == 4) {
-      z[0] = __uint_as_float(u.x), z[1] = __uint_as_float(u.y), z[2] = __uint_as_float(u.z),
-      z[3] = __uint_as_float(u.w);
+      z[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      z[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
     } else {
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = Type16<T>::unpack2(w[i]);
-        z[2 * i] = f.x;
-        z[2 * i + 1] = f.y;
-      }
+      for (int i = 0; i < 4; ++i)
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+          z[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+        else
+          z[i] = Type16<T>::unpack2(w[i]);
     }
   }
 };
+template <int N>
+__device__ __forceinline__ float at(const float2 (&z)[N], int i) {
+  return i & 1 ? z[i >> 1].y : z[i >> 1].x;
+}
 
 struct SampleArgs {
   const void* logits;
@@ -179,577 +226,1117 @@ struct SampleArgs {
   unsigned* err;
 };
 
-// What a CTA knows of its row, and its shared memory.
-template <typename T>
-struct Row {
-  const uint4* v;  // the row, in shared or global memory
-  int V, vecs, per_warp;  // vectors of the row, and of one warp's part
-  Scale scale;
-  uint32_t* hist;              // [kBins]
-  unsigned long long* list;    // [kList]
-  unsigned long long* sorted;  // [kList], in the place of hist
-};
+// Shared memory: this, and behind it the row.  (Reached by name, not through
+// pointers that are handed on: the compiler then knows that it is shared memory.)
 struct Shared {
-  Two part[32];
-  float aux[32];
+  union {
+    uint32_t hist[kBins];
+    struct {
+      Two by_order[kList], by_id[kList];
+    };
+  };
+  Place list[kList];
+  Two part[32], part2[32];
+  float aux[32], aux2[32];
   int num[32];
   uint32_t lo, hi;
-  int count, first, last;
-  float before;
-  unsigned long long cut;
-  Two kept, above;
-  float loose;
-  int found;
+  int count, first, last, found, bad;
+  Cut cut, cut_min;
+  float loose, margin, logprob;
+  Scale scale;
+  double least;
+  const uint4* global;
+  int V, vecs, per_warp;  // of the row, in vectors; of one warp's part
+  uint64_t bar[32];
   float2 table[65];
 };
-
-// The elements of this warp's part of the row, a lane's vector at a time.
-template <typename T, typename F>
-__device__ __forceinline__ void each(const Row<T>& r, int from, int to, F&& f) {
-  constexpr int kN = Vec<T>::kN;
-  const int lane = threadIdx.x & 31;
-  for (int v = from + lane; v < to; v += 32) {
-    float z[kN];
-    Vec<T>::unpack(r.v[v], z);
-#pragma unroll
-    for (int i = 0; i < kN; ++i)
-      if (v * kN + i >= r.V) z[i] = -INFINITY;  // behind the row: nothing
-    f(z, v * kN);
-  }
-}
-template <typename T, typename F>
-__device__ __forceinline__ void each_of_part(const Row<T>& r, F&& f) {
-  const int from = (threadIdx.x >> 5) * r.per_warp;
-  each(r, min(from, r.vecs), min(from + r.per_warp, r.vecs), f);
+constexpr size_t kFixed = (sizeof(Shared) + 15) / 16 * 16;
+__device__ __forceinline__ Shared& shared() {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  return *reinterpret_cast<Shared*>(s_raw);
 }
 
-// Sum of this lane's weights over elements at or above `cut`, in the order of
-// the ids; err adds the bound of its error (fp32 weights only).
-template <bool TWO, typename T>
-struct Weights {
-  const Row<T>& r;
-  const float2* table;
-  Two sum{0.f, 0.f};
-  float wt = 0.f;  // sum of w |t|
-  __device__ __forceinline__ Weights(const Row<T>& row, const float2* tab) : r(row), table(tab) {}
-  __device__ __forceinline__ void add_vec(const float (&z)[Vec<T>::kN], int id, unsigned long long cut) {
-    constexpr int kN = Vec<T>::kN;
-    const uint32_t key_cut = static_cast<uint32_t>(cut >> 32);
-    if constexpr (TWO) {
+// A kernel's element type, threads, and whether its rows fit shared memory.
+template <typename T_, int NT_, bool IN_SMEM_>
+struct Kind {
+  using T = T_;
+  static constexpr int NT = NT_, kWarps = NT_ / 32, kN = Vec<T_>::kN;
+  static constexpr bool IN_SMEM = IN_SMEM_;
+};
+template <typename K>
+__device__ __forceinline__ const uint4* row() {
+  extern __shared__ __align__(16) uint8_t s_raw[];
+  if constexpr (K::IN_SMEM)
+    return reinterpret_cast<const uint4*>(s_raw + kFixed);
+  else
+    return shared().global;
+}
+// Element i of the row, -inf behind its end.
+template <typename K>
+__device__ __forceinline__ float element(int i) {
+  return i < shared().V ? to_f32<typename K::T>(reinterpret_cast<const typename K::T*>(row<K>())[i]) : -INFINITY;
+}
+template <typename K>
+__device__ __forceinline__ void vector_of(int v, int V, float2 (&z)[K::kN / 2]) {
+  Vec<typename K::T>::unpack(row<K>()[v], z);
+  if ((v + 1) * K::kN > V) {
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t key = key_of(z[i]);
-        if (key > key_cut || (key == key_cut && place_of(key, id + i) >= cut)) sum = add(sum, weight2(r.scale, table, z[i]));
-      }
-    } else {
-      float w[kN];
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t key = key_of(z[i]);
-        float t;
-        w[i] = weight1(r.scale, z[i], t);
-        if (!(key > key_cut || (key == key_cut && place_of(key, id + i) >= cut))) w[i] = 0.f;
-        if (w[i] > 0.f) wt = fmaf(w[i], -t, wt);
-      }
-#pragma unroll
-      for (int o = 1; o < kN; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < kN; i += 2 * o) w[i] += w[i + o];
-      float s, e;
-      two_sum(sum.hi, w[0], s, e);
-      sum = {s, sum.lo + e};
+    for (int i = 0; i < K::kN / 2; ++i) {
+      if (v * K::kN + 2 * i >= V) z[i].x = -INFINITY;
+      if (v * K::kN + 2 * i + 1 >= V) z[i].y = -INFINITY;
     }
   }
-  __device__ __forceinline__ float error() const { return TWO ? 0.f : fmaf(sum.hi, kErrExp, wt * kErrArg); }
+}
+// This warp's part of the row: the vectors from .. to - 1.
+__device__ __forceinline__ void part_of(int warp, int& from, int& to) {
+  from = min(warp * shared().per_warp, shared().vecs);
+  to = min(from + shared().per_warp, shared().vecs);
+}
+
+// A lane's sum in two floats, of the even elements and of the odd ones.
+struct TwoPair {
+  float2 hi, lo;
+  __device__ __forceinline__ Two total() const {
+    Two a = norm(hi.x, lo.x);
+    return add(a, norm(hi.y, lo.y));
+  }
+  __device__ __forceinline__ void add(float2 x) {
+    const float2 s = add_f32x2(hi, x), t = fma_f32x2(hi, splat(-1.f), s);  // s - hi
+    const float2 e = add_f32x2(fma_f32x2(fma_f32x2(t, splat(-1.f), s), splat(-1.f), hi), fma_f32x2(t, splat(-1.f), x));
+    hi = s;
+    lo = add_f32x2(lo, e);
+  }
+  __device__ __forceinline__ Two add(Two a, Two b) const { return gpt2::add(a, b); }
 };
+// Weights 2^t of a vector's elements, added up pair by pair.
+template <int N>
+__device__ __forceinline__ float2 sum_of(const float2 (&t)[N]) {
+  float2 w[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) w[i] = make_float2(ex2_approx(t[i].x), ex2_approx(t[i].y));
+#pragma unroll
+  for (int o = 1; o < N; o <<= 1)
+#pragma unroll
+    for (int i = 0; i < N; i += 2 * o) w[i] = add_f32x2(w[i], w[i + o]);
+  return w[0];
+}
+template <int N>
+__device__ __forceinline__ void exponents(const Scale& s, const float2 (&z)[N], float2 (&t)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) t[i] = exponent2(s, z[i]);
+}
+// Exponents of elements that the cut does not keep become -inf.
+template <int N>
+__device__ __forceinline__ void cut_off(const Cut& cut, const float2 (&z)[N], int id, float2 (&t)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (!cut.keeps(z[i].x, id + 2 * i)) t[i].x = -INFINITY;
+    if (!cut.keeps(z[i].y, id + 2 * i + 1)) t[i].y = -INFINITY;
+  }
+}
+__device__ __forceinline__ void add_to(Two& sum, float x) {
+  float s, e;
+  two_sum(sum.hi, x, s, e);
+  sum = {s, sum.lo + e};
+}
+// Weight of the elements of vectors from .. to - 1 that the cut keeps, a warp's
+// lanes side by side: a lane's.
+template <typename K, bool TWO>
+__device__ __forceinline__ Two lane_sum(const Scale& s, int V, const Cut& cut, int from, int to) {
+  const int lane = threadIdx.x & 31;
+  if constexpr (TWO) {
+    Two sum{0.f, 0.f};
+#pragma unroll 1
+    for (int v = from + lane; v < to; v += 32)
+#pragma unroll 1
+      for (int i = v * K::kN; i < (v + 1) * K::kN; ++i) {
+        const float z = element<K>(i);
+        if (cut.keeps(z, i)) sum = add(sum, weight2(s, shared().table, z));
+      }
+    return norm(sum.hi, sum.lo);
+  } else {
+    TwoPair sum{splat(0.f), splat(0.f)};
+    const bool whole = cut.z == -INFINITY;  // (what is -inf weighs nothing)
+#pragma unroll 2
+    for (int v = from + lane; v < to; v += 32) {
+      float2 z[K::kN / 2], t[K::kN / 2];
+      vector_of<K>(v, V, z);
+      exponents(s, z, t);
+      if (!whole) cut_off(cut, z, v * K::kN, t);
+      sum.add(sum_of(t));
+    }
+    return sum.total();
+  }
+}
+// The same over the lanes.
+template <typename K, bool TWO>
+__device__ __noinline__ Two sum_vectors(Cut cut, int from, int to) {
+  const Two sum = lane_sum<K, TWO>(shared().scale, shared().V, cut, from, to);
+  __syncwarp();
+  return warp_add(sum);
+}
 
 // Sum over the block; every thread gets it.
-__device__ __forceinline__ Two block_add(Two a, Shared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  a = warp_add(a);
+template <typename K>
+__device__ __noinline__ Two block_add(Two a) {
+  Shared& sh = shared();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  a = warp_add(norm(a.hi, a.lo));
   if (lane == 0) sh.part[warp] = a;
   __syncthreads();
-  a = lane < warps ? sh.part[lane] : Two{0.f, 0.f};
+  a = lane < K::kWarps ? sh.part[lane] : Two{0.f, 0.f};
   a = warp_add(a);
   __syncthreads();
   return a;
 }
-__device__ __forceinline__ float block_add(float a, Shared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
-  if (lane == 0) sh.aux[warp] = a;
+template <typename K>
+__device__ __forceinline__ int block_add(int a) {
+  Shared& sh = shared();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  a = __reduce_add_sync(0xffffffffu, a);
+  if (lane == 0) sh.num[warp] = a;
   __syncthreads();
-  a = lane < warps ? sh.aux[lane] : 0.f;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+  a = __reduce_add_sync(0xffffffffu, lane < K::kWarps ? sh.num[lane] : 0);
   __syncthreads();
   return a;
 }
 
-// The place of the last element to keep of those at or above `cut`: the
-// `count` first of them (MASS false), or those before which less than `target`
-// of weight stands (MASS).  `total`: how many elements there are.  In *loose the
-// weight of the elements that may or may not belong (fp32 weights, whose sums
-// are off by up to `err`).
-//
-// A histogram leaves an interval of the order with few enough elements to rank;
-// the first one is over bins of equal width in z, later ones, where equal or
-// nearly equal logits crowd a bin, over bins of equal width in the place.  The
-// weights in it are whole multiples of a fixed step, so that sums do not depend
-// on the order of the additions; the bins around the border are taken with a
-// margin for that step.
-template <bool MASS, bool TWO, typename T>
-__device__ unsigned long long select(const Row<T>& r, Shared& sh, unsigned long long cut, int count, double target,
-                                     float err, float* loose) {
-  constexpr int kN = Vec<T>::kN;
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, warps = nt >> 5;
-  // bins of the first histogram: 64 to a factor of two of the weight
-  const float bin_scale = -64.f * r.scale.c_hi;
-  auto bin_of = [&](float z) {
-    return static_cast<int>(fminf((0.5f * z - r.scale.half_max) * bin_scale, static_cast<float>(kBins - 1)));
+// ------------------------------------------------------------ histogram
+// Bins of equal width in z, 64 to a factor of two of the weight, bin b around
+// 2^(-b / 64); the last one takes all below 2^-32.
+constexpr float kMagic = 8388608.f;  // 2^23: adding it rounds to whole numbers
+__device__ __forceinline__ float bin_edge(int b) { return kMagic + static_cast<float>(b); }
+__device__ __forceinline__ float bin_at(float t) { return __fmaf_rn(t, -64.f, kMagic); }  // compared with an edge
+// Counts a pair of weights, those above 2^-32, in units of their bins' steps
+// (2^(-b / 64) is `one` of them): integers, so that sums do not depend on the order
+// of the additions.  e^x with |x| <= ln 2 / 128 is taken as 1 + x: 1.5e-5 off at
+// most.
+__device__ __forceinline__ void count_weights(uint32_t* hist, float2 t, float one) {
+  const float unit = 0.010830424696249145f * one;  // ln 2 / 64
+  const float2 m = fma_f32x2(t, splat(-64.f), splat(kMagic)), b = add_f32x2(m, splat(-kMagic));
+  const float2 n = fma_f32x2(t, splat(64.f * unit), fma_f32x2(b, splat(unit), splat(one + kMagic)));
+  if (t.x > -31.9f) atomicAdd(hist + (__float_as_int(m.x) - 0x4b000000), __float_as_uint(n.x) - 0x4b000000u);
+  if (t.y > -31.9f) atomicAdd(hist + (__float_as_int(m.y) - 0x4b000000), __float_as_uint(n.y) - 0x4b000000u);
+}
+constexpr float kErrBin = 4e-5f;  // of a sum of bins: the above, the integers' step of 2^-15 at most half, fp32 sums
+
+// Where the running sum over the bins, each h / one times 2^(-b / 64) (or 1, if
+// flat), comes within `margin` of `want`, and where it passes it by as much: bins
+// first and last (the last bin of all where that is not found); in `count` the sum
+// of h / one of the bins up to last.
+template <typename K>
+__device__ __noinline__ void find_bins(bool flat, float one, float want, float margin, int& first, int& last,
+                                       float& count) {
+  constexpr int kPer = kBins / K::NT;
+  Shared& sh = shared();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const float scale = 1.f / one, slope = flat ? 0.f : -0.015625f;
+  float run = 0.f, n = 0.f;
+#pragma unroll 2
+  for (int i = 0; i < kPer; ++i) {
+    const float h = static_cast<float>(sh.hist[tid * kPer + i]) * scale;
+    n += h;
+    run = fmaf(h, ex2_approx(static_cast<float>(tid * kPer + i) * slope), run);
+  }
+  const float mine = run, mine_n = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float u = __shfl_up_sync(0xffffffffu, run, o), un = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) run += u, n += un;
+  }
+  if (lane == 31) {
+    sh.aux[warp] = run;
+    sh.aux2[warp] = n;
+  }
+  if (tid == 0) {
+    sh.first = kBins;
+    sh.last = -1;
+    sh.loose = 1e9f;
+  }
+  __syncthreads();
+  float ahead = lane < warp ? sh.aux[lane] : 0.f, ahead_n = lane < warp ? sh.aux2[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    ahead_n += __shfl_xor_sync(0xffffffffu, ahead_n, o);
+  }
+  run += ahead - mine;
+  n += ahead_n - mine_n;
+#pragma unroll 2
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * kPer + i;
+    const float h = static_cast<float>(sh.hist[b]) * scale, before = run;
+    n += h;
+    run = fmaf(h, ex2_approx(static_cast<float>(b) * slope), run);
+    if ((b == 0 || before < want - margin) && run >= want - margin) atomicMin(&sh.first, b);
+    if ((b == 0 || before < want + margin) && run >= want + margin) {
+      atomicMax(&sh.last, b);
+      sh.loose = n;
+    }
+  }
+  __syncthreads();
+  // (where one thread's sum ends a rounding below the next one's start a border may be found by neither)
+  first = sh.first;
+  last = first < kBins && sh.last >= first ? sh.last : kBins - 1;
+  count = sh.loose;
+  __syncthreads();
+}
+
+// Sums up to each of the kList values at a (in place, its own included), over the
+// block.
+template <typename K, bool BY_ID>
+__device__ __noinline__ void scan_list() {
+  constexpr int kPer = K::NT >= kList ? 1 : kList / K::NT;
+  Shared& sh = shared();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const bool on = tid * kPer < kList;
+  Two x[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    x[i] = on ? (BY_ID ? sh.by_id : sh.by_order)[tid * kPer + i] : Two{0.f, 0.f};
+    if (i > 0) x[i] = add(x[i - 1], x[i]);
+  }
+  Two incl = warp_incl(x[kPer - 1]);
+  if (lane == 31) sh.part[warp] = incl;
+  __syncthreads();
+  const Two parts = warp_incl(lane < K::kWarps ? sh.part[lane] : Two{0.f, 0.f});
+  Two before = shfl(incl, (lane + 31) & 31);
+  if (lane == 0) before = {0.f, 0.f};
+  const Two ahead = shfl(parts, (warp + 31) & 31);
+  if (warp > 0) before = add(ahead, before);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (on) (BY_ID ? sh.by_id : sh.by_order)[tid * kPer + i] = add(before, x[i]);
+  __syncthreads();
+}
+
+// An element of the list and its ranks: in the order, and among the ids.
+struct Listed {
+  Place p;
+  Two w;
+  int rank, rank_id;
+};
+template <typename K>
+constexpr int kListed = K::NT >= kList ? 1 : kList / K::NT;  // per thread
+
+// The n elements of the list: ranks and weights, and by_order the sums of the
+// weights in the order.  (Each against all: 3000 cycles for 100 of them, 15000 for
+// 500.)
+template <typename K>
+__device__ __forceinline__ void rank_list(int n, Listed (&mine)[kListed<K>]) {
+  Shared& sh = shared();
+  for (int i = threadIdx.x; i < kList; i += K::NT) {
+    sh.by_order[i] = {0.f, 0.f};
+    if (i >= n) sh.list[i] = 0;  // ranks behind all others
+  }
+  __syncthreads();
+  const Scale s = sh.scale;
+  const ulonglong2* list = reinterpret_cast<const ulonglong2*>(sh.list);
+#pragma unroll 1
+  for (int e = 0; e < kListed<K>; ++e) {
+    const int i = threadIdx.x + e * K::NT;
+    Listed x{0, {0.f, 0.f}, 0, 0};
+    if (i < n) {
+      x.p = sh.list[i];
+      const uint32_t low = static_cast<uint32_t>(x.p);
+#pragma unroll 4
+      for (int k = 0; k < (n + 1) / 2; ++k) {
+        const ulonglong2 q = list[k];
+        x.rank += (q.x > x.p) + (q.y > x.p);
+        // (a lower id has the larger number)
+        x.rank_id += (static_cast<uint32_t>(q.x) > low) + (static_cast<uint32_t>(q.y) > low);
+      }
+      x.w = weight2(s, sh.table, z_of(x.p));
+      sh.by_order[x.rank] = x.w;
+    }
+    mine[e] = x;
+  }
+  __syncthreads();
+  scan_list<K, false>();
+}
+
+// Of the list's elements, those that stay: the first `most`, kept by cut_min, and
+// before which, with `ahead` before the list, less than `target` stands; one at
+// least if `one`.  Their number; `loose`: the weight of those that an error of `err`
+// in the difference leaves undecided.
+template <typename K>
+__device__ __forceinline__ int keep_listed(int n, const Listed (&mine)[kListed<K>], int most, const Cut& cut_min,
+                                           Two ahead, Two target, float err, bool one, float& loose) {
+  Shared& sh = shared();
+  int in = 0;
+  Two unsure{0.f, 0.f};
+#pragma unroll 1
+  for (int e = 0; e < kListed<K>; ++e) {
+    if (threadIdx.x + e * K::NT >= n) break;
+    const Listed& x = mine[e];
+    Two before = ahead;
+    if (x.rank > 0) before = add(ahead, sh.by_order[x.rank - 1]);
+    if (x.rank < most && cut_min.keeps(z_of(x.p), id_of(x.p))) {
+      in += less(before, target) || (one && x.rank == 0);
+      if (err > 0.f && fabsf(minus(before, target)) <= err) add_to(unsure, x.w.hi);
+    } else if (one && x.rank == 0) {
+      ++in;
+    }
+  }
+  __syncwarp();
+  const int kept = block_add<K>(in);
+  loose = err > 0.f ? block_add<K>(unsure).hi : 0.f;
+  return kept;
+}
+__device__ __forceinline__ Two listed_sum(int kept, Two ahead) {
+  return kept > 0 ? add(ahead, shared().by_order[kept - 1]) : ahead;
+}
+
+// ------------------------------------------------------------ crowded borders
+// The last of the elements kept by `cut` that stays: the `count` first of them
+// (MASS false), or those before which less than `target` of weight stands (MASS).
+// For any row, at its own pace: histograms over ever smaller intervals of the
+// order, until few enough elements are left to rank; the first one of bins of equal
+// width in z, from the maximum to the least that is not -inf, later ones, where equal
+// or nearly equal logits crowd a bin, of bins of equal width in the place.  In *loose the weight of the elements that sums off by `err` leave
+// undecided (INFINITY: none decided).
+template <typename K, bool MASS, bool TWO>
+__device__ __noinline__ Cut select(Cut cut, int count, Two target, float err, float* loose) {
+  constexpr int kPer = kBins / K::NT;
+  Shared& sh = shared();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = sh.V;
+  const Scale s = sh.scale;
+  int from, to;
+  part_of(warp, from, to);
+  from *= K::kN;
+  to = min(to * K::kN, V);
+  Place lo = cut.place(), hi = place_of(2.f * s.half_max, 0);  // the interval
+  int n = V;         // elements that it holds, at most
+  int before_n = 0;  // elements ahead of it
+  auto weight = [&](float z, Two& sum) {
+    if constexpr (TWO)
+      sum = add(sum, weight2(s, sh.table, z));
+    else
+      add_to(sum, ex2_approx(exponent(s, z)));
   };
-  unsigned long long lo = 0, hi = ~0ull;  // the interval
-  int shift = -1;                     // its bins' width; -1: the first histogram
-  int n = r.V;                        // elements that the histogram counts, at most
-  int before_n = 0;                   // elements ahead of the interval
+  // the least that is not -inf, and with it the first histogram's bins
+  if (tid == 0) sh.lo = 0xffffffffu;
+  __syncthreads();
+  uint32_t least = 0xffffffffu;
+  int there = 0;  // (what is -inf is never drawn: it might as well not be there)
+#pragma unroll 1
+  for (int i = from + lane; i < to; i += 32) {
+    const float z = element<K>(i);
+    if (z > -INFINITY && cut.keeps(z, i)) {
+      least = min(least, key_of(z));
+      ++there;
+    }
+  }
+  __syncwarp();
+  least = __reduce_min_sync(0xffffffffu, least);
+  if (lane == 0) atomicMin(&sh.lo, least);
+  there = block_add<K>(there);
+  if (!MASS && there <= count) return cut;
+  const float per_z = static_cast<float>(kBins - 8) / (s.half_max - 0.5f * z_of(sh.lo));  // (halves: no overflow)
+  __syncthreads();
+  auto bin_of = [&](float z) {
+    return static_cast<int>(fminf((s.half_max - 0.5f * z) * per_z, static_cast<float>(kBins - 1)));
+  };
+  bool linear = per_z < 3e38f;
+#pragma unroll 1
   while (true) {
+    const int shift = max(0, 64 - __clzll(static_cast<long long>(hi - lo)) - 11);
     const int digits = 31 - min(31, 32 - __clz(n));  // n elements of at most 2^digits
     const float one = static_cast<float>(1u << digits);
-    // the heaviest weight in the interval
-    const float top = shift < 0 ? 0.f : (0.5f * z_of(static_cast<uint32_t>(hi >> 32)) - r.scale.half_max) * r.scale.c_hi;
-    for (int i = tid; i < kBins; i += nt) r.hist[i] = 0;
+    const float top = linear ? 0.f : exponent(s, z_of(hi));  // the heaviest weight in it
+    const float fall = linear ? s.c_hi / per_z : 0.f;  // of the heaviest weight's exponent, per bin
+    for (int i = tid; i < kBins; i += K::NT) sh.hist[i] = 0;
     __syncthreads();
-    float ahead = 0.f;  // weight ahead of the interval
-    each_of_part(r, [&](const float (&z)[kN], int id) {
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const unsigned long long p = place_of(key_of(z[i]), id + i);
-        if (p < cut || id + i >= r.V) continue;
-        int b;
-        float t = 0.f;
-        if (MASS) t = (0.5f * z[i] - r.scale.half_max) * r.scale.c_hi;
-        if (shift < 0) {
-          b = bin_of(z[i]);
-          if (MASS) t += static_cast<float>(b) * 0.015625f;  // over the bin's first
-        } else {
-          if (p > hi) {
-            if (MASS) ahead += ex2_approx(t);
-            continue;
-          }
-          if (p < lo) continue;
-          b = kBins - 1 - static_cast<int>((p - lo) >> shift);
-          t -= top;
-        }
-        atomicAdd(&r.hist[b], MASS ? __float2uint_rn(fminf(ex2_approx(t), 1.f) * one) : 1u);
+    Two ahead{0.f, 0.f};  // weight ahead of it
+#pragma unroll 1
+    for (int i = from + lane; i < to; i += 32) {
+      const float z = element<K>(i);
+      const Place p = place_of(z, i);
+      if (p < lo || z == -INFINITY) continue;
+      const float t = exponent(s, z);
+      if (p > hi) {
+        if (MASS) add_to(ahead, ex2_approx(t));
+        continue;
       }
-    });
-    if (MASS) ahead = block_add(ahead, sh);
-    __syncthreads();
-    // the bins that the border may be in
-    const int per = kBins / nt;
-    auto weight_of_bin = [&](int b) {
-      const float w = static_cast<float>(r.hist[b]) / one;
-      return shift < 0 ? ldexpf(exp2f(static_cast<float>(b & 63) * -0.015625f) * w, -(b >> 6)) : w * exp2f(top);
-    };
-    float mine = 0.f;
-    int mine_n = 0;
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      if (MASS)
-        mine += weight_of_bin(b);
-      else
-        mine_n += static_cast<int>(r.hist[b]);
+      const int b = linear ? bin_of(z) : kBins - 1 - static_cast<int>((p - lo) >> shift);
+      const float over = t - top + static_cast<float>(b) * fall;
+      atomicAdd(&sh.hist[b], MASS ? __float2uint_rn(fminf(ex2_approx(over), 1.02f) * 0.98f * one) : 1u);
     }
-    float run = mine;
-    int run_n = mine_n;
-#pragma unroll
+    __syncwarp();
+    ahead = block_add<K>(ahead);
+    // the bins that the border may be in (weights carry 0.98 of themselves, so that a bin's sum fits)
+    auto of_bin = [&](int b) {
+      const float h = static_cast<float>(sh.hist[b]);
+      return MASS ? h / (0.98f * one) * ex2_approx(top - static_cast<float>(b) * fall) : h;
+    };
+    float run = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < kPer; ++i) run += of_bin(tid * kPer + i);
+    const float mine = run;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
       const float u = __shfl_up_sync(0xffffffffu, run, o);
-      const int un = __shfl_up_sync(0xffffffffu, run_n, o);
-      if (lane >= o) run += u, run_n += un;
+      if (lane >= o) run += u;
     }
-    if (lane == 31) {
-      sh.aux[warp] = run;
-      sh.num[warp] = run_n;
-    }
+    if (lane == 31) sh.aux[warp] = run;
     if (tid == 0) {
-      sh.first = kBins - 1;
-      sh.last = kBins - 1;
+      sh.first = sh.last = kBins - 1;
       sh.count = 0;
       sh.lo = 0xffffffffu;
       sh.hi = 0;
     }
     __syncthreads();
-    float all = ahead;
-    for (int w = 0; w < warps; ++w) {
-      if (w < warp) run += sh.aux[w], run_n += sh.num[w];
+    float all = ahead.hi;
+#pragma unroll 1
+    for (int w = 0; w < K::kWarps; ++w) {
+      if (w < warp) run += sh.aux[w];
       all += sh.aux[w];
     }
-    run += ahead - mine;
-    run_n += before_n - mine_n;  // ahead of this thread's bins
-    // a step of the histogram per element, and the roundings of the sums
-    const float margin = MASS ? (shift < 0 ? all / one : static_cast<float>(n) / one * exp2f(top)) + 1e-5f * all + err : 0.f;
-    const float want = static_cast<float>(target);
-    for (int i = 0; i < per; ++i) {
-      const int b = tid * per + i;
-      if (MASS) {
-        const float next = run + weight_of_bin(b);
-        if (next >= want - margin) atomicMin(&sh.first, b);
-        if (next >= want + margin) atomicMin(&sh.last, b);
-        run = next;
-      } else {
-        const int next = run_n + static_cast<int>(r.hist[b]);
-        if (next >= count) {
-          atomicMin(&sh.first, b);
-          atomicMin(&sh.last, b);
-        }
-        run_n = next;
+    run += (MASS ? ahead.hi : static_cast<float>(before_n)) - mine;
+    // a step of the histogram per element, and the roundings of the sums (counts are exact)
+    const float margin =
+        MASS ? (linear ? 1.1f * all : static_cast<float>(n) * ex2_approx(top)) / one + 1e-4f * all + err : 0.f;
+    const float want = MASS ? target.hi : static_cast<float>(count);
+#pragma unroll 1
+    for (int i = 0; i < kPer; ++i) {
+      run += of_bin(tid * kPer + i);
+      if (run >= want - margin) atomicMin(&sh.first, tid * kPer + i);
+      if (run >= want + margin) {
+        atomicMin(&sh.last, tid * kPer + i);
+        break;
       }
     }
     __syncthreads();
-    const int first = sh.first, last = sh.last;
     // the elements in them, and the weight ahead of them
-    unsigned long long in_lo = 0, in_hi = 0;
-    if (shift >= 0) {
-      in_lo = lo + (static_cast<unsigned long long>(kBins - 1 - last) << shift);
-      const unsigned long long off =
-          (static_cast<unsigned long long>(kBins - 1 - first) << shift) + ((1ull << shift) - 1);
-      in_hi = off >= hi - lo ? hi : lo + off;
-    }
-    Weights<TWO, T> above(r, sh.table);
+    const int first = sh.first, last = sh.last;
+    const Place was = hi - lo, off = (static_cast<Place>(kBins - 1 - first) << shift) + ((1ull << shift) - 1);
+    const Place in_lo = lo + (static_cast<Place>(kBins - 1 - last) << shift), in_hi = off >= was ? hi : lo + off;
+    Two above{0.f, 0.f};
     uint32_t k_lo = 0xffffffffu, k_hi = 0;
     int ahead_n = 0;
-    each_of_part(r, [&](const float (&z)[kN], int id) {
-      float zz[kN];
-#pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        const uint32_t key = key_of(z[i]);
-        const unsigned long long p = place_of(key, id + i);
-        zz[i] = -INFINITY;
-        if (p < cut || id + i >= r.V) continue;
-        int where;  // 1 ahead, 0 in the interval, -1 behind
-        if (shift < 0) {
-          const int b = bin_of(z[i]);
-          where = b < first ? 1 : b > last ? -1 : 0;
-        } else {
-          where = p > in_hi ? 1 : p < in_lo ? -1 : 0;
-        }
-        if (where > 0) {
-          zz[i] = z[i];
-          ++ahead_n;
-        } else if (where == 0) {
-          const int at = atomicAdd(&sh.count, 1);
-          if (at < kList) r.list[at] = p;
-          k_lo = min(k_lo, key);
-          k_hi = max(k_hi, key);
-        }
+#pragma unroll 1
+    for (int i = from + lane; i < to; i += 32) {
+      const float z = element<K>(i);
+      const Place p = place_of(z, i);
+      if (p < lo || z == -INFINITY) continue;
+      int where;  // 1 ahead, 0 in them, -1 behind
+      if (linear) {
+        const int b = bin_of(z);
+        where = b < first ? 1 : b > last ? -1 : 0;
+      } else {
+        where = p > in_hi ? 1 : p < in_lo ? -1 : 0;
       }
-      if (MASS) above.add_vec(zz, id, 1ull << 32);  // -inf weighs nothing
-    });
+      if (where > 0) {
+        ++ahead_n;
+        if (MASS) weight(z, above);
+      } else if (where == 0) {
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < kList) sh.list[at] = p;
+        k_lo = min(k_lo, static_cast<uint32_t>(p >> 32));
+        k_hi = max(k_hi, static_cast<uint32_t>(p >> 32));
+      }
+    }
+    __syncwarp();
     k_lo = __reduce_min_sync(0xffffffffu, k_lo);
     k_hi = __reduce_max_sync(0xffffffffu, k_hi);
     if (lane == 0) {
       atomicMin(&sh.lo, k_lo);
       atomicMax(&sh.hi, k_hi);
     }
-    const Two ahead_w = MASS ? block_add(above.sum, sh) : Two{0.f, 0.f};
-    ahead_n = __reduce_add_sync(0xffffffffu, ahead_n);
-    if (lane == 0) sh.num[warp] = ahead_n;
-    __syncthreads();
-    ahead_n = 0;
-    for (int w = 0; w < warps; ++w) ahead_n += sh.num[w];
+    above = block_add<K>(above);
+    ahead_n = block_add<K>(ahead_n);
     n = sh.count;
     if (n > kList) {
-      const unsigned long long was = hi - lo;
-      if (shift < 0) {
-        lo = static_cast<unsigned long long>(sh.lo) << 32;
-        hi = (static_cast<unsigned long long>(sh.hi) << 32) | 0xffffffffu;
+      if (linear) {
+        lo = max(lo, static_cast<Place>(sh.lo) << 32);
+        hi = min(hi, (static_cast<Place>(sh.hi) << 32) | 0xffffffffu);
       } else {
         lo = in_lo;
         hi = in_hi;
       }
-      lo = max(lo, cut);
       if (lo >> 32 == hi >> 32) {  // one value: of its places the ids there are
-        lo = max(lo, place_of(static_cast<uint32_t>(lo >> 32), r.V - 1));
-        hi = min(hi, place_of(static_cast<uint32_t>(hi >> 32), 0));
+        lo = max(lo, place_at(static_cast<uint32_t>(lo >> 32), V - 1));
+        hi = min(hi, place_at(static_cast<uint32_t>(hi >> 32), 0));
       }
       before_n = ahead_n;
-      if (MASS && hi - lo > was / 2) {
+      if (MASS && !linear && hi - lo > was / 2) {
         // weights of very different sizes, too fine for the histogram's step: by halves
-        const unsigned long long mid = lo + (hi - lo) / 2;
-        Weights<TWO, T> w(r, sh.table);
-        int more = 0;
-        each_of_part(r, [&](const float (&z)[kN], int id) {
-          w.add_vec(z, id, max(mid, cut));
-#pragma unroll
-          for (int i = 0; i < kN; ++i) {
-            const unsigned long long p = place_of(key_of(z[i]), id + i);
-            more += id + i < r.V && p >= mid && p <= hi;
-          }
-        });
-        const double sum = value(block_add(w.sum, sh));
-        more = __reduce_add_sync(0xffffffffu, more);
-        if (lane == 0) sh.num[warp] = more;
-        __syncthreads();
-        more = 0;
-        for (int x = 0; x < warps; ++x) more += sh.num[x];
-        if (!TWO && fabs(sum - target) <= 2.0 * err) {  // left to the sums of two floats
+        const Place mid = lo + (hi - lo) / 2;
+        Two sum{0.f, 0.f};
+        int more_n = 0;
+#pragma unroll 1
+        for (int i = from + lane; i < to; i += 32) {
+          const float z = element<K>(i);
+          const Place p = place_of(z, i);
+          if (p < mid) continue;
+          more_n += p <= hi;
+          weight(z, sum);
+        }
+        __syncwarp();
+        sum = block_add<K>(sum);
+        more_n = block_add<K>(more_n);
+        if (!TWO && fabsf(minus(sum, target)) <= err) {  // left to the sums of two floats
           *loose = INFINITY;
-          __syncthreads();
           return cut;
         }
-        if (sum >= target) {
+        if (!less(sum, target)) {
           lo = mid;
-          n = more;
+          n = more_n;
         } else {
           hi = mid - 1;
-          n -= more;
-          before_n += more;
+          n -= more_n;
+          before_n += more_n;
         }
       }
-      shift = max(0, 64 - __clzll(static_cast<long long>(hi - lo)) - 11);
+      linear = false;
       __syncthreads();
       continue;
     }
-    // few enough: by rank
-    for (int i = tid; i < n; i += nt) {
-      const unsigned long long p = r.list[i];
-      int rank = 0;
-      for (int k = 0; k < n; ++k) rank += r.list[k] > p;
-      r.sorted[rank] = p;
+    Listed mine_l[kListed<K>];
+    rank_list<K>(n, mine_l);
+    int kept;
+    if (MASS) {
+      float unsure;
+      kept = keep_listed<K>(n, mine_l, n, Cut{-INFINITY, V}, above, target, err, true, unsure);
+      *loose = unsure;
+    } else {
+      kept = min(count - ahead_n, n);
     }
+#pragma unroll 1
+    for (int e = 0; e < kListed<K>; ++e)
+      if (tid + e * K::NT < n && mine_l[e].rank == kept - 1) sh.cut = cut_at(mine_l[e].p);
     __syncthreads();
-    if (!MASS) {
-      const unsigned long long c = r.sorted[min(count - ahead_n, n) - 1];
-      __syncthreads();
-      return c;
-    }
-    if (warp == 0) {
-      Two sum = ahead_w;  // of all before this round's
-      int kept = 0;       // of the list
-      float unsure = 0.f;
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        Two w{0.f, 0.f};
-        if (i < n) {
-          const float z = z_of(static_cast<uint32_t>(r.sorted[i] >> 32));
-          float t;
-          w = TWO ? weight2(r.scale, sh.table, z) : Two{weight1(r.scale, z, t), 0.f};
-        }
-        Two incl = w;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const Two u = shfl_up(incl, o);
-          if (lane >= o) incl = add(incl, u);
-        }
-        incl = add(sum, incl);
-        // weight before this element
-        const double before = value(incl) - value(w);
-        const bool in = i < n && before < target;
-        kept += __popc(__ballot_sync(0xffffffffu, in));
-        if (!TWO && i < n && fabs(before - target) <= 2.0 * err) unsure += w.hi;
-        sum = {__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) unsure += __shfl_xor_sync(0xffffffffu, unsure, o);
-      if (lane == 0) {
-        // (with the margin the list's first is in; where nothing is ahead of it it is kept anyway)
-        sh.cut = r.sorted[max(kept, 1) - 1];
-        sh.loose = unsure;
-      }
-    }
-    __syncthreads();
-    *loose = sh.loose;
-    const unsigned long long c = sh.cut;
+    const Cut c = sh.cut;
     __syncthreads();
     return c;
   }
 }
 
-// Draws the row's token from the elements at or above `cut`, of those the first
-// that top_p leaves, and at or above cut_min.  False where fp32 sums do not
-// decide it.
-template <bool TWO, typename T>
-__device__ bool draw(const Row<T>& r, Shared& sh, unsigned long long cut, unsigned long long cut_min, float top_p,
-                     float u, int& token, float& logprob) {
-  constexpr int kN = Vec<T>::kN;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  float loose = 0.f;
-  if (top_p < 1.f) {
-    Weights<TWO, T> w(r, sh.table);
-    each_of_part(r, [&](const float (&z)[kN], int id) { w.add_vec(z, id, cut); });
-    const Two all = block_add(w.sum, sh);
-    const float err = TWO ? 0.f : block_add(w.error(), sh);
-    const unsigned long long c =
-        select<true, TWO>(r, sh, cut, 0, static_cast<double>(top_p) * value(all), err, &loose);
-    cut = max(cut, c);
-  }
-  cut = max(cut, cut_min);
-  // the sums of the warps' parts
-  Weights<TWO, T> w(r, sh.table);
-  each_of_part(r, [&](const float (&z)[kN], int id) { w.add_vec(z, id, cut); });
-  const float err = (TWO ? 0.f : block_add(w.error(), sh)) + loose;
-  Two part = warp_add(norm(w.sum.hi, w.sum.lo));
-  if (lane == 0) sh.part[warp] = part;
+// ------------------------------------------------------------ drawing
+// The first lane whose end passes the target, or the last that has weight where
+// rounding leaves none.
+__device__ __forceinline__ int first_past(Two end, Two target, bool has) {
+  const unsigned past = __ballot_sync(0xffffffffu, has && less(target, end));
+  if (past) return __ffs(static_cast<int>(past)) - 1;
+  const unsigned any = __ballot_sync(0xffffffffu, has);
+  return any ? 31 - __clz(static_cast<int>(any)) : 0;
+}
+
+__device__ __forceinline__ float logprob_of(const Scale& s, float z, Two all) {
+  float d, d_lo;
+  two_sum(0.5f * z, -s.half_max, d, d_lo);
+  const float t = d * s.c_hi, t_lo = fmaf(d, s.c_hi, -t) + fmaf(d, s.c_lo, d_lo * s.c_hi);
+  return 0.693147180559945f * (t + (t_lo - log2f(all.hi)));
+}
+
+// Draws from the `kept` first of the ranked list, whose weight is `all`, `loose`
+// of which may not belong.
+template <typename K>
+__device__ __forceinline__ bool draw_listed(int n, const Listed (&mine)[kListed<K>], int kept, Two all, float loose,
+                                            float u, int& token, float& logprob) {
+  Shared& sh = shared();
+  const Two target = times(all, u);
+  for (int i = threadIdx.x; i < kList; i += K::NT) sh.by_id[i] = {0.f, 0.f};
+  if (threadIdx.x == 0) sh.first = -1;
   __syncthreads();
-  part = lane < warps ? sh.part[lane] : Two{0.f, 0.f};
-  Two incl = part;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Two up = shfl_up(incl, o);
-    if (lane >= o) incl = add(incl, up);
-  }
-  const Two all{__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-  const double target = static_cast<double>(u) * value(all);
-  __syncthreads();
-  // the first part whose end passes the target (the last that has weight, where rounding leaves none)
-  auto first_past = [&](const Two& end, bool has) {
-    const unsigned past = __ballot_sync(0xffffffffu, has && value(end) > target);
-    if (past) return __ffs(static_cast<int>(past)) - 1;
-    const unsigned any = __ballot_sync(0xffffffffu, has);
-    return any ? 31 - __clz(static_cast<int>(any)) : 0;
-  };
-  const int w0 = first_past(incl, part.hi > 0.f);
-  Two before{__shfl_sync(0xffffffffu, incl.hi, (w0 + 31) & 31), __shfl_sync(0xffffffffu, incl.lo, (w0 + 31) & 31)};
-  if (w0 == 0) before = {0.f, 0.f};
-  // that part of the row, cut among the warps in the same way
-  const int from = w0 * r.per_warp, to = min(from + r.per_warp, r.vecs);
-  const int step = ((to - from + warps - 1) / warps + 31) / 32 * 32;
-  const int a = min(from + warp * step, to), b = min(a + step, to);
-  Weights<TWO, T> w1(r, sh.table);
-  each(r, a, b, [&](const float (&z)[kN], int id) { w1.add_vec(z, id, cut); });
-  part = warp_add(norm(w1.sum.hi, w1.sum.lo));
-  if (lane == 0) sh.part[warp] = part;
-  __syncthreads();
-  part = lane < warps ? sh.part[lane] : Two{0.f, 0.f};
-  incl = part;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const Two up = shfl_up(incl, o);
-    if (lane >= o) incl = add(incl, up);
-  }
-  incl = add(before, incl);
-  const int w2 = first_past(incl, part.hi > 0.f);
-  if (w2 > 0)
-    before = {__shfl_sync(0xffffffffu, incl.hi, w2 - 1), __shfl_sync(0xffffffffu, incl.lo, w2 - 1)};
-  if (warp == 0) {  // and that one, vector by vector
-    const int v0 = from + w2 * step, v1 = min(v0 + step, to);
-    int found = -1;
-    float margin = 0.f, z_found = 0.f;
-    for (int v = v0; v < v1; v += 32) {
-      Weights<TWO, T> one(r, sh.table);
-      each(r, v, min(v + 32, v1), [&](const float (&z)[kN], int id) { one.add_vec(z, id, cut); });
-      const Two mine = norm(one.sum.hi, one.sum.lo);
-      incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const Two up = shfl_up(incl, o);
-        if (lane >= o) incl = add(incl, up);
-      }
-      incl = add(before, incl);
-      const unsigned has = __ballot_sync(0xffffffffu, mine.hi > 0.f);
-      const unsigned past = __ballot_sync(0xffffffffu, mine.hi > 0.f && value(incl) > target);
-      // (the last one that has weight, as long as no later one passes the target)
-      const int l = past ? __ffs(static_cast<int>(past)) - 1 : has ? 31 - __clz(static_cast<int>(has)) : -1;
-      if (l >= 0) {
-        Two run{__shfl_sync(0xffffffffu, incl.hi, (l + 31) & 31), __shfl_sync(0xffffffffu, incl.lo, (l + 31) & 31)};
-        if (l == 0) run = before;
-        const int vec = v + l;
-        float z[kN];
-        Vec<T>::unpack(r.v[vec], z);
-#pragma unroll
-        for (int i = 0; i < kN; ++i) {
-          const int id = vec * kN + i;
-          if (id >= r.V || place_of(key_of(z[i]), id) < cut) continue;
-          float t;
-          const Two x = TWO ? weight2(r.scale, sh.table, z[i]) : Two{weight1(r.scale, z[i], t), 0.f};
-          if (!(x.hi > 0.f)) continue;
-          const double start = value(run);
-          run = add(run, x);
-          if (found < 0 || start <= target) {
-            found = id;
-            z_found = z[i];
-            // how far the random number is from the ends of this token's share (nothing is before the first)
-            margin = static_cast<float>(value(run) - target);
-            if (start > 0.0 || loose > 0.f) margin = fminf(margin, static_cast<float>(target - start));
-          }
-        }
-      }
-      before = {__shfl_sync(0xffffffffu, incl.hi, 31), __shfl_sync(0xffffffffu, incl.lo, 31)};
-      if (past) break;
+#pragma unroll 1
+  for (int e = 0; e < kListed<K>; ++e)
+    if (threadIdx.x + e * K::NT < n && mine[e].rank < kept) {
+      sh.by_id[mine[e].rank_id] = mine[e].w;
+      if (mine[e].w.hi > 0.f) atomicMax(&sh.first, mine[e].rank_id);
     }
-    if (lane == 0) {
-      sh.found = found;
-      const double t = (0.5 * z_found - static_cast<double>(r.scale.half_max)) *
-                       (static_cast<double>(r.scale.c_hi) + r.scale.c_lo);
-      sh.before = 0.693147180559945f * (static_cast<float>(t) - log2f(all.hi));
-      sh.loose = margin;
+  __syncthreads();
+  scan_list<K, true>();
+#pragma unroll 1
+  for (int e = 0; e < kListed<K>; ++e) {
+    if (threadIdx.x + e * K::NT >= n) break;
+    const Listed& x = mine[e];
+    if (x.rank >= kept || !(x.w.hi > 0.f)) continue;
+    const Two end = sh.by_id[x.rank_id];
+    Two before{0.f, 0.f};
+    if (x.rank_id > 0) before = sh.by_id[x.rank_id - 1];
+    // (rounding may leave the last one's end below the target)
+    if (!less(target, before) && (less(target, end) || x.rank_id == sh.first)) {
+      sh.found = id_of(x.p);
+      // how far the random number is from the ends of this token's share (nothing is before the first)
+      sh.margin = minus(end, target);
+      if (before.hi > 0.f || loose > 0.f) sh.margin = fminf(sh.margin, minus(target, before));
+      sh.logprob = logprob_of(sh.scale, z_of(x.p), all);
     }
   }
   __syncthreads();
   token = sh.found;
-  logprob = sh.before;
-  const float margin = sh.loose;
+  logprob = sh.logprob;
+  const float margin = sh.margin;
   __syncthreads();
-  return TWO || (margin > 2.f * err && loose <= 4e-6f * all.hi);
+  return loose == 0.f || (margin > 2.f * loose && loose <= 4e-6f * all.hi);
 }
 
-template <typename T, int NT, bool IN_SMEM>
-__global__ void __launch_bounds__(NT, NT == 1024 ? 1 : NT == 512 ? 2 : 8) sample_rows(const SampleArgs a) {
-  constexpr int kN = Vec<T>::kN;
-  extern __shared__ __align__(16) uint8_t s_raw[];
-  __shared__ Shared sh;
-  __shared__ int s_bad;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long m = blockIdx.x;
-  Row<T> r;
-  r.V = a.V;
-  r.vecs = (a.V + kN - 1) / kN;
-  r.per_warp = ((r.vecs + NT / 32 - 1) / (NT / 32) + 31) / 32 * 32;
-  r.hist = reinterpret_cast<uint32_t*>(s_raw);
-  r.sorted = reinterpret_cast<unsigned long long*>(s_raw);
-  r.list = reinterpret_cast<unsigned long long*>(s_raw + kBins * 4);
-  uint4* kept = reinterpret_cast<uint4*>(s_raw + kBins * 4 + kList * 8);
-  const uint4* global = reinterpret_cast<const uint4*>(static_cast<const T*>(a.logits) + m * a.ld);
-  r.v = IN_SMEM ? kept : global;
-  for (int i = tid; i < 65; i += NT) sh.table[i] = kExp2[i];
-  if (tid == 0) s_bad = 0;
-  griddep_wait();
-  griddep_launch_dependents();
-  // the row, its maximum, and whether it has a NaN or +inf
-  float top = -INFINITY;
-  bool bad = false;
-  {
-    const int from = min(warp * r.per_warp, r.vecs), to = min(from + r.per_warp, r.vecs);
-#pragma unroll 4
-    for (int v = from + lane; v < to; v += 32) {
-      const uint4 u = global[v];
-      if (IN_SMEM) kept[v] = u;
-      float z[kN];
-      Vec<T>::unpack(u, z);
+// The elements with z >= least that the cut keeps into the list; how many there
+// are.
+template <typename K>
+__device__ __noinline__ int list_from(Cut cut, float least) {
+  Shared& sh = shared();
+  if (threadIdx.x == 0) sh.count = 0;
+  __syncthreads();
+  const int V = sh.V;
+  int from, to;
+  part_of(threadIdx.x >> 5, from, to);
+#pragma unroll 1
+  for (int v = from + (threadIdx.x & 31); v < to; v += 32) {
+    float2 z[K::kN / 2];
+    vector_of<K>(v, V, z);
+    uint32_t in = 0;
 #pragma unroll
-      for (int i = 0; i < kN; ++i) {
-        if (v * kN + i >= a.V) z[i] = -INFINITY;
-        top = fmaxf(top, z[i]);
-        bad |= !(z[i] < INFINITY);
+    for (int i = 0; i < K::kN; ++i) in |= at(z, i) >= least ? 1u << i : 0u;
+    for (; in; in &= in - 1) {
+      const int id = v * K::kN + __ffs(static_cast<int>(in)) - 1;
+      const float x = element<K>(id);
+      if (id >= V || !cut.keeps(x, id)) continue;
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < kList) sh.list[at] = place_of(x, id);
+    }
+  }
+  __syncthreads();
+  return sh.count;
+}
+// The least z whose bin is at most b (of those the row has, or a step beside it:
+// bins fall as z grows).
+__device__ __forceinline__ float least_in_bin(const Scale& s, int b) {
+  // t = -(b + 1/2) / 64, and outward by more than its roundings
+  const float t = -(static_cast<float>(b) + 0.5f) * 0.015625f;
+  const float d = t / s.c_hi;
+  return 2.f * (s.half_max + d) - (fabsf(s.half_max) + fabsf(d)) * 1e-6f;
+}
+
+// The histogram of the weights of the elements kept by `cut`, and their sum.
+template <typename K, bool TWO>
+__device__ __forceinline__ Two weigh(Cut cut, float one) {
+  Shared& sh = shared();
+  for (int i = threadIdx.x; i < kBins; i += K::NT) sh.hist[i] = 0;
+  __syncthreads();
+  const Scale s = sh.scale;
+  const int V = sh.V;
+  Two all{0.f, 0.f};
+  int from, to;
+  part_of(threadIdx.x >> 5, from, to);
+  if constexpr (TWO) {
+#pragma unroll 1
+    for (int i = from * K::kN + (threadIdx.x & 31); i < min(to * K::kN, V); i += 32) {
+      const float z = element<K>(i);
+      if (!cut.keeps(z, i)) continue;
+      all = add(all, weight2(s, sh.table, z));
+      count_weights(sh.hist, make_float2(exponent(s, z), -INFINITY), one);
+    }
+  } else {
+    TwoPair sum{splat(0.f), splat(0.f)};
+    const bool whole = cut.z == -INFINITY;
+#pragma unroll 1
+    for (int v = from + (threadIdx.x & 31); v < to; v += 32) {
+      float2 z[K::kN / 2], t[K::kN / 2];
+      vector_of<K>(v, V, z);
+      exponents(s, z, t);
+      if (!whole) cut_off(cut, z, v * K::kN, t);
+      sum.add(sum_of(t));
+#pragma unroll
+      for (int i = 0; i < K::kN / 2; ++i) count_weights(sh.hist, t[i], one);
+    }
+    all = sum.total();
+  }
+  __syncwarp();
+  return block_add<K>(all);
+}
+
+// What a sub-bin is of: bins first .. last, cut into kBins.
+struct SubBins {
+  float edge_first, edge_last, top, per_t, middle;
+  __device__ __forceinline__ SubBins(int first, int last)
+      : edge_first(bin_edge(first)), edge_last(bin_edge(last)), top((static_cast<float>(first) - 0.5f) * 0.015625f),
+        per_t(64.f * static_cast<float>(kBins) / static_cast<float>(last - first + 1)),
+        middle(static_cast<float>(first + last) * 0.0078125f) {}
+  __device__ __forceinline__ int of(float t) const {
+    return max(0, min(kBins - 1, static_cast<int>((-t - top) * per_t)));
+  }
+};
+
+// This warp's part of the row: the weight of the elements kept by `cut` ahead of
+// bin `first`; those in bins first .. last are counted in sub-bins, in units of the
+// weight of their middle / one.
+template <typename K, bool TWO>
+__device__ __noinline__ Two sum_ahead(Cut cut, int first, int last, float one) {
+  Shared& sh = shared();
+  const Scale s = sh.scale;
+  const int V = sh.V;
+  const SubBins sub(first, last);
+  const bool whole = cut.z == -INFINITY;
+  int from, to;
+  part_of(threadIdx.x >> 5, from, to);
+  TwoPair pair{splat(0.f), splat(0.f)};
+  Two sum{0.f, 0.f};
+#pragma unroll 1
+  for (int v = from + (threadIdx.x & 31); v < to; v += 32) {
+    float2 z[K::kN / 2], t[K::kN / 2];
+    vector_of<K>(v, V, z);
+    exponents(s, z, t);
+    if (!whole) cut_off(cut, z, v * K::kN, t);
+    uint32_t in = 0, more = 0;
+#pragma unroll
+    for (int i = 0; i < K::kN; ++i) {
+      const float b = bin_at(at(t, i));
+      if (b <= sub.edge_last) {
+        if (b >= sub.edge_first)
+          in |= 1u << i;
+        else
+          more |= 1u << i;
+      }
+    }
+    if constexpr (TWO) {
+      for (; more; more &= more - 1)
+        sum = add(sum, weight2(s, sh.table, element<K>(v * K::kN + __ffs(static_cast<int>(more)) - 1)));
+    } else if (more) {
+#pragma unroll
+      for (int i = 0; i < K::kN / 2; ++i) {
+        if (!((more >> (2 * i)) & 1)) t[i].x = -INFINITY;
+        if (!((more >> (2 * i + 1)) & 1)) t[i].y = -INFINITY;
+      }
+      pair.add(sum_of(t));
+    }
+    for (; in; in &= in - 1) {
+      const float x = exponent(s, element<K>(v * K::kN + __ffs(static_cast<int>(in)) - 1));
+      atomicAdd(&sh.hist[sub.of(x)], __float2uint_rn(ex2_approx(x + sub.middle) * one));
+    }
+  }
+  __syncwarp();
+  return warp_add(TWO ? norm(sum.hi, sum.lo) : pair.total());
+}
+// And of those in bins first .. last the weight of the ones ahead of sub-bin
+// sub_first, and the ones up to sub_last into the list.
+template <typename K, bool TWO>
+__device__ __noinline__ Two list_border(Cut cut, int first, int last, int sub_first, int sub_last) {
+  Shared& sh = shared();
+  const Scale s = sh.scale;
+  const int V = sh.V;
+  const SubBins sub(first, last);
+  int from, to;
+  part_of(threadIdx.x >> 5, from, to);
+  Two sum{0.f, 0.f};
+#pragma unroll 1
+  for (int v = from + (threadIdx.x & 31); v < to; v += 32) {
+    float2 z[K::kN / 2], t[K::kN / 2];
+    vector_of<K>(v, V, z);
+    exponents(s, z, t);
+    uint32_t in = 0;
+#pragma unroll
+    for (int i = 0; i < K::kN; ++i) {
+      const float b = bin_at(at(t, i));
+      in |= b >= sub.edge_first && b <= sub.edge_last ? 1u << i : 0u;
+    }
+    for (; in; in &= in - 1) {
+      const int id = v * K::kN + __ffs(static_cast<int>(in)) - 1;
+      const float x = element<K>(id), tx = exponent(s, x);
+      if (!cut.keeps(x, id)) continue;
+      const int b = sub.of(tx);
+      if (b < sub_first) {
+        if constexpr (TWO)
+          sum = add(sum, weight2(s, sh.table, x));
+        else
+          add_to(sum, ex2_approx(tx));
+      } else if (b <= sub_last) {
+        const int place = atomicAdd(&sh.count, 1);
+        if (place < kList) sh.list[place] = place_of(x, id);
       }
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  __syncwarp();
+  return warp_add(norm(sum.hi, sum.lo));
+}
+
+// Draws the row's token from the elements kept by `cut`, of those the first that
+// top_p leaves, and kept by cut_min.  False where fp32 sums do not decide it.
+template <typename K, bool TWO>
+__device__ __noinline__ bool draw(Cut cut, float top_p, float u, int& token, float& logprob) {
+  Shared& sh = shared();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = sh.V;
+  const Cut cut_min = sh.cut_min;
+  float loose = 0.f;
+  bool summed = false;  // sh.part2 has the sums of the warps' parts
+  if (top_p < 1.f) {
+    const int digits = 31 - (32 - __clz(V));  // as many elements of 1.01 * 2^digits fit 32 bits
+    const float one = static_cast<float>(1u << min(digits, 15));
+    const Two all = weigh<K, TWO>(cut, one);
+    const float err = TWO ? 0.f : 2.f * error_of(all.hi, V);  // of a border's two sides
+    const Two target = times(all, top_p);
+    int first, last;
+    float count;
+    find_bins<K>(false, one, target.hi, kErrBin * all.hi + 0.5f * all.hi / one + err, first, last, count);
+    // (the border is far below the maximum, or among very different weights)
+    bool crowded = last >= kBins - 64 || last - first > 64;
+    if (!crowded && count * 1.02f <= kList / 2) {
+      const int n = list_from<K>(cut, least_in_bin(sh.scale, last));
+      if (n <= kList) {
+        __syncthreads();
+        Listed mine[kListed<K>];
+        rank_list<K>(n, mine);
+        const int kept = keep_listed<K>(n, mine, n, cut_min, Two{0.f, 0.f}, target, err, true, loose);
+        return draw_listed<K>(n, mine, kept, listed_sum(kept, Two{0.f, 0.f}), loose, u, token, logprob);
+      }
+      crowded = true;
+      __syncthreads();
+    } else if (!crowded) {
+      // the sums of the elements ahead of the border's bins, by parts; a finer histogram of those bins; then
+      // the sums with its bins ahead of the border, and the elements around it
+      for (int i = tid; i < kBins; i += K::NT) sh.hist[i] = 0;
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      Two part = sum_ahead<K, TWO>(cut, first, last, one);
+      if (lane == 0) sh.part2[warp] = part;
+      __syncthreads();
+      Two ahead = warp_add(lane < K::kWarps ? sh.part2[lane] : Two{0.f, 0.f});
+      const float unit = ex2_approx(static_cast<float>(first + last) * -0.0078125f);
+      int sub_first, sub_last;
+      // (the sum ahead is off by err, the histogram by its step and its sums' roundings)
+      const float margin = err + (1.f / one + 2e-6f) * all.hi;
+      find_bins<K>(true, one / unit, minus(target, ahead), margin, sub_first, sub_last, count);
+      if (sub_first >= kBins) sub_first = 0, sub_last = kBins - 1;
+      part = add(part, list_border<K, TWO>(cut, first, last, sub_first, sub_last));
+      __syncthreads();
+      if (lane == 0) sh.part2[warp] = part;
+      __syncthreads();
+      const int n = sh.count;
+      crowded = n == 0 || n > kList;
+      if (!crowded) {
+        ahead = warp_add(lane < K::kWarps ? sh.part2[lane] : Two{0.f, 0.f});
+        Listed mine[kListed<K>];
+        rank_list<K>(n, mine);
+        const int kept = keep_listed<K>(n, mine, n, cut_min, ahead, target, err, false, loose);
+        // the list's elements into their parts, and the cut: its last that stays, or just ahead of its first
+#pragma unroll 1
+        for (int e = 0; e < kListed<K>; ++e) {
+          if (tid + e * K::NT >= n) break;
+          if (mine[e].rank < kept) {
+            sh.by_id[mine[e].rank] = mine[e].w;
+            sh.list[mine[e].rank] = static_cast<Place>(id_of(mine[e].p) / K::kN / sh.per_warp);
+          }
+          if (mine[e].rank == 0) sh.last = cut_min.keeps(z_of(mine[e].p), id_of(mine[e].p));
+          if (kept > 0 ? mine[e].rank == kept - 1 : mine[e].rank == 0)
+            sh.cut = {z_of(mine[e].p), id_of(mine[e].p) - (kept > 0 ? 0 : 1)};
+        }
+        __syncthreads();
+        cut = sh.cut;
+        // (where min_p leaves out the list's first, it may leave out some of those ahead of it, too)
+        summed = sh.last != 0;
+        Two more{0.f, 0.f};
+#pragma unroll 1
+        for (int i = lane; i < kept; i += 32)
+          if (static_cast<int>(sh.list[i]) == warp) more = add(more, sh.by_id[i]);
+        __syncwarp();
+        more = warp_add(more);
+        if (lane == 0) sh.part2[warp] = add(part, more);
+        __syncwarp();
+      }
+    }
+    if (crowded) cut = select<K, true, TWO>(cut, 0, target, err, &loose);
+  }
+  if (!TWO && loose == INFINITY) return false;
+  if (!summed) {
+    if (cut_min.z > cut.z) {
+      cut = cut_min;
+      if (!TWO && loose > 0.f) return false;
+    }
+    // the sums of the warps' parts
+    int from, to;
+    part_of(warp, from, to);
+    const Two part = sum_vectors<K, TWO>(cut, from, to);
+    __syncthreads();
+    if (lane == 0) sh.part2[warp] = part;
+  }
   __syncthreads();
-  if (lane == 0) sh.aux[warp] = top;
-  if (bad) s_bad = 1;
+  Two part = lane < K::kWarps ? sh.part2[lane] : Two{0.f, 0.f};
+  Two incl = warp_incl(part);
+  const Two all = shfl(incl, 31), target = times(all, u);
+  // the first part whose end passes the target
+  const int w0 = first_past(incl, target, part.hi > 0.f);
+  Two before = shfl(incl, (w0 + 31) & 31);
+  if (w0 == 0) before = {0.f, 0.f};
+  // that part of the row, cut among the warps in the same way
+  int from, to;
+  part_of(w0, from, to);
+  const int step = ((to - from + K::kWarps - 1) / K::kWarps + 31) / 32 * 32;
+  part = sum_vectors<K, TWO>(cut, min(from + warp * step, to), min(from + (warp + 1) * step, to));
+  if (lane == 0) sh.part[warp] = part;
   __syncthreads();
-  top = lane < NT / 32 ? sh.aux[lane] : -INFINITY;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  top += 0.f;
-  bad = s_bad != 0 || top == -INFINITY;
+  if (warp == 0) {
+    const Scale s = sh.scale;
+    part = lane < K::kWarps ? sh.part[lane] : Two{0.f, 0.f};
+    incl = add(before, warp_incl(part));
+    const int w1 = first_past(incl, target, part.hi > 0.f);
+    if (w1 > 0) before = shfl(incl, w1 - 1);
+    // and that one, 32 vectors at a time
+    const int v0 = from + w1 * step, v1 = min(v0 + step, to);
+    int found = -1;
+    float margin = 0.f, z_found = 0.f;
+#pragma unroll 1
+    for (int v = v0; v < v1; v += 32) {
+      const Two mine = lane_sum<K, TWO>(s, V, cut, v, min(v + 32, v1));
+      __syncwarp();
+      incl = add(before, warp_incl(mine));
+      const unsigned has = __ballot_sync(0xffffffffu, mine.hi > 0.f);
+      const unsigned past = __ballot_sync(0xffffffffu, mine.hi > 0.f && less(target, incl));
+      // (the last one that has weight, as long as no later one passes the target)
+      const int l = past ? __ffs(static_cast<int>(past)) - 1 : has ? 31 - __clz(static_cast<int>(has)) : -1;
+      if (l >= 0) {
+        Two run = shfl(incl, (l + 31) & 31);
+        if (l == 0) run = before;
+        // lane i: its element i
+        const int id = (v + l) * K::kN + lane;
+        Two w{0.f, 0.f};
+        float z = -INFINITY;
+        if (lane < K::kN) {
+          z = element<K>(id);
+          if (cut.keeps(z, id)) w = TWO ? weight2(s, sh.table, z) : Two{ex2_approx(exponent(s, z)), 0.f};
+        }
+        __syncwarp();
+        const Two end = add(run, warp_incl(w));
+        Two start = shfl(end, (lane + 31) & 31);
+        if (lane == 0) start = run;
+        const int e = first_past(end, target, w.hi > 0.f);
+        if (lane == e && (found < 0 || !less(target, start))) {
+          found = id;
+          z_found = z;
+          margin = minus(end, target);
+          if (start.hi > 0.f || loose > 0.f) margin = fminf(margin, minus(target, start));
+        }
+        found = __shfl_sync(0xffffffffu, found, e);
+        z_found = __shfl_sync(0xffffffffu, z_found, e);
+        margin = __shfl_sync(0xffffffffu, margin, e);
+      }
+      before = shfl(incl, 31);
+      if (past) break;
+    }
+    if (lane == 0) {
+      sh.found = found;
+      sh.logprob = logprob_of(s, z_found, all);
+      sh.margin = margin;
+    }
+  }
+  __syncthreads();
+  token = sh.found;
+  logprob = sh.logprob;
+  const float margin = sh.margin;
+  __syncthreads();
+  return TWO || (margin > 2.f * (error_of(all.hi, V) + loose) && loose <= 4e-6f * all.hi);
+}
+
+// The least z that `count` of the threads' two largest logits reach, or a step
+// below it: at least as many of the row do.  NaN where that is not a number.
+template <typename K>
+__device__ __forceinline__ float reached_by(int count, float top, float z1, float z2) {
+  Shared& sh = shared();
+  // bins of equal width from the maximum down to the least of them
+  for (int i = threadIdx.x; i < kBins; i += K::NT) sh.hist[i] = 0;
+  if (threadIdx.x == 0) sh.hi = 0xffffffffu;
+  __syncthreads();
+  const uint32_t low = __reduce_min_sync(0xffffffffu, key_of(z2 > -INFINITY ? z2 : z1 > -INFINITY ? z1 : top));
+  if ((threadIdx.x & 31) == 0) atomicMin(&sh.hi, low);
+  __syncthreads();
+  const float width = (0.5f * top - 0.5f * z_of(sh.hi)) / static_cast<float>(kBins - 8);
+  auto bin = [&](float z) { return min(kBins - 2, static_cast<int>((0.5f * top - 0.5f * z) / width)); };
+  if (!(width > 0.f)) return NAN;
+  if (z1 > -INFINITY) atomicAdd(&sh.hist[bin(z1)], 1u);
+  if (z2 > -INFINITY) atomicAdd(&sh.hist[bin(z2)], 1u);
+  __syncthreads();
+  int first, last;
+  float n;
+  find_bins<K>(true, 1.f, static_cast<float>(count), 0.f, first, last, n);
+  if (first >= kBins || last >= kBins - 1) return NAN;
+  // the least of them in those bins
+  if (threadIdx.x == 0) sh.lo = 0xffffffffu;
+  __syncthreads();
+  uint32_t least = 0xffffffffu;
+  if (z1 > -INFINITY && bin(z1) <= last) least = key_of(z1);
+  if (z2 > -INFINITY && bin(z2) <= last) least = min(least, key_of(z2));
+  least = __reduce_min_sync(0xffffffffu, least);
+  if ((threadIdx.x & 31) == 0) atomicMin(&sh.lo, least);
+  __syncthreads();
+  const float z = z_of(sh.lo);
+  __syncthreads();
+  return z;
+}
+
+template <typename K>
+__global__ void __launch_bounds__(K::NT, K::NT >= 256 ? 1024 / K::NT : 7) sample_rows(const SampleArgs a) {
+  Shared& sh = shared();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const long long m = blockIdx.x;
+  const uint4* global = reinterpret_cast<const uint4*>(static_cast<const typename K::T*>(a.logits) + m * a.ld);
+  for (int i = tid; i < 65; i += K::NT) sh.table[i] = kExp2[i];
+  if (tid == 0) {
+    sh.bad = 0;
+    sh.global = global;
+    sh.V = a.V;
+    sh.vecs = (a.V + K::kN - 1) / K::kN;
+    sh.per_warp = ((sh.vecs + K::kWarps - 1) / K::kWarps + 31) / 32 * 32;
+  }
+  if (lane == 0) {
+    mbar_init(smem_u32(&sh.bar[warp]), 1);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
+  int from, to;  // this warp's part
+  part_of(warp, from, to);
+  const uint32_t bar = smem_u32(&sh.bar[warp]);
+  if (K::IN_SMEM && lane == 0 && from < to) {
+    mbar_arrive_expect_tx(bar, (to - from) * 16);
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(row<K>() + from)),
+                 "l"(global + from), "r"((to - from) * 16), "r"(bar)
+                 : "memory");
+  }
+  __syncwarp();
   const float temperature = a.temperature ? a.temperature[m] : 1.f, top_p = a.top_p ? a.top_p[m] : 1.f,
               min_p = a.min_p ? a.min_p[m] : 0.f, u = a.uniform[m];
   const int top_k = a.top_k ? a.top_k[m] : 0;
+  if (tid == K::NT - 1) {  // (one thread, while the row comes: 64-bit arithmetic is slow here)
+    // 2 log2(e) / temperature
+    const double c = 2.8853900817779268 / fmin(fmax(static_cast<double>(temperature), 0x1p-100), 0x1p100);
+    sh.scale.c_hi = __double2float_rd(c * (1.0 - 0x1p-25));  // (below c)
+    sh.scale.c_lo = static_cast<float>(c - sh.scale.c_hi);
+    if (min_p > 0.f) sh.least = static_cast<double>(temperature) * log(static_cast<double>(min_p));
+  }
+  __syncwarp();
+  // the row's maximum, and whether it has a NaN or +inf
+  float top = -INFINITY, second = -INFINITY;  // this thread's largest two
+  bool bad = false;
+  if (K::IN_SMEM && from < to && !mbar_wait(bar, 0)) {
+    record_error(a.err, kErrTimeout, kSiteSampleLoad);
+    (void)mbar_wait(bar, 0);  // (the copy must not outlive the CTA)
+    bad = true;
+  }
+#pragma unroll 2
+  for (int v = from + lane; v < to; v += 32) {
+    float2 z[K::kN / 2];
+    vector_of<K>(v, a.V, z);
+#pragma unroll
+    for (int i = 0; i < K::kN; ++i) {
+      second = fmaxf(second, fminf(top, at(z, i)));
+      top = fmaxf(top, at(z, i));
+      bad |= !(at(z, i) < INFINITY);
+    }
+  }
+  __syncwarp();
+  const float mine = top;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if (lane == 0) sh.aux[warp] = top;
+  if (bad) sh.bad = 1;
+  __syncthreads();
+  top = lane < K::kWarps ? sh.aux[lane] : -INFINITY;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  top += 0.f;
+  bad = sh.bad != 0 || top == -INFINITY;
   const bool wrong = !(temperature >= 0.f && temperature < INFINITY) || top_k < 0 || !(top_p >= 0.f) ||
                      !(min_p >= 0.f && min_p <= 1.f) || !(u >= 0.f && u < 1.f);
   int token = -1;
@@ -758,41 +1345,67 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : NT == 512 ? 2 : 8) sample
     if (tid == 0) record_error(a.err, kErrRange, kSiteSampleRow);
   } else if (!bad && (temperature == 0.f || top_k == 1 || top_p == 0.f)) {
     // the first of the order alone
-    __syncthreads();
     int first = a.V;
-    each_of_part(r, [&](const float (&z)[kN], int id) {
+#pragma unroll 1
+    for (int v = from + lane; v < to; v += 32) {
+      float2 z[K::kN / 2];
+      vector_of<K>(v, a.V, z);
 #pragma unroll
-      for (int i = kN - 1; i >= 0; --i)
-        if (z[i] == top) first = min(first, id + i);
-    });
+      for (int i = K::kN - 1; i >= 0; --i)
+        if (at(z, i) == top) first = min(first, v * K::kN + i);
+    }
+    __syncwarp();
     first = __reduce_min_sync(0xffffffffu, first);
     if (lane == 0) sh.num[warp] = first;
     __syncthreads();
-    for (int w = 0; w < NT / 32; ++w) first = min(first, sh.num[w]);
+    first = __reduce_min_sync(0xffffffffu, lane < K::kWarps ? sh.num[lane] : a.V);
     token = first;
     logprob = 0.f;
   } else if (!bad) {
-    // 2 log2(e) / temperature
-    const double c = 2.8853900817779268 / fmin(fmax(static_cast<double>(temperature), 0x1p-100), 0x1p100);
-    r.scale.half_max = 0.5f * top;
-    r.scale.c_hi = static_cast<float>(c);
-    r.scale.c_lo = static_cast<float>(c - r.scale.c_hi);
-    unsigned long long cut = 0, cut_min = 0;
-    if (min_p > 0.f) {
-      // the least z with z - max >= temperature log(min_p)
-      const double least = static_cast<double>(temperature) * log(static_cast<double>(min_p));
-      float z = static_cast<float>(top + least);
-      if (!(z >= -3.402823466e38f)) z = -3.402823466e38f;
-      auto in = [&](float x) { return static_cast<double>(x) - top >= least; };
-      // (one step at most, unless z is so small beside the maximum that the difference does not show it)
-      for (int i = 0; i < 4 && z > -3.402823466e38f && in(nextafterf(z, -INFINITY)); ++i) z = nextafterf(z, -INFINITY);
-      for (int i = 0; i < 4 && !in(z); ++i) z = nextafterf(z, INFINITY);
-      cut_min = static_cast<unsigned long long>(key_of(z)) << 32;
+    if (tid == 0) {
+      sh.scale.half_max = 0.5f * top;
+      sh.cut_min = {-INFINITY, a.V - 1};
+      if (min_p > 0.f) {
+        // the least z with z - max >= temperature log(min_p)
+        const double least = sh.least;
+        float z = static_cast<float>(top + least);
+        if (!(z >= -3.402823466e38f)) z = -3.402823466e38f;
+        auto in = [&](float x) { return static_cast<double>(x) - top >= least; };
+        // (one step at most, unless z is so small beside the maximum that the difference does not show it)
+        for (int i = 0; i < 4 && z > -3.402823466e38f && in(nextafterf(z, -INFINITY)); ++i) z = nextafterf(z, -INFINITY);
+        for (int i = 0; i < 4 && !in(z); ++i) z = nextafterf(z, INFINITY);
+        sh.cut_min.z = z;
+      }
     }
     __syncthreads();
-    if (top_k > 0 && top_k < a.V) cut = select<false, false>(r, sh, 0ull, top_k, 0.0, 0.f, nullptr);
-    if (!draw<false>(r, sh, cut, cut_min, top_p, u, token, logprob))
-      draw<true>(r, sh, cut, cut_min, top_p, u, token, logprob);
+    Cut cut{-INFINITY, a.V - 1};
+    bool done = false;
+    if (a.V <= kList || (top_k > 0 && top_k < a.V)) {
+      const int count = top_k > 0 ? min(top_k, a.V) : a.V;
+      int n = kList + 1;
+      // all that can stay into the list
+      if (a.V <= kList) {
+        n = list_from<K>(cut, -INFINITY);
+      } else if (count <= min(kList * 4 / 5, K::NT)) {
+        const float least = reached_by<K>(count, top, mine, second);
+        if (least == least) n = list_from<K>(cut, least);
+      }
+      if (n <= kList) {
+        __syncthreads();
+        Listed listed[kListed<K>];
+        rank_list<K>(n, listed);
+        const Two none{0.f, 0.f}, sum = listed_sum(min(count, n), none);
+        float loose;
+        const int kept = keep_listed<K>(n, listed, count, sh.cut_min, none,
+                                        top_p < 1.f ? times(sum, top_p) : Two{INFINITY, 0.f}, 0.f, true, loose);
+        draw_listed<K>(n, listed, kept, listed_sum(kept, none), 0.f, u, token, logprob);
+        done = true;
+      } else {
+        __syncthreads();
+        cut = select<K, false, false>(cut, count, Two{0.f, 0.f}, 0.f, nullptr);
+      }
+    }
+    if (!done && !draw<K, false>(cut, top_p, u, token, logprob)) draw<K, true>(cut, top_p, u, token, logprob);
   }
   if (tid == 0) {
     a.tokens[m] = token;
@@ -800,8 +1413,9 @@ __global__ void __launch_bounds__(NT, NT == 1024 ? 1 : NT == 512 ? 2 : 8) sample
   }
 }
 
-// Threads per row: many rows that are short keep the SM busy with several CTAs,
-// a row that fills its shared memory with one.
+// Threads per row: much of a row's time is latency (sums over the block, the list,
+// the last steps by one warp), which other CTAs on the SM fill; so short rows take
+// few threads each, and a row that fills the SM's shared memory all of them.
 template <typename T, int NT, bool IN_SMEM>
 cudaError_t launch_nt(const SampleArgs& a, int64_t M, size_t smem, cudaStream_t s) {
   static int configured[64] = {0};
@@ -809,20 +1423,22 @@ cudaError_t launch_nt(const SampleArgs& a, int64_t M, size_t smem, cudaStream_t 
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(sample_rows<T, NT, IN_SMEM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         227 * 1024 - 2048);
+    cudaError_t e = cudaFuncSetAttribute(sample_rows<Kind<T, NT, IN_SMEM>>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         227 * 1024);
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
-  return launch_pdl(sample_rows<T, NT, IN_SMEM>, static_cast<unsigned>(M), NT, smem, s, 0, a);
+  return launch_pdl(sample_rows<Kind<T, NT, IN_SMEM>>, static_cast<unsigned>(M), NT, smem, s, 0, a);
 }
 template <typename T>
 cudaError_t launch_type(const SampleArgs& a, int64_t M, cudaStream_t s) {
-  const size_t row = (static_cast<size_t>(a.V) * sizeof(T) + 15) / 16 * 16, fixed = kBins * 4 + kList * 8;
-  if (row <= 16 * 1024) return launch_nt<T, 128, true>(a, M, fixed + row, s);
-  if (row + fixed <= 112 * 1024 - 2048) return launch_nt<T, 512, true>(a, M, fixed + row, s);
-  if (row + fixed <= 227 * 1024 - 2048) return launch_nt<T, 1024, true>(a, M, fixed + row, s);
-  return launch_nt<T, 1024, false>(a, M, fixed, s);
+  const size_t need = kFixed + (static_cast<size_t>(a.V) * sizeof(T) + 15) / 16 * 16;
+  const size_t own = need + 1024;  // with what the system keeps of each CTA's
+  if (own <= 228 * 1024 / 5) return launch_nt<T, 128, true>(a, M, need, s);
+  if (own <= 228 * 1024 / 3) return launch_nt<T, 256, true>(a, M, need, s);
+  if (own <= 228 * 1024 / 2) return launch_nt<T, 512, true>(a, M, need, s);
+  if (own <= 228 * 1024) return launch_nt<T, 1024, true>(a, M, need, s);
+  return launch_nt<T, 1024, false>(a, M, kFixed, s);
 }
 
 }  // namespace
