@@ -133,33 +133,69 @@ __device__ __forceinline__ float error_of(float sum, int V) {
   return sum * (4.8e-7f + 8.4e-8f * fmaxf(log2f(static_cast<float>(V) / sum), 0.f)) + 1e-30f;
 }
 
-// The same to about 2^-45 of itself: 2^t = 2^n 2^(k/64) e^x with the integer n, the
-// nearest k and |x| <= ln 2 / 128, whose series ends with x^5.  Weights below 2^-100
-// count as 0.
-__device__ __forceinline__ Two weight2(const Scale& s, const float2* table, float z) {
-  const float a = 0.5f * z;
-  float d, d_lo;
-  two_sum(a, -s.half_max, d, d_lo);
-  const float t = d * s.c_hi;
-  // (below 2^-36 of the largest weight fp32 will do; below 2^-100 they count as 0)
-  if (!(t > -36.f)) return {t > -100.f ? ex2_approx(fmaf(d, s.c_lo, t)) : 0.f, 0.f};
-  const float t_lo = fmaf(d, s.c_hi, -t) + fmaf(d, s.c_lo, d_lo * s.c_hi);
-  const float n = rintf(t), f = t - n, k = rintf(64.f * f), g = fmaf(k, -0.015625f, f);
+// Two sums or weights of two floats each, on paired instructions.
+struct TwoPair {
+  float2 hi, lo;
+};
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return fma_f32x2(b, splat(-1.f), a); }
+__device__ __forceinline__ TwoPair norm2(float2 a, float2 b) {  // |a| >= |b|
+  const float2 s = add_f32x2(a, b);
+  return {s, sub2(b, sub2(s, a))};
+}
+__device__ __forceinline__ TwoPair two_sum2(float2 a, float2 b) {
+  const float2 s = add_f32x2(a, b), t = sub2(s, a);
+  return {s, add_f32x2(sub2(a, sub2(s, t)), sub2(b, t))};
+}
+__device__ __forceinline__ TwoPair add2(TwoPair a, TwoPair b) {
+  const TwoPair s = two_sum2(a.hi, b.hi);
+  return norm2(s.hi, add_f32x2(s.lo, add_f32x2(a.lo, b.lo)));
+}
+__device__ __forceinline__ Two total(TwoPair a) { return add(norm(a.hi.x, a.lo.x), norm(a.hi.y, a.lo.y)); }
+
+// The weights of two logits to about 2^-45 of themselves: 2^t = 2^n 2^(k/64) e^x with
+// the integer n, the nearest k and |x| <= ln 2 / 128, whose series ends with x^5.
+// Below 2^-36 of the largest weight fp32 will do; below 2^-100 they count as 0.
+__device__ __forceinline__ TwoPair weights2(const Scale& s, const float2* table, float2 z) {
+  const TwoPair d = two_sum2(mul_f32x2(z, splat(0.5f)), splat(-s.half_max));
+  const float2 t = mul_f32x2(d.hi, splat(s.c_hi));
+  if (!(fmaxf(t.x, t.y) > -36.f)) {
+    const float2 u = fma_f32x2(d.hi, splat(s.c_lo), t);
+    return {make_float2(t.x > -100.f ? ex2_approx(u.x) : 0.f, t.y > -100.f ? ex2_approx(u.y) : 0.f), splat(0.f)};
+  }
+  const float2 t_lo = add_f32x2(fma_f32x2(d.hi, splat(s.c_hi), make_float2(-t.x, -t.y)),
+                                fma_f32x2(d.hi, splat(s.c_lo), mul_f32x2(d.lo, splat(s.c_hi))));
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole numbers
+  const float2 nm = add_f32x2(t, splat(kRound)), n = add_f32x2(nm, splat(-kRound)), f = sub2(t, n);
+  const float2 km = fma_f32x2(f, splat(64.f), splat(kRound)), k = add_f32x2(km, splat(-kRound));
+  const float2 g = fma_f32x2(k, splat(-0.015625f), f);
   constexpr float kLn2Hi = 0.6931471824645996f, kLn2Lo = -1.9046542121259336e-09f;  // ln 2
-  const float x = g * kLn2Hi;
-  const float x_lo = fmaf(g, kLn2Hi, -x) + fmaf(g, kLn2Lo, t_lo * kLn2Hi);
-  const float h = 0.5f * x, q = h * x;
-  const float q_lo = fmaf(h, x, -q) + x * x_lo;
-  const float p = x * x * x * fmaf(x, fmaf(x, 1.f / 120.f, 1.f / 24.f), 1.f / 6.f);
-  const Two y = norm(x, q);  // e^x - 1
-  const float y_lo = y.lo + (x_lo + q_lo + p);
-  const float2 b = table[static_cast<int>(k) + 32];
-  const float m = b.x * y.hi;
-  const float m_lo = fmaf(b.x, y.hi, -m) + fmaf(b.x, y_lo, fmaf(b.y, y.hi, b.y));
-  const Two w = norm(b.x, m);
-  const Two r = norm(w.hi, w.lo + m_lo);
-  const float scale = __int_as_float((static_cast<int>(n) + 127) << 23);
-  return {r.hi * scale, r.lo * scale};
+  const float2 x = mul_f32x2(g, splat(kLn2Hi));
+  const float2 x_lo = add_f32x2(fma_f32x2(g, splat(kLn2Hi), make_float2(-x.x, -x.y)),
+                                fma_f32x2(g, splat(kLn2Lo), mul_f32x2(t_lo, splat(kLn2Hi))));
+  const float2 h = mul_f32x2(x, splat(0.5f)), q = mul_f32x2(h, x);
+  const float2 q_lo = add_f32x2(fma_f32x2(h, x, make_float2(-q.x, -q.y)), mul_f32x2(x, x_lo));
+  const float2 c = fma_f32x2(x, fma_f32x2(x, splat(1.f / 120.f), splat(1.f / 24.f)), splat(1.f / 6.f));
+  const float2 p = mul_f32x2(mul_f32x2(x, mul_f32x2(x, x)), c);
+  const TwoPair y = norm2(x, q);  // e^x - 1
+  const float2 y_lo = add_f32x2(y.lo, add_f32x2(x_lo, add_f32x2(q_lo, p)));
+  const float2 b0 = table[min(64, max(0, __float_as_int(km.x) - 0x4b400000 + 32))],
+               b1 = table[min(64, max(0, __float_as_int(km.y) - 0x4b400000 + 32))];
+  const float2 b = make_float2(b0.x, b1.x), b_lo = make_float2(b0.y, b1.y);
+  const float2 m = mul_f32x2(b, y.hi);
+  const float2 m_lo = add_f32x2(fma_f32x2(b, y.hi, make_float2(-m.x, -m.y)),
+                                fma_f32x2(b, y_lo, fma_f32x2(b_lo, y.hi, b_lo)));
+  const TwoPair w = norm2(b, m), r = norm2(w.hi, add_f32x2(w.lo, m_lo));
+  // (a pair may be of one such element and one that is -inf or far below)
+  const float2 scale = make_float2(t.x > -100.f ? __int_as_float((__float_as_int(nm.x) - 0x4b400000 + 127) << 23) : 0.f,
+                                   t.y > -100.f ? __int_as_float((__float_as_int(nm.y) - 0x4b400000 + 127) << 23) : 0.f);
+  TwoPair out{mul_f32x2(r.hi, scale), mul_f32x2(r.lo, scale)};
+  if (!(t.x > -100.f)) out.hi.x = out.lo.x = 0.f;
+  if (!(t.y > -100.f)) out.hi.y = out.lo.y = 0.f;
+  return out;
+}
+__device__ __forceinline__ Two weight2(const Scale& s, const float2* table, float z) {
+  const TwoPair w = weights2(s, table, splat(z));
+  return {w.hi.x, w.lo.x};
 }
 
 // Elements in order: larger z first, lowest id first on ties, as one number
@@ -241,6 +277,7 @@ struct Shared {
   int num[32];
   uint32_t lo, hi;
   int count, first, last, found, bad;
+  int how, bins[4];  // of draw: where top_p's border was found
   Cut cut, cut_min;
   float loose, margin, logprob;
   Scale scale;
@@ -293,21 +330,11 @@ __device__ __forceinline__ void part_of(int warp, int& from, int& to) {
   to = min(from + shared().per_warp, shared().vecs);
 }
 
-// A lane's sum in two floats, of the even elements and of the odd ones.
-struct TwoPair {
-  float2 hi, lo;
-  __device__ __forceinline__ Two total() const {
-    Two a = norm(hi.x, lo.x);
-    return add(a, norm(hi.y, lo.y));
-  }
-  __device__ __forceinline__ void add(float2 x) {
-    const float2 s = add_f32x2(hi, x), t = fma_f32x2(hi, splat(-1.f), s);  // s - hi
-    const float2 e = add_f32x2(fma_f32x2(fma_f32x2(t, splat(-1.f), s), splat(-1.f), hi), fma_f32x2(t, splat(-1.f), x));
-    hi = s;
-    lo = add_f32x2(lo, e);
-  }
-  __device__ __forceinline__ Two add(Two a, Two b) const { return gpt2::add(a, b); }
-};
+// Adds a pair to the sums of the even elements and of the odd ones.
+__device__ __forceinline__ void add_to(TwoPair& sum, float2 x) {
+  const TwoPair s = two_sum2(sum.hi, x);
+  sum = {s.hi, add_f32x2(sum.lo, s.lo)};
+}
 // Weights 2^t of a vector's elements, added up pair by pair.
 template <int N>
 __device__ __forceinline__ float2 sum_of(const float2 (&t)[N]) {
@@ -339,23 +366,31 @@ __device__ __forceinline__ void add_to(Two& sum, float x) {
   two_sum(sum.hi, x, s, e);
   sum = {s, sum.lo + e};
 }
+// Elements i and i + 1 (i even), -inf behind the row's end.
+template <typename K>
+__device__ __forceinline__ float2 elements(int i, int V) {
+  float2 z;
+  if constexpr (sizeof(typename K::T) == 4)
+    z = reinterpret_cast<const float2*>(row<K>())[i >> 1];
+  else
+    z = Type16<typename K::T>::unpack2(reinterpret_cast<const uint32_t*>(row<K>())[i >> 1]);
+  return make_float2(i < V ? z.x : -INFINITY, i + 1 < V ? z.y : -INFINITY);
+}
 // Weight of the elements of vectors from .. to - 1 that the cut keeps, a warp's
 // lanes side by side: a lane's.
 template <typename K, bool TWO>
 __device__ __forceinline__ Two lane_sum(const Scale& s, int V, const Cut& cut, int from, int to) {
   const int lane = threadIdx.x & 31;
+  TwoPair sum{splat(0.f), splat(0.f)};
   if constexpr (TWO) {
-    Two sum{0.f, 0.f};
 #pragma unroll 1
-    for (int v = from + lane; v < to; v += 32)
-#pragma unroll 1
-      for (int i = v * K::kN; i < (v + 1) * K::kN; ++i) {
-        const float z = element<K>(i);
-        if (cut.keeps(z, i)) sum = add(sum, weight2(s, shared().table, z));
-      }
-    return norm(sum.hi, sum.lo);
+    for (int i = from * K::kN + 2 * lane; i < to * K::kN; i += 64) {
+      float2 z = elements<K>(i, V);
+      if (!cut.keeps(z.x, i)) z.x = -INFINITY;
+      if (!cut.keeps(z.y, i + 1)) z.y = -INFINITY;
+      sum = add2(sum, weights2(s, shared().table, z));
+    }
   } else {
-    TwoPair sum{splat(0.f), splat(0.f)};
     const bool whole = cut.z == -INFINITY;  // (what is -inf weighs nothing)
 #pragma unroll 2
     for (int v = from + lane; v < to; v += 32) {
@@ -363,12 +398,33 @@ __device__ __forceinline__ Two lane_sum(const Scale& s, int V, const Cut& cut, i
       vector_of<K>(v, V, z);
       exponents(s, z, t);
       if (!whole) cut_off(cut, z, v * K::kN, t);
-      sum.add(sum_of(t));
+      add_to(sum, sum_of(t));
     }
-    return sum.total();
   }
+  return total(sum);
 }
-// The same over the lanes.
+// The weight of vector v's elements that the cut keeps.
+template <typename K, bool TWO>
+__device__ __forceinline__ Two vector_sum(const Scale& s, int V, const Cut& cut, int v) {
+  TwoPair sum{splat(0.f), splat(0.f)};
+  if constexpr (TWO) {
+#pragma unroll 1
+    for (int i = v * K::kN; i < (v + 1) * K::kN; i += 2) {
+      float2 z = elements<K>(i, V);
+      if (!cut.keeps(z.x, i)) z.x = -INFINITY;
+      if (!cut.keeps(z.y, i + 1)) z.y = -INFINITY;
+      sum = add2(sum, weights2(s, shared().table, z));
+    }
+  } else {
+    float2 z[K::kN / 2], t[K::kN / 2];
+    vector_of<K>(v, V, z);
+    exponents(s, z, t);
+    cut_off(cut, z, v * K::kN, t);
+    add_to(sum, sum_of(t));
+  }
+  return total(sum);
+}
+// lane_sum over the lanes.
 template <typename K, bool TWO>
 __device__ __noinline__ Two sum_vectors(Cut cut, int from, int to) {
   const Two sum = lane_sum<K, TWO>(shared().scale, shared().V, cut, from, to);
@@ -869,7 +925,7 @@ __device__ __forceinline__ bool draw_listed(int n, const Listed (&mine)[kListed<
   logprob = sh.logprob;
   const float margin = sh.margin;
   __syncthreads();
-  return loose == 0.f || (margin > 2.f * loose && loose <= 4e-6f * all.hi);
+  return loose == 0.f || (margin > 2.f * loose && loose <= 1e-5f * all.hi);
 }
 
 // The elements with z >= least that the cut keeps into the list; how many there
@@ -910,41 +966,29 @@ __device__ __forceinline__ float least_in_bin(const Scale& s, int b) {
 }
 
 // The histogram of the weights of the elements kept by `cut`, and their sum.
-template <typename K, bool TWO>
+template <typename K>
 __device__ __forceinline__ Two weigh(Cut cut, float one) {
   Shared& sh = shared();
   for (int i = threadIdx.x; i < kBins; i += K::NT) sh.hist[i] = 0;
   __syncthreads();
   const Scale s = sh.scale;
   const int V = sh.V;
-  Two all{0.f, 0.f};
   int from, to;
   part_of(threadIdx.x >> 5, from, to);
-  if constexpr (TWO) {
+  TwoPair sum{splat(0.f), splat(0.f)};
+  const bool whole = cut.z == -INFINITY;
 #pragma unroll 1
-    for (int i = from * K::kN + (threadIdx.x & 31); i < min(to * K::kN, V); i += 32) {
-      const float z = element<K>(i);
-      if (!cut.keeps(z, i)) continue;
-      all = add(all, weight2(s, sh.table, z));
-      count_weights(sh.hist, make_float2(exponent(s, z), -INFINITY), one);
-    }
-  } else {
-    TwoPair sum{splat(0.f), splat(0.f)};
-    const bool whole = cut.z == -INFINITY;
-#pragma unroll 1
-    for (int v = from + (threadIdx.x & 31); v < to; v += 32) {
-      float2 z[K::kN / 2], t[K::kN / 2];
-      vector_of<K>(v, V, z);
-      exponents(s, z, t);
-      if (!whole) cut_off(cut, z, v * K::kN, t);
-      sum.add(sum_of(t));
+  for (int v = from + (threadIdx.x & 31); v < to; v += 32) {
+    float2 z[K::kN / 2], t[K::kN / 2];
+    vector_of<K>(v, V, z);
+    exponents(s, z, t);
+    if (!whole) cut_off(cut, z, v * K::kN, t);
+    add_to(sum, sum_of(t));
 #pragma unroll
-      for (int i = 0; i < K::kN / 2; ++i) count_weights(sh.hist, t[i], one);
-    }
-    all = sum.total();
+    for (int i = 0; i < K::kN / 2; ++i) count_weights(sh.hist, t[i], one);
   }
   __syncwarp();
-  return block_add<K>(all);
+  return block_add<K>(total(sum));
 }
 
 // What a sub-bin is of: bins first .. last, cut into kBins.
@@ -962,7 +1006,7 @@ struct SubBins {
 // This warp's part of the row: the weight of the elements kept by `cut` ahead of
 // bin `first`; those in bins first .. last are counted in sub-bins, in units of the
 // weight of their middle / one.
-template <typename K, bool TWO>
+template <typename K>
 __device__ __noinline__ Two sum_ahead(Cut cut, int first, int last, float one) {
   Shared& sh = shared();
   const Scale s = sh.scale;
@@ -971,8 +1015,7 @@ __device__ __noinline__ Two sum_ahead(Cut cut, int first, int last, float one) {
   const bool whole = cut.z == -INFINITY;
   int from, to;
   part_of(threadIdx.x >> 5, from, to);
-  TwoPair pair{splat(0.f), splat(0.f)};
-  Two sum{0.f, 0.f};
+  TwoPair sum{splat(0.f), splat(0.f)};
 #pragma unroll 1
   for (int v = from + (threadIdx.x & 31); v < to; v += 32) {
     float2 z[K::kN / 2], t[K::kN / 2];
@@ -990,16 +1033,13 @@ __device__ __noinline__ Two sum_ahead(Cut cut, int first, int last, float one) {
           more |= 1u << i;
       }
     }
-    if constexpr (TWO) {
-      for (; more; more &= more - 1)
-        sum = add(sum, weight2(s, sh.table, element<K>(v * K::kN + __ffs(static_cast<int>(more)) - 1)));
-    } else if (more) {
+    if (more) {
 #pragma unroll
       for (int i = 0; i < K::kN / 2; ++i) {
         if (!((more >> (2 * i)) & 1)) t[i].x = -INFINITY;
         if (!((more >> (2 * i + 1)) & 1)) t[i].y = -INFINITY;
       }
-      pair.add(sum_of(t));
+      add_to(sum, sum_of(t));
     }
     for (; in; in &= in - 1) {
       const float x = exponent(s, element<K>(v * K::kN + __ffs(static_cast<int>(in)) - 1));
@@ -1007,11 +1047,11 @@ __device__ __noinline__ Two sum_ahead(Cut cut, int first, int last, float one) {
     }
   }
   __syncwarp();
-  return warp_add(TWO ? norm(sum.hi, sum.lo) : pair.total());
+  return warp_add(total(sum));
 }
 // And of those in bins first .. last the weight of the ones ahead of sub-bin
 // sub_first, and the ones up to sub_last into the list.
-template <typename K, bool TWO>
+template <typename K>
 __device__ __noinline__ Two list_border(Cut cut, int first, int last, int sub_first, int sub_last) {
   Shared& sh = shared();
   const Scale s = sh.scale;
@@ -1037,10 +1077,7 @@ __device__ __noinline__ Two list_border(Cut cut, int first, int last, int sub_fi
       if (!cut.keeps(x, id)) continue;
       const int b = sub.of(tx);
       if (b < sub_first) {
-        if constexpr (TWO)
-          sum = add(sum, weight2(s, sh.table, x));
-        else
-          add_to(sum, ex2_approx(tx));
+        add_to(sum, ex2_approx(tx));
       } else if (b <= sub_last) {
         const int place = atomicAdd(&sh.count, 1);
         if (place < kList) sh.list[place] = place_of(x, id);
@@ -1050,6 +1087,36 @@ __device__ __noinline__ Two list_border(Cut cut, int first, int last, int sub_fi
   __syncwarp();
   return warp_add(norm(sum.hi, sum.lo));
 }
+// The sums of both in two floats each, and in `rest` the weight of the others.
+template <typename K>
+__device__ __noinline__ Two sum_both(Cut cut, int first, int last, int sub_first, Two& rest) {
+  const Scale s = shared().scale;
+  const int V = shared().V;
+  const SubBins sub(first, last);
+  int from, to;
+  part_of(threadIdx.x >> 5, from, to);
+  TwoPair ahead{splat(0.f), splat(0.f)}, others = ahead;
+#pragma unroll 1
+  for (int i = from * K::kN + 2 * (threadIdx.x & 31); i < to * K::kN; i += 64) {
+    float2 z = elements<K>(i, V);
+    if (!cut.keeps(z.x, i)) z.x = -INFINITY;
+    if (!cut.keeps(z.y, i + 1)) z.y = -INFINITY;
+    const TwoPair w = weights2(s, shared().table, z);
+    auto is_ahead = [&](float x) {
+      const float t = exponent(s, x), b = bin_at(t);
+      return b < sub.edge_first || (b <= sub.edge_last && sub.of(t) < sub_first);
+    };
+    const bool x = is_ahead(z.x), y = is_ahead(z.y);
+    ahead = add2(ahead, {make_float2(x ? w.hi.x : 0.f, y ? w.hi.y : 0.f), make_float2(x ? w.lo.x : 0.f, y ? w.lo.y : 0.f)});
+    others = add2(others, {make_float2(x ? 0.f : w.hi.x, y ? 0.f : w.hi.y), make_float2(x ? 0.f : w.lo.x, y ? 0.f : w.lo.y)});
+  }
+  __syncwarp();
+  rest = warp_add(total(others));
+  return warp_add(total(ahead));
+}
+
+// How the elements that top_p keeps are found.
+enum { kFew, kMany, kCrowded };
 
 // Draws the row's token from the elements kept by `cut`, of those the first that
 // top_p leaves, and kept by cut_min.  False where fp32 sums do not decide it.
@@ -1061,17 +1128,58 @@ __device__ __noinline__ bool draw(Cut cut, float top_p, float u, int& token, flo
   float loose = 0.f;
   bool summed = false;  // sh.part2 has the sums of the warps' parts
   if (top_p < 1.f) {
-    const int digits = 31 - (32 - __clz(V));  // as many elements of 1.01 * 2^digits fit 32 bits
-    const float one = static_cast<float>(1u << min(digits, 15));
-    const Two all = weigh<K, TWO>(cut, one);
-    const float err = TWO ? 0.f : 2.f * error_of(all.hi, V);  // of a border's two sides
-    const Two target = times(all, top_p);
-    int first, last;
-    float count;
-    find_bins<K>(false, one, target.hi, kErrBin * all.hi + 0.5f * all.hi / one + err, first, last, count);
-    // (the border is far below the maximum, or among very different weights)
-    bool crowded = last >= kBins - 64 || last - first > 64;
-    if (!crowded && count * 1.02f <= kList / 2) {
+    // where the border is: found in fp32, with the margin that its sums need
+    int first, last, sub_first = 0, sub_last = kBins - 1;
+    Two all, part{0.f, 0.f}, target;
+    float err = 0.f;
+    if constexpr (!TWO) {
+      const int digits = 31 - (32 - __clz(V));  // as many elements of 1.01 * 2^digits fit 32 bits
+      const float one = static_cast<float>(1u << min(digits, 15));
+      all = weigh<K>(cut, one);
+      err = 2.f * error_of(all.hi, V);  // of a border's two sides
+      target = times(all, top_p);
+      float count;
+      find_bins<K>(false, one, target.hi, kErrBin * all.hi + 0.5f * all.hi / one + err, first, last, count);
+      // (the border is far below the maximum, or among very different weights)
+      int how = last >= kBins - 64 || last - first > 64 ? kCrowded : count * 1.02f <= kList / 2 ? kFew : kMany;
+      if (how == kMany) {
+        // the sums of the elements ahead of the border's bins, by parts; a finer histogram of those bins; then
+        // the sums with its bins ahead of the border, and the elements around it
+        for (int i = tid; i < kBins; i += K::NT) sh.hist[i] = 0;
+        if (tid == 0) sh.count = 0;
+        __syncthreads();
+        part = sum_ahead<K>(cut, first, last, one);
+        if (lane == 0) sh.part2[warp] = part;
+        __syncthreads();
+        const Two ahead = warp_add(lane < K::kWarps ? sh.part2[lane] : Two{0.f, 0.f});
+        const float unit = ex2_approx(static_cast<float>(first + last) * -0.0078125f);
+        // (the sum ahead is off by err, the histogram by its step and its sums' roundings)
+        const float margin = err + (1.f / one + 2e-6f) * all.hi;
+        find_bins<K>(true, one / unit, minus(target, ahead), margin, sub_first, sub_last, count);
+        if (sub_first >= kBins) sub_first = 0, sub_last = kBins - 1;
+      }
+      if (tid == 0) {
+        sh.how = how;
+        sh.bins[0] = first, sh.bins[1] = last, sh.bins[2] = sub_first, sh.bins[3] = sub_last;
+      }
+    } else {
+      first = sh.bins[0], last = sh.bins[1], sub_first = sh.bins[2], sub_last = sh.bins[3];
+      if (sh.how == kMany) {
+        Two rest;
+        part = sum_both<K>(cut, first, last, sub_first, rest);
+        all = block_add<K>(lane == 0 ? add(part, rest) : Two{0.f, 0.f});
+        if (tid == 0) sh.count = 0;
+      } else {
+        int from, to;
+        part_of(warp, from, to);
+        all = block_add<K>(lane_sum<K, true>(sh.scale, V, cut, from, to));
+      }
+      target = times(all, top_p);
+    }
+    __syncthreads();
+    const int how = sh.how;
+    bool crowded = how == kCrowded;
+    if (how == kFew) {
       const int n = list_from<K>(cut, least_in_bin(sh.scale, last));
       if (n <= kList) {
         __syncthreads();
@@ -1082,30 +1190,16 @@ __device__ __noinline__ bool draw(Cut cut, float top_p, float u, int& token, flo
       }
       crowded = true;
       __syncthreads();
-    } else if (!crowded) {
-      // the sums of the elements ahead of the border's bins, by parts; a finer histogram of those bins; then
-      // the sums with its bins ahead of the border, and the elements around it
-      for (int i = tid; i < kBins; i += K::NT) sh.hist[i] = 0;
-      if (tid == 0) sh.count = 0;
-      __syncthreads();
-      Two part = sum_ahead<K, TWO>(cut, first, last, one);
-      if (lane == 0) sh.part2[warp] = part;
-      __syncthreads();
-      Two ahead = warp_add(lane < K::kWarps ? sh.part2[lane] : Two{0.f, 0.f});
-      const float unit = ex2_approx(static_cast<float>(first + last) * -0.0078125f);
-      int sub_first, sub_last;
-      // (the sum ahead is off by err, the histogram by its step and its sums' roundings)
-      const float margin = err + (1.f / one + 2e-6f) * all.hi;
-      find_bins<K>(true, one / unit, minus(target, ahead), margin, sub_first, sub_last, count);
-      if (sub_first >= kBins) sub_first = 0, sub_last = kBins - 1;
-      part = add(part, list_border<K, TWO>(cut, first, last, sub_first, sub_last));
+    } else if (how == kMany) {
+      const Two more_part = list_border<K>(cut, first, last, sub_first, sub_last);
+      if (!TWO) part = add(part, more_part);
       __syncthreads();
       if (lane == 0) sh.part2[warp] = part;
       __syncthreads();
       const int n = sh.count;
       crowded = n == 0 || n > kList;
       if (!crowded) {
-        ahead = warp_add(lane < K::kWarps ? sh.part2[lane] : Two{0.f, 0.f});
+        const Two ahead = warp_add(lane < K::kWarps ? sh.part2[lane] : Two{0.f, 0.f});
         Listed mine[kListed<K>];
         rank_list<K>(n, mine);
         const int kept = keep_listed<K>(n, mine, n, cut_min, ahead, target, err, false, loose);
@@ -1177,7 +1271,9 @@ __device__ __noinline__ bool draw(Cut cut, float top_p, float u, int& token, flo
     float margin = 0.f, z_found = 0.f;
 #pragma unroll 1
     for (int v = v0; v < v1; v += 32) {
-      const Two mine = lane_sum<K, TWO>(s, V, cut, v, min(v + 32, v1));
+      // (each lane its own vector)
+      Two mine{0.f, 0.f};
+      if (v + lane < v1) mine = vector_sum<K, TWO>(s, V, cut, v + lane);
       __syncwarp();
       incl = add(before, warp_incl(mine));
       const unsigned has = __ballot_sync(0xffffffffu, mine.hi > 0.f);
@@ -1224,7 +1320,7 @@ __device__ __noinline__ bool draw(Cut cut, float top_p, float u, int& token, flo
   logprob = sh.logprob;
   const float margin = sh.margin;
   __syncthreads();
-  return TWO || (margin > 2.f * (error_of(all.hi, V) + loose) && loose <= 4e-6f * all.hi);
+  return TWO || (margin > 2.f * (error_of(all.hi, V) + loose) && loose <= 1e-5f * all.hi);
 }
 
 // The least z that `count` of the threads' two largest logits reach, or a step
