@@ -12,12 +12,12 @@
 // The n * (n_head / n_kv_head) query rows of one key-value head share its keys
 // and values, which are read once for a block of up to 64 rows.  A position (256
 // bytes) takes 4 * 64 flop a row: 64 rows are 64 flop a byte, a quarter of what
-// the tensor cores need to be the limit, and what a row costs beside its
-// products (two roundings of p, its exponential, maximum and sum: about nine
-// instructions a score and lane) is what the rows pay for on either kind of
-// matrix instruction.  So the products are mma.sync m16n8k16 with rows in blocks
-// of 16, whose results stay in registers, and the layout serves the loads: each
-// warp runs its own ring of TMA boxes (16 rows of K, 16 of V).
+// the tensor cores need to be the limit.  The products are mma.sync m16n8k16 with
+// 16 rows to a warp, whose scores and results stay in registers; with p as the sum
+// of two 16-bit numbers they take 192 cycles of an SM's four tensor pipes for 64
+// rows and 16 positions, which come from HBM in 170.  Up to 16 rows, the warps of a
+// CTA take tiles of positions in turn, each from a ring of TMA boxes of its own;
+// with more rows two or four warps share a ring, each with 16 rows of the block.
 #include <algorithm>
 
 #include "internal.h"
@@ -32,20 +32,20 @@ constexpr int kTile = 16;  // positions per tile; page sizes are multiples of it
 constexpr int kWarps = 4;  // warps per CTA; they take a piece's tiles in turn
 constexpr int kThreads = kWarps * 32;
 constexpr int kBoxBytes = kTile * kHd * 2;
-constexpr int kStageBytes = 2 * kBoxBytes;  // K, then V
+constexpr int kTileBytes = 2 * kBoxBytes;  // K, then V
 constexpr int kMinRun = 2 * kWarps;         // tiles per CTA at least
+constexpr int kCtasPerSm = 4;
 
-// NB: blocks of 16 query rows.  RIDE: up to 8 rows in one block, whose other 8
-// carry the rounding remainder of p.
-template <int NB, bool RIDE>
+// WR: warps that share a ring, with 16 query rows each.  RIDE: up to 8 rows in
+// all, whose other 8 carry the rounding remainder of p.
+template <int WR, bool RIDE>
 struct Shape {
-  static constexpr int kRows = RIDE ? 8 : 16 * NB;
-  // a warp's result (fp32 rows of 64) takes the place of its ring
-  static constexpr int kStages = NB >= 4 ? 4 : 2;
-  static constexpr int kCtasPerSm = NB >= 4 ? 2 : NB == 2 ? 3 : 4;
-  static constexpr int kRingBytes = kStages * kStageBytes;
-  static constexpr bool kSharedQ = NB >= 4;  // the query rows in shared memory, not in registers
-  static_assert(kRingBytes >= kRows * kHd * 4, "a warp's result fits its ring");
+  static constexpr int kRows = RIDE ? 8 : 16 * WR;
+  static constexpr int kRings = kWarps / WR;
+  static constexpr int kUnits = WR == 1 ? 1 : 2;       // tiles that a warp takes at a time
+  static constexpr int kStages = WR == 1 ? 2 : 3 * WR / 2;  // of each ring: 128 or 192 KB of them on an SM
+  static constexpr int kSlotBytes = kUnits * kTileBytes;
+  static constexpr int kRingBytes = kStages * kSlotBytes;
 };
 
 template <typename T16>
@@ -171,21 +171,21 @@ __device__ __forceinline__ void build_tree(const DraftArgs<T16>& a, int b, const
   }
 }
 
-// A warp's ring of tiles.
+// A ring of tiles.
 struct Ring {
   const CUtensorMap* map;
-  uint8_t* buf;   // [stages][K box, V box], 1024-byte aligned
-  uint64_t* bar;  // [stages]
+  uint8_t* buf;     // [stages][K box, V box], 1024-byte aligned
+  uint64_t* full;   // [stages]
+  uint64_t* empty;  // [stages], where several warps share the ring
   int slot, parity;  // of the tile to take next
 };
 
 // What one warp makes of its tiles of one item: o (not divided by l), m (log2
-// units) and l of its query rows.  Lane (r = lane / 4, j = lane % 4) holds rows
-// r and r + 8 of each block: o[i] their dimensions 16j + i and 16j + 8 + i.
-template <int NB>
+// units) and l of its query rows.  Lane (r = lane / 4, j = lane % 4) holds rows r
+// and r + 8: o[i] their dimensions 8i + 2j and 8i + 2j + 1.
 struct Acc {
-  float o[NB][8][4];
-  float m[NB][2], l[NB][2];
+  float o[8][4];
+  float m[2], l[2];
 };
 
 // One block of query rows of one key-value head of a sequence.
@@ -211,11 +211,6 @@ __device__ __forceinline__ const T16* q_row(const DraftArgs<T16>& a, const Item<
 }
 
 template <typename T16>
-__device__ __forceinline__ bool finite2(uint32_t w) {
-  constexpr uint32_t kExp = std::is_same<T16, __half>::value ? 0x7c00u : 0x7f80u;
-  return (w & kExp) != kExp && ((w >> 16) & kExp) != kExp;
-}
-template <typename T16>
 __device__ __forceinline__ uint32_t only_finite2(uint32_t w) {
   constexpr uint32_t kExp = std::is_same<T16, __half>::value ? 0x7c00u : 0x7f80u;
   if ((w & kExp) == kExp) w &= 0xffff0000u;
@@ -223,11 +218,11 @@ __device__ __forceinline__ uint32_t only_finite2(uint32_t w) {
   return w;
 }
 
-// fp16 p times a value that is not finite (of place `at` of the tile whose
-// values are vb): what the products with zero in that place have left out.
-template <typename T16, int NB, bool RIDE>
-__device__ __forceinline__ void add_not_finite(Acc<NB>& acc, int blk, const float (&s)[2][4], const uint8_t* vb,
-                                               int places) {
+// p times a value that is not finite, of the first `places` places of the tile
+// whose values are at vb: what the products with zero in their place have left out.
+// (p below 0: not visible.)
+template <typename T16, bool RIDE>
+__device__ __forceinline__ void add_not_finite(Acc& acc, const float (&s)[2][4], const uint8_t* vb, int places) {
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
 #pragma unroll 1
   for (int at = 0; at < places; ++at) {
@@ -239,289 +234,320 @@ __device__ __forceinline__ void add_not_finite(Acc<NB>& acc, int blk, const floa
       p[g] = __shfl_sync(0xffffffffu, at < 8 ? lo : hi, from);
     }
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const uint4 u = *reinterpret_cast<const uint4*>(vb + at * 128 + (((2 * j + e) ^ (at & 7)) << 4));
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t w = *reinterpret_cast<const uint32_t*>(vb + at * 128 + ((i ^ (at & 7)) << 4) + 4 * j);
+      if (w == only_finite2<T16>(w)) continue;
+      const float2 v = Type16<T16>::unpack2(w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (finite2<T16>(w[i])) continue;
-        const float2 v = Type16<T16>::unpack2(w[i]);
-#pragma unroll
-        for (int g = 0; g < (RIDE ? 1 : 2); ++g) {
-          if (p[g] < 0.f) continue;  // not visible
-          if (!isfinite(v.x)) acc.o[blk][2 * i][2 * g + e] += p[g] * v.x;
-          if (!isfinite(v.y)) acc.o[blk][2 * i + 1][2 * g + e] += p[g] * v.y;
-        }
+      for (int g = 0; g < (RIDE ? 1 : 2); ++g) {
+        if (p[g] < 0.f) continue;
+        if (!isfinite(v.x)) acc.o[i][2 * g] += p[g] * v.x;
+        if (!isfinite(v.y)) acc.o[i][2 * g + 1] += p[g] * v.y;
       }
     }
   }
 }
 
-// Attention of an item's query rows over its tiles j0, j0 + step, ... (cnt of
-// them) by one warp.  False if a wait ran out.  s_q: the query rows in shared
-// memory (Shape::kSharedQ), swizzled as a tile is.
+// Four 8 x 8 tiles of 16-bit values, transposed; lane i gives the address of row
+// i & 7 of tile i >> 3.
+__device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(a), "=r"(b), "=r"(c), "=r"(d)
+               : "r"(addr)
+               : "memory");
+}
+// The first product of a sum.
+template <typename T16>
+__device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  if constexpr (std::is_same<T16, __half>::value)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%10, %10, %10, %10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// Attention of query rows i0 .. i0 + 15 of an item over its tiles j0 .. j0 + cnt - 1 by
+// one warp, kUnits of them at a time: those of ring `at`.  `leader`: the warp that
+// fills the ring.  False if a wait ran out.
 //
-// The B fragments of both products come out of shared memory as they are: sums
-// over dimensions and the order of output dimensions are free, so lane (r, j)
-// reads of key rows r and r + 8 the dimensions 16j..16j+15 (q alike) and of value
-// rows 2j, 2j+1, 2j+8, 2j+9 the dimensions 8r..8r+7, where output column r of
-// product i stands for dimension 8r + i.  With the boxes' 128-byte swizzle
-// (16-byte unit u of row x at u ^ (x & 7)) no bank is read twice in a phase.
+// The B fragments of q . k come out of shared memory as they are: sums over
+// dimensions are free in their order, so lane (r, j) reads of key rows r and r + 8
+// the dimensions 16j..16j+15 (q alike); those of p . v are read transposed.  With
+// the boxes' 128-byte swizzle (16-byte unit u of row x at u ^ (x & 7)) no bank is
+// read twice in a phase.
 //
 // Tiles with places behind the cached positions are brought by the lanes
 // (16-byte asynchronous copies): cached places from their page, drafted ones
 // from k and v, which are also stored in the page from here.
-template <typename T16, int NB, bool RIDE>
-__device__ __forceinline__ bool attend(const DraftArgs<T16>& a, const Item<T16>& x, int j0, int step, int cnt,
-                                       Ring& ring, const uint8_t* s_q, Tree& tree, Acc<NB>& acc) {
-  using S = Shape<NB, RIDE>;
-  constexpr int kStages = S::kStages;
+template <typename T16, int WR, bool RIDE>
+__device__ __forceinline__ bool attend(const DraftArgs<T16>& a, const Item<T16>& x, int i0, bool leader, int at, int j0,
+                                       int cnt, Ring& ring, Tree& tree, Acc& acc) {
+  using S = Shape<WR, RIDE>;
+  constexpr int kStages = S::kStages, U = S::kUnits;
   constexpr int kHalves = RIDE ? 1 : 2;  // row groups of a lane that hold rows
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
   const int len = x.sp.len, end = len + x.sp.n;
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc.o[b][i][e] = 0.f;
-    acc.m[b][0] = acc.m[b][1] = -INFINITY;
-    acc.l[b][0] = acc.l[b][1] = 0.f;
-  }
-  auto tile_no = [&](int i) {
-    const int t = j0 + i * step;
-    return t < x.sp.ts ? t : x.sp.tw + (t - x.sp.ts);
+    for (int e = 0; e < 4; ++e) acc.o[i][e] = 0.f;
+  acc.m[0] = acc.m[1] = -INFINITY;
+  acc.l[0] = acc.l[1] = 0.f;
+  const int units = (cnt + U - 1) / U, mine = units > at ? (units - at + S::kRings - 1) / S::kRings : 0;
+  if (mine == 0) return true;
+  // first position of tile u of this ring's i-th unit
+  auto place = [&](int i, int u) {
+    const int t = j0 + (at + i * S::kRings) * U + u;
+    return (t < x.sp.ts ? t : x.sp.tw + (t - x.sp.ts)) * kTile;
   };
-  // lane i: first row (K) of tile (i + a multiple of 32) of this run, -1 when its page is not there
-  int rows32 = -1, fetched = 0;
-  auto issue = [&](int i, int slot) {
-    if ((i & 31) == 0) {
-      rows32 = -1;
-      if (i + lane < cnt) {
-        const int pos = tile_no(i + lane) * kTile, c = pos / a.page_size;
-        const int page = x.pages[c];
-        if (page >= 0 && page < a.n_pages)
-          rows32 = page * a.page_rows + a.row0 + x.kvh * a.page_size + (pos - c * a.page_size);
-        else
-          record_error(a.err, kErrRange, kSitePagedPage);
-      }
-    }
-    const int row = __shfl_sync(0xffffffffu, rows32, i & 31);
-    const uint32_t bar = smem_u32(&ring.bar[slot]), dst = smem_u32(ring.buf + slot * kStageBytes);
-    const int pos0 = tile_no(i) * kTile;
-    if (row >= 0 && a.k && pos0 + kTile > len) {  // (the same for all lanes)
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const int at = (lane >> 3) + 4 * (u & 3), c = lane & 7, part = u >> 2, p = pos0 + at;
-        const T16* from = nullptr;
-        if (p < len)
-          from = a.pages + (static_cast<long long>(row - a.row0) + at + part * a.n_kv * a.page_size) * kHd + c * 8;
-        else if (p < end)
-          from = (part ? a.v : a.k) + (static_cast<long long>(x.b) * a.T + (p - len)) * a.ldkv + x.kvh * kHd + c * 8;
-        if (from)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + part * kBoxBytes + at * 128 +
-                                                                         ((c ^ (at & 7)) << 4)),
-                       "l"(from)
-                       : "memory");
-      }
-      asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    } else if (lane == 0) {
-      if (row >= 0) {
-        mbar_arrive_expect_tx(bar, kStageBytes);
-        tma_load_2d(dst, ring.map, bar, 0, row);
-        tma_load_2d(dst + kBoxBytes, ring.map, bar, 0, row + a.n_kv * a.page_size);
-      } else {
-        mbar_arrive(bar);  // nothing to wait for
-      }
-    }
-    return row;
+  auto there = [&](int i, int u) { return U == 1 || (at + i * S::kRings) * U + u < cnt; };
+  // first row (K) of a tile in the pool, -1 when its page is not there (or there is no such tile); lane k of
+  // tile k of the units from i on
+  auto find_rows = [&](int i) {
+    const int n = i + lane / U, u = lane % U;
+    if (n >= mine || !there(n, u)) return -1;
+    const int pos = place(n, u), c = pos / a.page_size;
+    const int page = x.pages[c];
+    if (page >= 0 && page < a.n_pages)
+      return page * a.page_rows + a.row0 + x.kvh * a.page_size + (pos - c * a.page_size);
+    record_error(a.err, kErrRange, kSitePagedPage);
+    return -1;
   };
-  int rows[kStages];  // of the tiles in the ring, oldest first
-  int slot = ring.slot;
+  int fetch32 = -1, rows32 = -1, fetched = 0;  // of the units to fetch, and of those to take
+  auto issue = [&](int slot) {
+    const int i = fetched++;
+    if (i % (32 / U) == 0) fetch32 = find_rows(i);
+    const uint32_t bar = smem_u32(&ring.full[slot]), base = smem_u32(ring.buf + slot * S::kSlotBytes);
+    int boxes = 0, rows[U];
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) {
-    rows[s] = -1;
-    if (fetched < cnt) {
-      rows[s] = issue(fetched, slot);
-      ++fetched;
+    for (int u = 0; u < U; ++u) {
+      rows[u] = __shfl_sync(0xffffffffu, fetch32, (i * U + u) & 31);
+      const uint32_t dst = base + u * kTileBytes;
+      const int pos0 = place(i, u);
+      if (rows[u] >= 0 && a.k && pos0 + kTile > len) {  // (the same for all lanes)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int y = (lane >> 3) + 4 * (k & 3), c = lane & 7, part = k >> 2, p = pos0 + y;
+          const T16* from = nullptr;
+          if (p < len)
+            from = a.pages + (static_cast<long long>(rows[u] - a.row0) + y + part * a.n_kv * a.page_size) * kHd + c * 8;
+          else if (p < end)
+            from = (part ? a.v : a.k) + (static_cast<long long>(x.b) * a.T + (p - len)) * a.ldkv + x.kvh * kHd + c * 8;
+          if (from)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + part * kBoxBytes + y * 128 +
+                                                                           ((c ^ (y & 7)) << 4)),
+                         "l"(from)
+                         : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+        rows[u] = -1;
+      }
+      boxes += rows[u] >= 0 ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane == 0) {
+      if (boxes > 0)
+        mbar_arrive_expect_tx(bar, boxes * kTileBytes);
+      else
+        mbar_arrive(bar);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (rows[u] >= 0) {
+          tma_load_2d(base + u * kTileBytes, ring.map, bar, 0, rows[u]);
+          tma_load_2d(base + u * kTileBytes + kBoxBytes, ring.map, bar, 0, rows[u] + a.n_kv * a.page_size);
+        }
+    }
+  };
+  if (leader) {
+    int slot = ring.slot;
+#pragma unroll 1
+    for (int s = 0; s < kStages && fetched < mine; ++s) {
+      issue(slot);
       slot = slot + 1 == kStages ? 0 : slot + 1;
     }
   }
-  // q: lane (r, j) holds dimensions 16j..16j+15 of rows r and r + 8 of each block
-  uint4 qf[S::kSharedQ ? 1 : NB][4] = {};
-  if constexpr (!S::kSharedQ) {
+  // q: lane (r, j) holds dimensions 16j..16j+15 of rows r and r + 8
+  uint4 qf[4] = {};
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int g = 0; g < kHalves; ++g)
-        if (16 * b + 8 * g + r < x.rows) {
-          const uint4* from = reinterpret_cast<const uint4*>(q_row(a, x, 16 * b + 8 * g + r) + 16 * j);
-          qf[b][2 * g] = from[0];
-          qf[b][2 * g + 1] = from[1];
-        }
-  }
+  for (int g = 0; g < kHalves; ++g)
+    if (i0 + 8 * g + r < x.rows) {
+      const uint4* from = reinterpret_cast<const uint4*>(q_row(a, x, i0 + 8 * g + r) + 16 * j);
+      qf[2 * g] = from[0];
+      qf[2 * g + 1] = from[1];
+    }
+  const bool idle = i0 >= x.rows;  // no rows for this warp
   bool have_tree = false;
+  // where this lane reads: of key rows r and r + 8, and of value row lane & 15
+  const int k_at0 = r * 128 + (((2 * j) ^ r) << 4), k_at1 = r * 128 + (((2 * j + 1) ^ r) << 4);
+  const int v_row = kBoxBytes + (lane & 15) * 128, v_unit = lane >> 4, v_swz = lane & 7;
 
-  for (int i = 0; i < cnt; ++i) {
-    const bool ok = mbar_wait(smem_u32(&ring.bar[ring.slot]), ring.parity);
+  for (int i = 0; i < mine; ++i) {
+    const bool ok = mbar_wait(smem_u32(&ring.full[ring.slot]), ring.parity);
     if (!__all_sync(0xffffffffu, ok)) {
       if (lane == 0) {
         record_error(a.err, kErrTimeout, kSitePagedLoad);
-        for (int s = 0; s < kStages && i + s < cnt; ++s) {  // the loads in flight must not outlive the CTA
+        for (int s = 0; s < kStages && i + s < mine; ++s) {  // the loads in flight must not outlive the CTA
           const int k = ring.slot + s;
-          (void)mbar_wait(smem_u32(&ring.bar[k % kStages]), ring.parity ^ (k >= kStages ? 1 : 0));
+          (void)mbar_wait(smem_u32(&ring.full[k % kStages]), ring.parity ^ (k >= kStages ? 1 : 0));
         }
       }
       __syncwarp();
       return false;
     }
-    uint8_t* kb = ring.buf + ring.slot * kStageBytes;
-    uint8_t* vb = kb + kBoxBytes;
-    const int row = rows[0], pos0 = tile_no(i) * kTile;
-    if (row >= 0) {
-      // a tile that every row sees all of
-      const bool whole = pos0 + kTile <= len && (a.window <= 0 || pos0 >= end - a.window || pos0 + kTile <= a.sinks);
-      if (!whole && !have_tree) {
-        build_tree(a, x.b, x.sp, tree);
-        have_tree = true;
-      }
-      if (a.k && x.block == 0 && pos0 + kTile > len) {  // the drafted tokens' K and V into their page
-        const int page = x.pages[pos0 / a.page_size];
-        if (a.refs[page] > 1) {  // not into a page that other sequences read
-          if (lane == 0) record_error(a.err, kErrRange, kSitePagedShared);
-        } else {
+    if (i % (32 / U) == 0) rows32 = find_rows(i);
+    uint8_t* const tiles = ring.buf + ring.slot * S::kSlotBytes;
+    int rows[U], pos0[U];
+    bool any = false, whole = true;  // every row sees all of the tiles
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const int at = (lane >> 3) + 4 * (u & 3), c = lane & 7, part = u >> 2, p = pos0 + at;
+    for (int u = 0; u < U; ++u) {
+      rows[u] = __shfl_sync(0xffffffffu, rows32, (i * U + u) & 31);
+      pos0[u] = place(i, u);
+      any |= rows[u] >= 0;
+      whole = whole && rows[u] >= 0 && pos0[u] + kTile <= len &&
+              (a.window <= 0 || pos0[u] >= end - a.window || pos0[u] + kTile <= a.sinks);
+    }
+    if (any && (!idle || leader)) {
+      if (!whole) {
+        if (!have_tree) {
+          build_tree(a, x.b, x.sp, tree);
+          have_tree = true;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          // the drafted tokens' K and V into their page
+          if (!leader || !a.k || x.block != 0 || rows[u] < 0 || pos0[u] + kTile <= len) continue;
+          const int page = x.pages[pos0[u] / a.page_size];
+          if (a.refs[page] > 1) {  // not into a page that other sequences read
+            if (lane == 0) record_error(a.err, kErrRange, kSitePagedShared);
+            continue;
+          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int y = (lane >> 3) + 4 * (k & 3), c = lane & 7, part = k >> 2, p = pos0[u] + y;
             if (p >= len && p < end)
               *reinterpret_cast<uint4*>(
-                  a.pages + (static_cast<long long>(row - a.row0) + at + part * a.n_kv * a.page_size) * kHd + c * 8) =
-                  *reinterpret_cast<const uint4*>(kb + part * kBoxBytes + at * 128 + ((c ^ (at & 7)) << 4));
+                  a.pages + (static_cast<long long>(rows[u] - a.row0) + y + part * a.n_kv * a.page_size) * kHd + c * 8) =
+                  *reinterpret_cast<const uint4*>(tiles + u * kTileBytes + part * kBoxBytes + y * 128 +
+                                                  ((c ^ (y & 7)) << 4));
           }
         }
       }
-      uint4 kf[2][2];
+      float s[U][2][4];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint8_t* kr = kb + (r + 8 * e) * 128;
-        kf[e][0] = *reinterpret_cast<const uint4*>(kr + (((2 * j) ^ r) << 4));
-        kf[e][1] = *reinterpret_cast<const uint4*>(kr + (((2 * j + 1) ^ r) << 4));
-      }
-      uint32_t vf[8][2];
-      bool odd = false;  // a value that is not finite, in a tile that not every row sees all of
-      {
-        uint4 v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int vr = 2 * j + (e & 1) + (e >> 1) * 8;
-          v[e] = *reinterpret_cast<const uint4*>(vb + vr * 128 + ((r ^ (vr & 7)) << 4));
-          if (!whole) {
-            if (pos0 + vr >= end) v[e] = make_uint4(0, 0, 0, 0);  // nothing wrote it: it may hold anything
-            odd |= !(finite2<T16>(v[e].x) && finite2<T16>(v[e].y) && finite2<T16>(v[e].z) && finite2<T16>(v[e].w));
-          }
-        }
-        if (!whole) {
-          odd = __any_sync(0xffffffffu, odd);
-          if (odd)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              v[e] = make_uint4(only_finite2<T16>(v[e].x), only_finite2<T16>(v[e].y), only_finite2<T16>(v[e].z),
-                                only_finite2<T16>(v[e].w));
-        }
-        const uint32_t* v0 = reinterpret_cast<const uint32_t*>(&v[0]);
-        const uint32_t* v1 = reinterpret_cast<const uint32_t*>(&v[1]);
-        const uint32_t* v2 = reinterpret_cast<const uint32_t*>(&v[2]);
-        const uint32_t* v3 = reinterpret_cast<const uint32_t*>(&v[3]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
-          vf[k][0] = __byte_perm(v0[k >> 1], v1[k >> 1], sel);
-          vf[k][1] = __byte_perm(v2[k >> 1], v3[k >> 1], sel);
-        }
-      }
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (NB > 1 && 16 * b >= x.rows) break;
-        uint4 q0, q1, q2, q3;  // rows r (its two halves), r + 8
-        if constexpr (S::kSharedQ) {
-          const uint8_t* qr = s_q + (16 * b + r) * 128;
-          q0 = *reinterpret_cast<const uint4*>(qr + (((2 * j) ^ r) << 4));
-          q1 = *reinterpret_cast<const uint4*>(qr + (((2 * j + 1) ^ r) << 4));
-          q2 = *reinterpret_cast<const uint4*>(qr + 1024 + (((2 * j) ^ r) << 4));
-          q3 = *reinterpret_cast<const uint4*>(qr + 1024 + (((2 * j + 1) ^ r) << 4));
-        } else {
-          q0 = qf[b][0], q1 = qf[b][1], q2 = qf[b][2], q3 = qf[b][3];
-        }
-        float s[2][4];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          s[e][0] = s[e][1] = s[e][2] = s[e][3] = 0.f;
-          mma16816<T16>(s[e], q0.x, q2.x, q0.y, q2.y, kf[e][0].x, kf[e][0].y);
-          mma16816<T16>(s[e], q0.z, q2.z, q0.w, q2.w, kf[e][0].z, kf[e][0].w);
-          mma16816<T16>(s[e], q1.x, q3.x, q1.y, q3.y, kf[e][1].x, kf[e][1].y);
-          mma16816<T16>(s[e], q1.z, q3.z, q1.w, q3.w, kf[e][1].z, kf[e][1].w);
+          const uint8_t* kr = tiles + u * kTileBytes + e * 1024;
+          const uint4 k0 = *reinterpret_cast<const uint4*>(kr + k_at0);
+          const uint4 k1 = *reinterpret_cast<const uint4*>(kr + k_at1);
+          mma16816_first<T16>(s[u][e], qf[0].x, qf[2].x, qf[0].y, qf[2].y, k0.x, k0.y);
+          mma16816<T16>(s[u][e], qf[0].z, qf[2].z, qf[0].w, qf[2].w, k0.z, k0.w);
+          mma16816<T16>(s[u][e], qf[1].x, qf[3].x, qf[1].y, qf[3].y, k1.x, k1.y);
+          mma16816<T16>(s[u][e], qf[1].z, qf[3].z, qf[1].w, qf[3].w, k1.z, k1.w);
         }
-        uint32_t hidden = 0;  // bit 4e + 2g + k: score s[e][2g + k] is not visible
-        if (!whole) {
+      uint32_t hidden = 0;  // bit 8u + 4e + 2g + k: score s[u][e][2g + k] is not visible
+      if (!whole) {
 #pragma unroll
-          for (int g = 0; g < kHalves; ++g) {
-            const int i_row = min(16 * b + 8 * g + r, x.rows - 1);
-            const int t = (x.row0 + i_row) / a.group;
-            const unsigned long long anc = tree.anc[t];
-            const int first = a.window > 0 ? len + tree.depth[t] + 1 - a.window : 0;
+        for (int g = 0; g < kHalves; ++g) {
+          const int i_row = min(i0 + 8 * g + r, x.rows - 1);
+          const int t = (x.row0 + i_row) / a.group;
+          const unsigned long long anc = tree.anc[t];
+          const int first = a.window > 0 ? len + tree.depth[t] + 1 - a.window : 0;
+#pragma unroll
+          for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
-                const int p = pos0 + 8 * e + 2 * j + k;
-                const bool seen = p < len ? (p >= first || p < a.sinks) : p < end && ((anc >> (p - len)) & 1);
+                const int p = pos0[u] + 8 * e + 2 * j + k;
+                const bool seen = rows[u] >= 0 && (p < len ? (p >= first || p < a.sinks)
+                                                           : p < end && ((anc >> (p - len)) & 1));
                 if (!seen) {
-                  s[e][2 * g + k] = -INFINITY;
-                  hidden |= 1u << (4 * e + 2 * g + k);
+                  s[u][e][2 * g + k] = -INFINITY;
+                  hidden |= 1u << (8 * u + 4 * e + 2 * g + k);
                 }
               }
-          }
         }
-        float alpha[2] = {1.f, 1.f};
+      }
+      float alpha[2] = {1.f, 1.f};
 #pragma unroll
-        for (int g = 0; g < kHalves; ++g) {
-          float mx = fmaxf(fmaxf(s[0][2 * g], s[0][2 * g + 1]), fmaxf(s[1][2 * g], s[1][2 * g + 1]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-          const float mn = fmaxf(acc.m[b][g], mx * a.scale_log2);
-          const float ms = mn == -INFINITY ? 0.f : mn;  // every score so far is -inf
-          alpha[g] = acc.m[b][g] == mn ? 1.f : ex2_approx(acc.m[b][g] - ms);
-          acc.m[b][g] = mn;
-          const float bias = kShift<T16> - ms;
+      for (int g = 0; g < kHalves; ++g) {
+        float mx = max3f(s[0][0][2 * g], s[0][0][2 * g + 1], s[0][1][2 * g]);
+        if constexpr (U == 1)
+          mx = fmaxf(mx, s[0][1][2 * g + 1]);
+        else
+          mx = max3f(max3f(mx, s[0][1][2 * g + 1], s[U - 1][0][2 * g]), s[U - 1][0][2 * g + 1],
+                     fmaxf(s[U - 1][1][2 * g], s[U - 1][1][2 * g + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(acc.m[g], mx * a.scale_log2);
+        const float ms = mn == -INFINITY ? 0.f : mn;  // every score so far is -inf
+        alpha[g] = acc.m[g] == mn ? 1.f : ex2_approx(acc.m[g] - ms);
+        acc.m[g] = mn;
+        const float bias = kShift<T16> - ms;
+        float sum = 0.f;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
-            for (int k = 0; k < 2; ++k) s[e][2 * g + k] = ex2_approx(fmaf(s[e][2 * g + k], a.scale_log2, bias));
-          acc.l[b][g] = fmaf(acc.l[b][g], alpha[g], (s[0][2 * g] + s[0][2 * g + 1]) + (s[1][2 * g] + s[1][2 * g + 1]));
+            for (int k = 0; k < 2; ++k)
+              s[u][e][2 * g + k] = ex2_approx(fmaf(s[u][e][2 * g + k], a.scale_log2, bias));
+          sum += (s[u][0][2 * g] + s[u][0][2 * g + 1]) + (s[u][1][2 * g] + s[u][1][2 * g + 1]);
         }
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+        acc.l[g] = fmaf(acc.l[g], alpha[g], sum);
+      }
+      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          acc.o[k][0] *= alpha[0];
+          acc.o[k][1] *= alpha[0];
+          acc.o[k][2] *= alpha[RIDE ? 0 : 1];
+          acc.o[k][3] *= alpha[RIDE ? 0 : 1];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint32_t vf[8][2];
+        const uint32_t vb = smem_u32(tiles + u * kTileBytes) + v_row;
+#pragma unroll
+        for (int k = 0; k < 8; k += 2)
+          load_transposed(vb + (((k + v_unit) ^ v_swz) << 4), vf[k][0], vf[k][1], vf[k + 1][0], vf[k + 1][1]);
+        bool odd = false;  // a value that is not finite, in a tile that not every row sees all of
+        if (!whole) {
+          // places that nothing wrote may hold anything
+          const int left = rows[u] >= 0 ? end - pos0[u] - 2 * j : 0;
+          const uint32_t m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+          const uint32_t m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
-            acc.o[b][k][0] *= alpha[0];
-            acc.o[b][k][1] *= alpha[0];
-            acc.o[b][k][2] *= alpha[RIDE ? 0 : 1];
-            acc.o[b][k][3] *= alpha[RIDE ? 0 : 1];
+            vf[k][0] &= m0;
+            vf[k][1] &= m1;
+            const uint32_t f0 = only_finite2<T16>(vf[k][0]), f1 = only_finite2<T16>(vf[k][1]);
+            odd |= f0 != vf[k][0] || f1 != vf[k][1];
+            vf[k][0] = f0;
+            vf[k][1] = f1;
           }
+          odd = __any_sync(0xffffffffu, odd);
         }
         uint32_t ph[2][2], pl[2][2];  // [position half][row half]
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
-          for (int g = 0; g < kHalves; ++g) split2<T16>(s[e][2 * g], s[e][2 * g + 1], ph[e][g], pl[e][g]);
+          for (int g = 0; g < kHalves; ++g) split2<T16>(s[u][e][2 * g], s[u][e][2 * g + 1], ph[e][g], pl[e][g]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if constexpr (RIDE) {
-            mma16816<T16>(acc.o[b][k], ph[0][0], pl[0][0], ph[1][0], pl[1][0], vf[k][0], vf[k][1]);
+            mma16816<T16>(acc.o[k], ph[0][0], pl[0][0], ph[1][0], pl[1][0], vf[k][0], vf[k][1]);
           } else {
-            mma16816<T16>(acc.o[b][k], ph[0][0], ph[0][1], ph[1][0], ph[1][1], vf[k][0], vf[k][1]);
-            mma16816<T16>(acc.o[b][k], pl[0][0], pl[0][1], pl[1][0], pl[1][1], vf[k][0], vf[k][1]);
+            mma16816<T16>(acc.o[k], ph[0][0], ph[0][1], ph[1][0], ph[1][1], vf[k][0], vf[k][1]);
+            mma16816<T16>(acc.o[k], pl[0][0], pl[0][1], pl[1][0], pl[1][1], vf[k][0], vf[k][1]);
           }
         }
         if (odd) {
@@ -529,20 +555,29 @@ __device__ __forceinline__ bool attend(const DraftArgs<T16>& a, const Item<T16>&
           for (int e = 0; e < 2; ++e)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if ((hidden >> (4 * e + k)) & 1) s[e][k] = -1.f;
-          add_not_finite<T16, NB, RIDE>(acc, b, s, vb, min(kTile, end - pos0));
+              if ((hidden >> (8 * u + 4 * e + k)) & 1) s[u][e][k] = -1.f;
+          add_not_finite<T16, RIDE>(acc, s[u], tiles + u * kTileBytes + kBoxBytes, min(kTile, end - pos0[u]));
         }
       }
     }
-    // the slot is read: the tile kStages further on
+    // the slot is read: the unit kStages further on (where warps share the ring, into the slot before, which
+    // the others have read by now)
     __syncwarp();
-    if (lane == 0) fence_proxy_async_smem();
-#pragma unroll
-    for (int s = 0; s + 1 < kStages; ++s) rows[s] = rows[s + 1];
-    rows[kStages - 1] = -1;
-    if (fetched < cnt) {
-      rows[kStages - 1] = issue(fetched, ring.slot);
-      ++fetched;
+    if constexpr (WR == 1) {
+      if (lane == 0) fence_proxy_async_smem();
+      if (fetched < mine) issue(ring.slot);
+    } else {
+      if (lane == 0) mbar_arrive(smem_u32(&ring.empty[ring.slot]));
+      if (leader && i > 0 && fetched < mine) {
+        const int before = ring.slot == 0 ? kStages - 1 : ring.slot - 1;
+        const bool free = mbar_wait(smem_u32(&ring.empty[before]), ring.slot == 0 ? ring.parity ^ 1 : ring.parity);
+        if (!__all_sync(0xffffffffu, free)) {
+          if (lane == 0) record_error(a.err, kErrTimeout, kSitePagedLoad);
+          fetched = mine;  // (nothing more is brought: the waits for it run out)
+        } else {
+          issue(before);
+        }
+      }
     }
     if (++ring.slot == kStages) {
       ring.slot = 0;
@@ -550,43 +585,34 @@ __device__ __forceinline__ bool attend(const DraftArgs<T16>& a, const Item<T16>&
     }
   }
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
+  for (int g = 0; g < 2; ++g) {  // sums over the four lanes of a row
+    acc.l[g] += __shfl_xor_sync(0xffffffffu, acc.l[g], 1);
+    acc.l[g] += __shfl_xor_sync(0xffffffffu, acc.l[g], 2);
+  }
+  if (RIDE) {
 #pragma unroll
-    for (int g = 0; g < 2; ++g) {  // sums over the four lanes of a row
-      acc.l[b][g] += __shfl_xor_sync(0xffffffffu, acc.l[b][g], 1);
-      acc.l[b][g] += __shfl_xor_sync(0xffffffffu, acc.l[b][g], 2);
-    }
-    if (RIDE) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        acc.o[b][i][0] += acc.o[b][i][2];
-        acc.o[b][i][1] += acc.o[b][i][3];
-      }
+    for (int i = 0; i < 8; ++i) {
+      acc.o[i][0] += acc.o[i][2];
+      acc.o[i][1] += acc.o[i][3];
     }
   }
   return true;
 }
 
 // The rows of one warp's result: dst[row][64], ml[row] = (m, l).
-template <typename T16, int NB, bool RIDE>
-__device__ __forceinline__ void put_piece(const Acc<NB>& acc, int rows, float* dst, float2* ml) {
+template <typename T16, bool RIDE>
+__device__ __forceinline__ void put_piece(const Acc& acc, int rows, float* dst, float2* ml) {
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
+  for (int g = 0; g < (RIDE ? 1 : 2); ++g) {
+    const int i = 8 * g + r;
+    if (i >= rows) continue;
+    float* po = dst + i * kHd + 2 * j;
 #pragma unroll
-    for (int g = 0; g < (RIDE ? 1 : 2); ++g) {
-      const int i = 16 * b + 8 * g + r;
-      if (i >= rows) continue;
-      float* po = dst + i * kHd + 16 * j;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        *reinterpret_cast<float4*>(po + 8 * e) = make_float4(acc.o[b][0][2 * g + e], acc.o[b][1][2 * g + e],
-                                                             acc.o[b][2][2 * g + e], acc.o[b][3][2 * g + e]);
-        *reinterpret_cast<float4*>(po + 8 * e + 4) = make_float4(acc.o[b][4][2 * g + e], acc.o[b][5][2 * g + e],
-                                                                 acc.o[b][6][2 * g + e], acc.o[b][7][2 * g + e]);
-      }
-      if (j == 0) ml[i] = make_float2(acc.m[b][g] - kShift<T16>, acc.l[b][g]);
-    }
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<float2*>(po + 8 * k) = make_float2(acc.o[k][2 * g], acc.o[k][2 * g + 1]);
+    if (j == 0) ml[i] = make_float2(acc.m[g] - kShift<T16>, acc.l[g]);
+  }
 }
 
 // Four dimensions of row i of an item, and its log-sum-exp, into the output.
@@ -604,6 +630,27 @@ __device__ __forceinline__ void put_row(const DraftArgs<T16>& a, const Item<T16>
   if (a.lse && d4 == 0) a.lse[token * a.H + head] = M + log2f(L);
 }
 
+// The rows of one warp's whole result into the output.
+template <typename T16>
+__device__ __forceinline__ void put_rows(const DraftArgs<T16>& a, const Item<T16>& x, int i0, const Acc& acc) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+#pragma unroll
+  for (int g = 0; g < 2; ++g) {
+    const int i = i0 + 8 * g + r;
+    if (i >= x.rows) continue;
+    int t, head;
+    row_of(a, x, i, t, head);
+    const long long token = static_cast<long long>(x.b) * a.T + t;
+    const float l = acc.l[g], inv = l == 0.f ? 0.f : 1.f / l;
+    T16* to = a.out + token * a.ldo + static_cast<long long>(head) * kHd + 2 * j;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      *reinterpret_cast<uint32_t*>(to + 8 * k) =
+          Type16<T16>::pack2(acc.o[k][2 * g] * inv, acc.o[k][2 * g + 1] * inv);
+    if (a.lse && j == 0) a.lse[token * a.H + head] = acc.m[g] - kShift<T16> + log2f(l);
+  }
+}
+
 template <typename T16>
 __device__ __forceinline__ Item<T16> item_of(const DraftArgs<T16>& a, int b, int item, const Span& sp, int rows) {
   Item<T16> x;
@@ -618,30 +665,35 @@ __device__ __forceinline__ Item<T16> item_of(const DraftArgs<T16>& a, int b, int
 }
 
 // Work is cut into equal runs of tiles over all (sequence, key-value head, row
-// block) items laid end to end, one run per CTA, whatever the lengths are.  The
-// warps of a CTA take the tiles of an item in turn and meet in shared memory; a
-// CTA that holds all tiles of an item writes its output, pieces of an item go to
-// the workspace and a second kernel joins them.
-template <typename T16, int NB, bool RIDE>
-__global__ void __launch_bounds__(kThreads, (Shape<NB, RIDE>::kCtasPerSm))
+// block) items laid end to end, one run per CTA, whatever the lengths are.  A CTA
+// that holds all tiles of an item writes its output, pieces of an item go to the
+// workspace and a second kernel joins them.  Rings of one or two warps take the
+// tiles of a piece in turn and meet in shared memory.
+template <typename T16, int WR, bool RIDE>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
     draft_attn(const __grid_constant__ CUtensorMap map, const DraftArgs<T16> a) {
-  using S = Shape<NB, RIDE>;
+  using S = Shape<WR, RIDE>;
+  constexpr int kRings = S::kRings;
   extern __shared__ uint8_t s_raw[];
-  __shared__ __align__(8) uint64_t s_bar[kWarps * S::kStages];
+  __shared__ __align__(8) uint64_t s_bar[2][kRings * S::kStages];
   __shared__ int s_sum[kWarps];
-  __shared__ float2 s_ml[kWarps * S::kRows];
+  __shared__ float2 s_ml[kRings * S::kRows];
   __shared__ Tree s_tree[kWarps];
   uint8_t* s_tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* s_q = s_tiles + kWarps * S::kRingBytes;
-  int* s_base = reinterpret_cast<int*>(s_q + (S::kSharedQ ? S::kRows * 128 : 0));  // [n_seq + 1]
+  int* s_base = reinterpret_cast<int*>(s_tiles + kRings * S::kRingBytes);  // [n_seq + 1]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  Ring ring{&map, s_tiles + warp * S::kRingBytes, s_bar + warp * S::kStages, 0, 0};
-  if (lane == 0) {
-    for (int s = 0; s < S::kStages; ++s) mbar_init(smem_u32(&ring.bar[s]), 1);
+  // which ring, and which 16 rows: not always the last ones on the same quarter of the SM
+  const int at = warp / WR, rank = (warp + static_cast<int>(blockIdx.x)) % WR;
+  const bool leader = rank == 0;
+  Ring ring{&map, s_tiles + at * S::kRingBytes, s_bar[0] + at * S::kStages, s_bar[1] + at * S::kStages, 0, 0};
+  if (tid == 0) {
+    for (int s = 0; s < kRings * S::kStages; ++s) {
+      mbar_init(smem_u32(&s_bar[0][s]), 1);
+      mbar_init(smem_u32(&s_bar[1][s]), WR);
+    }
     fence_barrier_init();
     tma_prefetch_desc(&map);
   }
-  __syncwarp();
   griddep_wait();
   // base[b] = tiles of all items of sequences before b
   int carry = 0;
@@ -693,48 +745,47 @@ __global__ void __launch_bounds__(kThreads, (Shape<NB, RIDE>::kCtasPerSm))
     const int j0 = (t - s_base[lo]) - item * sp.nt;  // first tile of this piece within the item
     const int cnt = min(sp.nt - j0, t_end - t);
     const Item<T16> x = item_of(a, lo, item, sp, S::kRows);
-    if constexpr (S::kSharedQ) {
-      for (int i = tid; i < S::kRows * 8; i += kThreads) {
-        const int row = i >> 3, c = i & 7;
-        uint4 u = make_uint4(0, 0, 0, 0);
-        if (row < x.rows) u = *reinterpret_cast<const uint4*>(q_row(a, x, row) + 8 * c);
-        *reinterpret_cast<uint4*>(s_q + row * 128 + ((c ^ (row & 7)) << 4)) = u;
-      }
-      __syncthreads();
-    }
-    bool ok = true;
-    {
-      Acc<NB> acc;
-      const int mine = cnt > warp ? (cnt - warp + kWarps - 1) / kWarps : 0;
-      if (mine > 0) {
-        ok = attend<T16, NB, RIDE>(a, x, j0 + warp, kWarps, mine, ring, s_q, s_tree[warp], acc);
-        __syncwarp();
-        if (ok)
-          put_piece<T16, NB, RIDE>(acc, x.rows, reinterpret_cast<float*>(ring.buf), s_ml + warp * S::kRows);
-      }
-    }
-    if (!__syncthreads_and(ok)) return;
-    t += cnt;
-    if (t >= t_end) griddep_launch_dependents();
     const bool all = cnt == sp.nt;
-    const int pieces = min(cnt, kWarps);
-    const long long part = 2ll * blockIdx.x + (t - cnt == static_cast<int>(t_first) ? 0 : 1);
-    for (int k = tid; k < x.rows * 16; k += kThreads) {
-      const int i = k >> 4, d4 = k & 15;
-      float M = -INFINITY, L = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = 0; w < pieces; ++w)
-        merge(o, M, L, *reinterpret_cast<const float4*>(s_tiles + w * S::kRingBytes + (i * kHd + 4 * d4) * 4),
-              s_ml[w * S::kRows + i]);
-      if (all) {
-        put_row(a, x, i, d4, o, M, L);
+    const long long part = 2ll * blockIdx.x + (t == static_cast<int>(t_first) ? 0 : 1);
+    const int i0 = RIDE ? 0 : 16 * rank;
+    Acc acc;
+    const bool ok = attend<T16, WR, RIDE>(a, x, i0, leader, at, j0, cnt, ring, s_tree[warp], acc);
+    t += cnt;
+    __syncwarp();
+    if constexpr (kRings == 1) {
+      if (!ok) {
+        // (the others' waits run out, too)
+      } else if (all) {
+        put_rows(a, x, i0, acc);
       } else {
-        *reinterpret_cast<float4*>(a.part_o + (part * S::kRows + i) * kHd + 4 * d4) = o;
-        if (d4 == 0) a.part_ml[part * S::kRows + i] = make_float2(M, L);
+        put_piece<T16, RIDE>(acc, x.rows - i0, a.part_o + (part * S::kRows + i0) * kHd, a.part_ml + part * S::kRows + i0);
       }
-    }
-    if (t < t_end) {
-      // the rings take tiles again: generic reads before asynchronous writes
+      if (t >= t_end) griddep_launch_dependents();
+      fence_proxy_async_smem();
+      if (!__syncthreads_and(ok)) return;  // (and every warp is through with the ring)
+    } else {
+      // a warp's result (fp32 rows of 64) takes the place of its ring
+      if (WR > 1 && !__syncthreads_and(ok)) return;
+      const int pieces = min((cnt + S::kUnits - 1) / S::kUnits, kRings);
+      if (at < pieces && ok)
+        put_piece<T16, RIDE>(acc, x.rows - i0, reinterpret_cast<float*>(ring.buf) + i0 * kHd, s_ml + at * S::kRows + i0);
+      if (!__syncthreads_and(ok)) return;
+      if (t >= t_end) griddep_launch_dependents();
+      for (int k = tid; k < x.rows * 16; k += kThreads) {
+        const int i = k >> 4, d4 = k & 15;
+        float M = -INFINITY, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < pieces; ++w)
+          merge(o, M, L, *reinterpret_cast<const float4*>(s_tiles + w * S::kRingBytes + (i * kHd + 4 * d4) * 4),
+                s_ml[w * S::kRows + i]);
+        if (all) {
+          put_row(a, x, i, d4, o, M, L);
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (part * S::kRows + i) * kHd + 4 * d4) = o;
+          if (d4 == 0) a.part_ml[part * S::kRows + i] = make_float2(M, L);
+        }
+      }
+      // the rings take tiles again: generic accesses before asynchronous writes
       fence_proxy_async_smem();
       __syncthreads();
     }
@@ -804,32 +855,25 @@ __global__ void __launch_bounds__(kJoinThreads) draft_join(const DraftArgs<T16> 
 
 size_t align256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
 
-// Query rows per block, and what follows from them, for T tokens of a group of
-// heads: few rows leave registers for more warps (and, up to 8, carry the
-// remainder of p for nothing), more of them read the cache less often.
-struct Plan {
-  int kind;  // 0: 8 rows, 1: 16, 2: 32, 3: 64
-  int rows, ctas_per_sm;
-};
-Plan plan_of(int T, int group) {
+// Query rows per block for T tokens of a group of heads: few rows leave the warps
+// their own tiles (and, up to 8, carry the remainder of p for nothing), more of
+// them read the cache less often.
+int rows_of(int T, int group) {
   const int rows = T * group;
-  if (rows <= 8) return {0, 8, Shape<1, true>::kCtasPerSm};
-  if (rows <= 16) return {1, 16, Shape<1, false>::kCtasPerSm};
-  if (rows <= 32) return {2, 32, Shape<2, false>::kCtasPerSm};
-  return {3, 64, Shape<4, false>::kCtasPerSm};
+  return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
-template <typename T16, int NB, bool RIDE>
+template <typename T16, int WR, bool RIDE>
 cudaError_t launch_kind(const CUtensorMap& map, const DraftArgs<T16>& a, cudaStream_t s) {
-  using S = Shape<NB, RIDE>;
-  const int fixed = kWarps * S::kRingBytes + 1024 + (S::kSharedQ ? S::kRows * 128 : 0);
+  using S = Shape<WR, RIDE>;
+  constexpr int kFixed = S::kRings * S::kRingBytes + 1024;
   static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!configured[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(draft_attn<T16, NB, RIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         fixed + (kMaxPagedSeqs + 1) * 4);
+    cudaError_t e = cudaFuncSetAttribute(draft_attn<T16, WR, RIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kFixed + (kMaxPagedSeqs + 1) * 4);
     if (e != cudaSuccess) return e;
     // the join leaves the SMs split as draft_attn has them: between two splits an SM has to run empty
     e = cudaFuncSetAttribute(draft_join<T16, S::kRows>, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -838,7 +882,7 @@ cudaError_t launch_kind(const CUtensorMap& map, const DraftArgs<T16>& a, cudaStr
     configured[dev] = 1;
   }
   const int sms = num_sms();
-  cudaError_t e = launch_pdl(draft_attn<T16, NB, RIDE>, sms * S::kCtasPerSm, kThreads, fixed + (a.n_seq + 1) * 4, s, 0,
+  cudaError_t e = launch_pdl(draft_attn<T16, WR, RIDE>, sms * kCtasPerSm, kThreads, kFixed + (a.n_seq + 1) * 4, s, 0,
                              map, a);
   if (e != cudaSuccess) return e;
   const int max_blocks = (a.T * a.group + S::kRows - 1) / S::kRows;
@@ -885,8 +929,8 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   a.window = window;
   a.sinks = sinks;
   a.scale_log2 = score_scale * 1.4426950408889634f;
-  const Plan p = plan_of(T, a.group);
-  const size_t slots = 2ull * num_sms() * p.ctas_per_sm * p.rows;
+  const int rows = rows_of(T, a.group);
+  const size_t slots = 2ull * num_sms() * kCtasPerSm * rows;
   char* base = static_cast<char*>(ws);
   a.plan = reinterpret_cast<int*>(base);
   base += align256((static_cast<size_t>(c->n_seq) + 2) * 4);
@@ -898,10 +942,10 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   if (!encode_tma_2d(&map, Type16<T16>::kTma, c->pages, kHd, static_cast<uint64_t>(c->n_pages) * a.page_rows, kHd * 2,
                      kHd, kTile))
     return cudaErrorInvalidValue;
-  switch (p.kind) {
-    case 0: return launch_kind<T16, 1, true>(map, a, s);
-    case 1: return launch_kind<T16, 1, false>(map, a, s);
-    case 2: return launch_kind<T16, 2, false>(map, a, s);
+  switch (rows) {
+    case 8: return launch_kind<T16, 1, true>(map, a, s);
+    case 16: return launch_kind<T16, 1, false>(map, a, s);
+    case 32: return launch_kind<T16, 2, false>(map, a, s);
     default: return launch_kind<T16, 4, false>(map, a, s);
   }
 }
@@ -909,8 +953,7 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
 }  // namespace
 
 size_t attention_draft_workspace(const gpt2_paged_cache* c, int T, int n_head) {
-  const Plan p = plan_of(T, n_head / c->n_kv_head);
-  const size_t slots = 2ull * num_sms() * p.ctas_per_sm * p.rows;
+  const size_t slots = 2ull * num_sms() * kCtasPerSm * rows_of(T, n_head / c->n_kv_head);
   return align256((static_cast<size_t>(c->n_seq) + 2) * 4) + align256(slots * sizeof(float2)) +
          align256(slots * kHd * 4);
 }
@@ -919,8 +962,8 @@ bool attention_draft_fits(const gpt2_paged_cache* c, int T, int n_head) {
   // rows of the pool are TMA coordinates, and tiles of all items are counted, in
   // 32 bits, the latter with room for one run more
   if (static_cast<double>(c->n_pages) * c->n_layer * 2 * c->n_kv_head * c->page_size >= 2147483648.0) return false;
-  const Plan p = plan_of(T, n_head / c->n_kv_head);
-  const long long blocks = (static_cast<long long>(T) * (n_head / c->n_kv_head) + p.rows - 1) / p.rows;
+  const int rows = rows_of(T, n_head / c->n_kv_head);
+  const long long blocks = (static_cast<long long>(T) * (n_head / c->n_kv_head) + rows - 1) / rows;
   return static_cast<long long>(c->n_seq) * c->n_kv_head * blocks *
              (static_cast<long long>(c->max_pages) * c->page_size / kTile) <
          (1ll << 30);
