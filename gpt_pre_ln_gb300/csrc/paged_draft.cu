@@ -15,9 +15,18 @@
 // the tensor cores need to be the limit.  The products are mma.sync m16n8k16 with
 // 16 rows to a warp, whose scores and results stay in registers; with p as the sum
 // of two 16-bit numbers they take 192 cycles of an SM's four tensor pipes for 64
-// rows and 16 positions, which come from HBM in 170.  Up to 16 rows, the warps of a
-// CTA take tiles of positions in turn, each from a ring of TMA boxes of its own;
-// with more rows two or four warps share a ring, each with 16 rows of the block.
+// rows and 16 positions, which come from HBM in 170.
+//
+// Up to 16 rows, the warps of a CTA take tiles of 16 positions in turn, each from a
+// ring of TMA boxes that it fills itself.  With more rows two or four warps take the
+// same tiles, 32 positions at a time, each with 16 rows of the block, and a fifth
+// warp brings them: the warp that also filled the ring held up all four (64 rows,
+// 16 sequences of 4096: 116 us, with the fifth warp 83; 48 rows, 8 of 32768: 109 and
+// 81).  Up to 16 rows the fifth warp cost more than it gave (12 rows, 32 sequences
+// up to 2048: 29 us without, 39 with it).
+//
+// What bounds it is the instructions around the products (exponentials, the split
+// of p, running maxima), not memory: 2.3 TB/s at 64 rows, 5.0 at 5.
 #include <algorithm>
 
 #include "internal.h"
@@ -29,23 +38,29 @@ namespace {
 
 constexpr int kHd = 64;
 constexpr int kTile = 16;  // positions per tile; page sizes are multiples of it
-constexpr int kWarps = 4;  // warps per CTA; they take a piece's tiles in turn
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 4;  // warps per CTA that take tiles
+constexpr int kTakers = kWarps * 32;
 constexpr int kBoxBytes = kTile * kHd * 2;
 constexpr int kTileBytes = 2 * kBoxBytes;  // K, then V
-constexpr int kMinRun = 2 * kWarps;         // tiles per CTA at least
-constexpr int kCtasPerSm = 4;
+constexpr int kMinRun = 2 * kWarps;        // tiles per CTA at least
 
-// WR: warps that share a ring, with 16 query rows each.  RIDE: up to 8 rows in
-// all, whose other 8 carry the rounding remainder of p.
+// WR: warps that take the same tiles, with 16 query rows each.  RIDE: up to 8 rows
+// in all, whose other 8 carry the rounding remainder of p.
 template <int WR, bool RIDE>
 struct Shape {
   static constexpr int kRows = RIDE ? 8 : 16 * WR;
-  static constexpr int kRings = kWarps / WR;
-  static constexpr int kUnits = WR == 1 ? 1 : 2;       // tiles that a warp takes at a time
-  static constexpr int kStages = WR == 1 ? 2 : 3 * WR / 2;  // of each ring: 128 or 192 KB of them on an SM
-  static constexpr int kSlotBytes = kUnits * kTileBytes;
-  static constexpr int kRingBytes = kStages * kSlotBytes;
+  static constexpr int kGroups = kWarps / WR;
+  static constexpr bool kBringer = WR > 1;          // a warp that brings the tiles
+  static constexpr int kUnit = kBringer ? 2 : 1;    // tiles that a warp takes at a time
+  static constexpr int kRings = kBringer ? 1 : kWarps;
+  static constexpr int kSlots = kBringer ? 6 : 2;   // units in a ring: 144 or 128 KB of them on an SM
+  static constexpr int kCtas = kBringer ? 3 : 4;    // per SM
+  static constexpr int kThreads = kTakers + (kBringer ? 32 : 0);
+  static constexpr int kRingBytes = kSlots * kUnit * kTileBytes;
+  // where the groups' results (fp32 rows of 64) meet: their rings, or a place of its own
+  static constexpr int kMeetBytes = kBringer && kGroups > 1 ? kGroups * kRows * kHd * 4 : 0;
+  // A slot's uses one after another belong to one group: a wait for the phase after the next would not wait.
+  static_assert(!kBringer || kSlots % kGroups == 0, "slots are a multiple of the groups");
 };
 
 template <typename T16>
@@ -171,13 +186,35 @@ __device__ __forceinline__ void build_tree(const DraftArgs<T16>& a, int b, const
   }
 }
 
-// A ring of tiles.
+// A unit of tiles in the ring: their first rows (K) in the pool, -1 where there is
+// no such tile or its page is not there, and positions; pos[0] < 0: every query row
+// sees all of them.
+template <int U>
+struct Unit {
+  int row[U], pos[U];
+};
+template <int U>
 struct Ring {
-  const CUtensorMap* map;
-  uint8_t* buf;     // [stages][K box, V box], 1024-byte aligned
-  uint64_t* full;   // [stages]
-  uint64_t* empty;  // [stages], where several warps share the ring
-  int slot, parity;  // of the tile to take next
+  uint8_t* buf;     // [slots][U][K box, V box], 1024-byte aligned
+  Unit<U>* unit;    // [slots]
+  uint64_t* full;   // [slots]
+  uint64_t* empty;  // [slots]
+};
+// Where a warp is in a ring.
+template <int SLOTS>
+struct Turn {
+  int slot, parity;
+  __device__ __forceinline__ void step(int n) {  // at most SLOTS
+    slot += n;
+    if (slot >= SLOTS) {
+      slot -= SLOTS;
+      parity ^= 1;
+    }
+  }
+  __device__ __forceinline__ void advance(int n) {
+    parity ^= ((slot + n) / SLOTS) & 1;
+    slot = (slot + n) % SLOTS;
+  }
 };
 
 // What one warp makes of its tiles of one item: o (not divided by l), m (log2
@@ -272,318 +309,371 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 
-// Attention of query rows i0 .. i0 + 15 of an item over its tiles j0 .. j0 + cnt - 1 by
-// one warp, kUnits of them at a time: those of ring `at`.  `leader`: the warp that
-// fills the ring.  False if a wait ran out.
+// Brings one unit of tiles into a slot of the ring (a whole warp).
+//
+// Tiles with places behind the cached positions are brought by the lanes
+// (16-byte asynchronous copies): cached places from their page, drafted ones
+// from k and v.
+template <typename T16, int U>
+__device__ __forceinline__ void bring(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, Unit<U> unit,
+                                      const Ring<U>& ring, int slot) {
+  const int lane = threadIdx.x & 31, len = x.sp.len, end = len + x.sp.n;
+  bool whole = true;
+  int boxes = 0, tma[U];
+  const uint32_t bar = smem_u32(&ring.full[slot]), base = smem_u32(ring.buf + slot * U * kTileBytes);
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int at = unit.row[u], pos0 = unit.pos[u];
+    tma[u] = at;
+    whole = whole && at >= 0 && pos0 + kTile <= len &&
+            (a.window <= 0 || pos0 >= end - a.window || pos0 + kTile <= a.sinks);
+    if (at >= 0 && a.k && pos0 + kTile > len) {  // (the same for all lanes)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int y = (lane >> 3) + 4 * (k & 3), c = lane & 7, part = k >> 2, p = pos0 + y;
+        const T16* from = nullptr;
+        if (p < len)
+          from = a.pages + (static_cast<long long>(at - a.row0) + y + part * a.n_kv * a.page_size) * kHd + c * 8;
+        else if (p < end)
+          from = (part ? a.v : a.k) + (static_cast<long long>(x.b) * a.T + (p - len)) * a.ldkv + x.kvh * kHd + c * 8;
+        if (from)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(base + u * kTileBytes + part * kBoxBytes +
+                                                                         y * 128 + ((c ^ (y & 7)) << 4)),
+                       "l"(from)
+                       : "memory");
+      }
+      asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+      tma[u] = -1;
+    }
+    boxes += tma[u] >= 0 ? 1 : 0;
+  }
+  __syncwarp();
+  if (lane == 0) {
+    if (whole) unit.pos[0] = -1;
+    ring.unit[slot] = unit;
+    if (boxes > 0)
+      mbar_arrive_expect_tx(bar, boxes * kTileBytes);
+    else
+      mbar_arrive(bar);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (tma[u] >= 0) {
+        tma_load_2d(base + u * kTileBytes, map, bar, 0, tma[u]);
+        tma_load_2d(base + u * kTileBytes + kBoxBytes, map, bar, 0, tma[u] + a.n_kv * a.page_size);
+      }
+  }
+  __syncwarp();
+}
+
+// First positions and rows of tiles j0, j0 + step, ... of an item, 32 at a time: those
+// of tile i + lane of them.
+template <typename T16>
+__device__ __forceinline__ void find_tiles(const DraftArgs<T16>& a, const Item<T16>& x, int j0, int step, int i, int cnt,
+                                           int& row, int& pos) {
+  const int n = i + static_cast<int>(threadIdx.x & 31), t = j0 + n * step;
+  row = -1;
+  pos = (t < x.sp.ts ? t : x.sp.tw + (t - x.sp.ts)) * kTile;
+  if (n >= cnt) return;
+  const int c = pos / a.page_size, page = x.pages[c];
+  if (page >= 0 && page < a.n_pages)
+    row = page * a.page_rows + a.row0 + x.kvh * a.page_size + (pos - c * a.page_size);
+  else
+    record_error(a.err, kErrRange, kSitePagedPage);
+}
+
+// The warp that brings tiles j0 .. j0 + cnt - 1 of an item.  False if a wait ran out.
+template <typename T16, int U, int SLOTS>
+__device__ __forceinline__ bool bring_all(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, int j0,
+                                          int cnt, const Ring<U>& ring, Turn<SLOTS>& turn, bool& around) {
+  int row = -1, pos = 0;
+  for (int i = 0; i < cnt; i += U) {
+    if ((i & 31) == 0) find_tiles(a, x, j0, 1, i, cnt, row, pos);
+    if (around) {
+      const bool free = mbar_wait(smem_u32(&ring.empty[turn.slot]), turn.parity ^ 1);
+      if (!__all_sync(0xffffffffu, free)) {
+        if ((threadIdx.x & 31) == 0) record_error(a.err, kErrTimeout, kSitePagedLoad);
+        return false;
+      }
+    }
+    Unit<U> unit;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      unit.row[u] = __shfl_sync(0xffffffffu, row, (i + u) & 31);
+      unit.pos[u] = __shfl_sync(0xffffffffu, pos, (i + u) & 31);
+    }
+    bring<T16, U>(map, a, x, unit, ring, turn.slot);
+    turn.step(1);
+    if (turn.slot == 0) around = true;
+  }
+  return true;
+}
+
+// 16 query rows from i0 on, as the A operands of q . k.
+struct Query {
+  uint32_t a[4][4];
+};
+
+// One unit of tiles by one warp; MASKED: not every row sees all of it.
 //
 // The B fragments of q . k come out of shared memory as they are: sums over
 // dimensions are free in their order, so lane (r, j) reads of key rows r and r + 8
 // the dimensions 16j..16j+15 (q alike); those of p . v are read transposed.  With
 // the boxes' 128-byte swizzle (16-byte unit u of row x at u ^ (x & 7)) no bank is
 // read twice in a phase.
-//
-// Tiles with places behind the cached positions are brought by the lanes
-// (16-byte asynchronous copies): cached places from their page, drafted ones
-// from k and v, which are also stored in the page from here.
-template <typename T16, int WR, bool RIDE>
-__device__ __forceinline__ bool attend(const DraftArgs<T16>& a, const Item<T16>& x, int i0, bool leader, int at, int j0,
-                                       int cnt, Ring& ring, Tree& tree, Acc& acc) {
-  using S = Shape<WR, RIDE>;
-  constexpr int kStages = S::kStages, U = S::kUnits;
+template <typename T16, bool RIDE, bool MASKED, int U>
+__device__ __forceinline__ void take(const DraftArgs<T16>& a, const Item<T16>& x, int i0, const Query& q,
+                                     const uint8_t* tiles, const Unit<U>& unit, const Tree& tree, Acc& acc) {
   constexpr int kHalves = RIDE ? 1 : 2;  // row groups of a lane that hold rows
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
   const int len = x.sp.len, end = len + x.sp.n;
+  float s[U][2][4];
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const uint8_t* kr = tiles + u * kTileBytes + (r + 8 * e) * 128;
+      const uint4 k0 = *reinterpret_cast<const uint4*>(kr + (((2 * j) ^ r) << 4));
+      const uint4 k1 = *reinterpret_cast<const uint4*>(kr + (((2 * j + 1) ^ r) << 4));
+      mma16816_first<T16>(s[u][e], q.a[0][0], q.a[0][1], q.a[0][2], q.a[0][3], k0.x, k0.y);
+      mma16816<T16>(s[u][e], q.a[1][0], q.a[1][1], q.a[1][2], q.a[1][3], k0.z, k0.w);
+      mma16816<T16>(s[u][e], q.a[2][0], q.a[2][1], q.a[2][2], q.a[2][3], k1.x, k1.y);
+      mma16816<T16>(s[u][e], q.a[3][0], q.a[3][1], q.a[3][2], q.a[3][3], k1.z, k1.w);
+    }
+  uint32_t hidden = 0;  // bit 8u + 4e + 2g + k: score s[u][e][2g + k] is not visible
+  if constexpr (MASKED) {
+#pragma unroll
+    for (int g = 0; g < kHalves; ++g) {
+      const int i_row = min(i0 + 8 * g + r, x.rows - 1);
+      const int t = (x.row0 + i_row) / a.group;
+      const unsigned long long anc = tree.anc[t];
+      const int first = a.window > 0 ? len + tree.depth[t] + 1 - a.window : 0;
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int p = unit.pos[u] + 8 * e + 2 * j + k;
+            const bool seen = unit.row[u] >= 0 && (p < len ? (p >= first || p < a.sinks)
+                                                           : p < end && ((anc >> (p - len)) & 1));
+            if (!seen) {
+              s[u][e][2 * g + k] = -INFINITY;
+              hidden |= 1u << (8 * u + 4 * e + 2 * g + k);
+            }
+          }
+    }
+  }
+  float alpha[2] = {1.f, 1.f};
+#pragma unroll
+  for (int g = 0; g < kHalves; ++g) {
+    float mx = max3f(s[0][0][2 * g], s[0][0][2 * g + 1], fmaxf(s[0][1][2 * g], s[0][1][2 * g + 1]));
+#pragma unroll
+    for (int u = 1; u < U; ++u)
+      mx = max3f(max3f(mx, s[u][0][2 * g], s[u][0][2 * g + 1]), s[u][1][2 * g], s[u][1][2 * g + 1]);
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float mn = fmaxf(acc.m[g], mx * a.scale_log2);
+    const float ms = mn == -INFINITY ? 0.f : mn;  // every score so far is -inf
+    alpha[g] = acc.m[g] == mn ? 1.f : ex2_approx(acc.m[g] - ms);
+    acc.m[g] = mn;
+    const float bias = kShift<T16> - ms;
+    float sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) s[u][e][2 * g + k] = ex2_approx(fmaf(s[u][e][2 * g + k], a.scale_log2, bias));
+      sum += (s[u][0][2 * g] + s[u][0][2 * g + 1]) + (s[u][1][2 * g] + s[u][1][2 * g + 1]);
+    }
+    acc.l[g] = fmaf(acc.l[g], alpha[g], sum);
+  }
+  if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      acc.o[k][0] *= alpha[0];
+      acc.o[k][1] *= alpha[0];
+      acc.o[k][2] *= alpha[RIDE ? 0 : 1];
+      acc.o[k][3] *= alpha[RIDE ? 0 : 1];
+    }
+  }
+  const uint32_t v_row = smem_u32(tiles) + kBoxBytes + (lane & 15) * 128;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    uint32_t vf[8][2];
+#pragma unroll
+    for (int k = 0; k < 8; k += 2)
+      load_transposed(v_row + u * kTileBytes + (((k + (lane >> 4)) ^ (lane & 7)) << 4), vf[k][0], vf[k][1], vf[k + 1][0],
+                      vf[k + 1][1]);
+    bool odd = false;  // a value that is not finite, in a tile that not every row sees all of
+    if constexpr (MASKED) {
+      // places that nothing wrote may hold anything
+      const int left = unit.row[u] >= 0 ? end - unit.pos[u] - 2 * j : 0;
+      const uint32_t m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
+      const uint32_t m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        vf[k][0] &= m0;
+        vf[k][1] &= m1;
+        const uint32_t f0 = only_finite2<T16>(vf[k][0]), f1 = only_finite2<T16>(vf[k][1]);
+        odd |= f0 != vf[k][0] || f1 != vf[k][1];
+        vf[k][0] = f0;
+        vf[k][1] = f1;
+      }
+      odd = __any_sync(0xffffffffu, odd);
+    }
+    uint32_t ph[2][2], pl[2][2];  // [position half][row half]
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int g = 0; g < kHalves; ++g) split2<T16>(s[u][e][2 * g], s[u][e][2 * g + 1], ph[e][g], pl[e][g]);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (RIDE) {
+        mma16816<T16>(acc.o[k], ph[0][0], pl[0][0], ph[1][0], pl[1][0], vf[k][0], vf[k][1]);
+      } else {
+        mma16816<T16>(acc.o[k], ph[0][0], ph[0][1], ph[1][0], ph[1][1], vf[k][0], vf[k][1]);
+        mma16816<T16>(acc.o[k], pl[0][0], pl[0][1], pl[1][0], pl[1][1], vf[k][0], vf[k][1]);
+      }
+    }
+    if constexpr (MASKED) {
+      if (odd) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if ((hidden >> (8 * u + 4 * e + k)) & 1) s[u][e][k] = -1.f;
+        add_not_finite<T16, RIDE>(acc, s[u], tiles + u * kTileBytes + kBoxBytes, min(kTile, end - unit.pos[u]));
+      }
+    }
+  }
+}
+
+// The drafted tokens' K and V of a unit from shared memory into their pages.
+template <typename T16, int U>
+__device__ __forceinline__ void store_drafts(const DraftArgs<T16>& a, const Item<T16>& x, const uint8_t* tiles,
+                                             const Unit<U>& unit) {
+  const int lane = threadIdx.x & 31, len = x.sp.len, end = len + x.sp.n;
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (unit.row[u] < 0 || unit.pos[u] + kTile <= len) continue;
+    const int page = x.pages[unit.pos[u] / a.page_size];
+    if (a.refs[page] > 1) {  // not into a page that other sequences read
+      if (lane == 0) record_error(a.err, kErrRange, kSitePagedShared);
+      continue;
+    }
+#pragma unroll 1
+    for (int k = 0; k < 8; ++k) {
+      const int y = (lane >> 3) + 4 * (k & 3), c = lane & 7, part = k >> 2, p = unit.pos[u] + y;
+      if (p >= len && p < end)
+        *reinterpret_cast<uint4*>(
+            a.pages + (static_cast<long long>(unit.row[u] - a.row0) + y + part * a.n_kv * a.page_size) * kHd + c * 8) =
+            *reinterpret_cast<const uint4*>(tiles + u * kTileBytes + part * kBoxBytes + y * 128 + ((c ^ (y & 7)) << 4));
+    }
+  }
+}
+
+// Attention of query rows i0 .. i0 + 15 of an item over its tiles j0 .. j0 + cnt - 1 by
+// one warp: units at, at + kGroups, ... of them; `first`: of the warps with the same
+// units the one that stores drafted K and V.  False if a wait ran out.
+template <typename T16, int WR, bool RIDE>
+__device__ __forceinline__ bool attend(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, int i0,
+                                       bool first, int at, int j0, int cnt, const Ring<Shape<WR, RIDE>::kUnit>& ring,
+                                       Turn<Shape<WR, RIDE>::kSlots>& turn, Tree& tree, Acc& acc) {
+  using S = Shape<WR, RIDE>;
+  constexpr int U = S::kUnit, kSlots = S::kSlots;
+  const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc.o[i][e] = 0.f;
   acc.m[0] = acc.m[1] = -INFINITY;
   acc.l[0] = acc.l[1] = 0.f;
-  const int units = (cnt + U - 1) / U, mine = units > at ? (units - at + S::kRings - 1) / S::kRings : 0;
-  if (mine == 0) return true;
-  // first position of tile u of this ring's i-th unit
-  auto place = [&](int i, int u) {
-    const int t = j0 + (at + i * S::kRings) * U + u;
-    return (t < x.sp.ts ? t : x.sp.tw + (t - x.sp.ts)) * kTile;
-  };
-  auto there = [&](int i, int u) { return U == 1 || (at + i * S::kRings) * U + u < cnt; };
-  // first row (K) of a tile in the pool, -1 when its page is not there (or there is no such tile); lane k of
-  // tile k of the units from i on
-  auto find_rows = [&](int i) {
-    const int n = i + lane / U, u = lane % U;
-    if (n >= mine || !there(n, u)) return -1;
-    const int pos = place(n, u), c = pos / a.page_size;
-    const int page = x.pages[c];
-    if (page >= 0 && page < a.n_pages)
-      return page * a.page_rows + a.row0 + x.kvh * a.page_size + (pos - c * a.page_size);
-    record_error(a.err, kErrRange, kSitePagedPage);
-    return -1;
-  };
-  int fetch32 = -1, rows32 = -1, fetched = 0;  // of the units to fetch, and of those to take
-  auto issue = [&](int slot) {
-    const int i = fetched++;
-    if (i % (32 / U) == 0) fetch32 = find_rows(i);
-    const uint32_t bar = smem_u32(&ring.full[slot]), base = smem_u32(ring.buf + slot * S::kSlotBytes);
-    int boxes = 0, rows[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rows[u] = __shfl_sync(0xffffffffu, fetch32, (i * U + u) & 31);
-      const uint32_t dst = base + u * kTileBytes;
-      const int pos0 = place(i, u);
-      if (rows[u] >= 0 && a.k && pos0 + kTile > len) {  // (the same for all lanes)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int y = (lane >> 3) + 4 * (k & 3), c = lane & 7, part = k >> 2, p = pos0 + y;
-          const T16* from = nullptr;
-          if (p < len)
-            from = a.pages + (static_cast<long long>(rows[u] - a.row0) + y + part * a.n_kv * a.page_size) * kHd + c * 8;
-          else if (p < end)
-            from = (part ? a.v : a.k) + (static_cast<long long>(x.b) * a.T + (p - len)) * a.ldkv + x.kvh * kHd + c * 8;
-          if (from)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + part * kBoxBytes + y * 128 +
-                                                                           ((c ^ (y & 7)) << 4)),
-                         "l"(from)
-                         : "memory");
-        }
-        asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
-        rows[u] = -1;
-      }
-      boxes += rows[u] >= 0 ? 1 : 0;
-    }
-    __syncwarp();
-    if (lane == 0) {
-      if (boxes > 0)
-        mbar_arrive_expect_tx(bar, boxes * kTileBytes);
-      else
-        mbar_arrive(bar);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (rows[u] >= 0) {
-          tma_load_2d(base + u * kTileBytes, ring.map, bar, 0, rows[u]);
-          tma_load_2d(base + u * kTileBytes + kBoxBytes, ring.map, bar, 0, rows[u] + a.n_kv * a.page_size);
-        }
+  const int units = (cnt + U - 1) / U, mine = units > at ? (units - at + S::kGroups - 1) / S::kGroups : 0;
+  // a warp with a ring of its own: tiles j0 + at, j0 + at + kGroups, ...
+  int row = -1, pos = 0, fetched = 0;
+  auto next = [&](int slot) {
+    if constexpr (!S::kBringer) {
+      if ((fetched & 31) == 0) find_tiles(a, x, j0 + at, S::kGroups, fetched, mine, row, pos);
+      Unit<U> unit;
+      unit.row[0] = __shfl_sync(0xffffffffu, row, fetched & 31);
+      unit.pos[0] = __shfl_sync(0xffffffffu, pos, fetched & 31);
+      ++fetched;
+      bring<T16, U>(map, a, x, unit, ring, slot);
     }
   };
-  if (leader) {
-    int slot = ring.slot;
+  if constexpr (!S::kBringer) {
+    Turn<kSlots> ahead = turn;
 #pragma unroll 1
-    for (int s = 0; s < kStages && fetched < mine; ++s) {
-      issue(slot);
-      slot = slot + 1 == kStages ? 0 : slot + 1;
+    for (int s = 0; s < kSlots && fetched < mine; ++s) {
+      next(ahead.slot);
+      ahead.step(1);
     }
   }
   // q: lane (r, j) holds dimensions 16j..16j+15 of rows r and r + 8
-  uint4 qf[4] = {};
+  Query q;
+  {
+    uint4 f[4] = {};
 #pragma unroll
-  for (int g = 0; g < kHalves; ++g)
-    if (i0 + 8 * g + r < x.rows) {
-      const uint4* from = reinterpret_cast<const uint4*>(q_row(a, x, i0 + 8 * g + r) + 16 * j);
-      qf[2 * g] = from[0];
-      qf[2 * g + 1] = from[1];
-    }
-  const bool idle = i0 >= x.rows;  // no rows for this warp
-  bool have_tree = false;
-  // where this lane reads: of key rows r and r + 8, and of value row lane & 15
-  const int k_at0 = r * 128 + (((2 * j) ^ r) << 4), k_at1 = r * 128 + (((2 * j + 1) ^ r) << 4);
-  const int v_row = kBoxBytes + (lane & 15) * 128, v_unit = lane >> 4, v_swz = lane & 7;
-
+    for (int g = 0; g < (RIDE ? 1 : 2); ++g)
+      if (i0 + 8 * g + r < x.rows) {
+        const uint4* from = reinterpret_cast<const uint4*>(q_row(a, x, i0 + 8 * g + r) + 16 * j);
+        f[2 * g] = from[0];
+        f[2 * g + 1] = from[1];
+      }
+    const uint32_t q_of[4][4] = {{f[0].x, f[2].x, f[0].y, f[2].y},
+                                 {f[0].z, f[2].z, f[0].w, f[2].w},
+                                 {f[1].x, f[3].x, f[1].y, f[3].y},
+                                 {f[1].z, f[3].z, f[1].w, f[3].w}};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q.a[i >> 2][i & 3] = q_of[i >> 2][i & 3];
+  }
+  const bool idle = i0 >= x.rows || mine == 0;  // no rows, or no tiles, for this warp
+  // The tree matters where drafted places are, and to a window; it is made while the first tiles are on their
+  // way.
+  const int last = j0 + cnt - 1;
+  const bool drafts = ((last < x.sp.ts ? last : x.sp.tw + last - x.sp.ts) + 1) * kTile > x.sp.len;
+  if ((drafts || a.window > 0) && !idle) build_tree(a, x.b, x.sp, tree);
+  Turn<kSlots> now = turn;
+  if constexpr (S::kBringer) now.step(at);
   for (int i = 0; i < mine; ++i) {
-    const bool ok = mbar_wait(smem_u32(&ring.full[ring.slot]), ring.parity);
+    const bool ok = mbar_wait(smem_u32(&ring.full[now.slot]), now.parity);
     if (!__all_sync(0xffffffffu, ok)) {
       if (lane == 0) {
         record_error(a.err, kErrTimeout, kSitePagedLoad);
-        for (int s = 0; s < kStages && i + s < mine; ++s) {  // the loads in flight must not outlive the CTA
-          const int k = ring.slot + s;
-          (void)mbar_wait(smem_u32(&ring.full[k % kStages]), ring.parity ^ (k >= kStages ? 1 : 0));
-        }
+        if constexpr (!S::kBringer)
+          for (int s = 0; s < kSlots && i + s < mine; ++s) {  // the loads in flight must not outlive the CTA
+            (void)mbar_wait(smem_u32(&ring.full[now.slot]), now.parity);
+            now.step(1);
+          }
       }
       __syncwarp();
       return false;
     }
-    if (i % (32 / U) == 0) rows32 = find_rows(i);
-    uint8_t* const tiles = ring.buf + ring.slot * S::kSlotBytes;
-    int rows[U], pos0[U];
-    bool any = false, whole = true;  // every row sees all of the tiles
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      rows[u] = __shfl_sync(0xffffffffu, rows32, (i * U + u) & 31);
-      pos0[u] = place(i, u);
-      any |= rows[u] >= 0;
-      whole = whole && rows[u] >= 0 && pos0[u] + kTile <= len &&
-              (a.window <= 0 || pos0[u] >= end - a.window || pos0[u] + kTile <= a.sinks);
-    }
-    if (any && (!idle || leader)) {
-      if (!whole) {
-        if (!have_tree) {
-          build_tree(a, x.b, x.sp, tree);
-          have_tree = true;
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          // the drafted tokens' K and V into their page
-          if (!leader || !a.k || x.block != 0 || rows[u] < 0 || pos0[u] + kTile <= len) continue;
-          const int page = x.pages[pos0[u] / a.page_size];
-          if (a.refs[page] > 1) {  // not into a page that other sequences read
-            if (lane == 0) record_error(a.err, kErrRange, kSitePagedShared);
-            continue;
-          }
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int y = (lane >> 3) + 4 * (k & 3), c = lane & 7, part = k >> 2, p = pos0[u] + y;
-            if (p >= len && p < end)
-              *reinterpret_cast<uint4*>(
-                  a.pages + (static_cast<long long>(rows[u] - a.row0) + y + part * a.n_kv * a.page_size) * kHd + c * 8) =
-                  *reinterpret_cast<const uint4*>(tiles + u * kTileBytes + part * kBoxBytes + y * 128 +
-                                                  ((c ^ (y & 7)) << 4));
-          }
-        }
-      }
-      float s[U][2][4];
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint8_t* kr = tiles + u * kTileBytes + e * 1024;
-          const uint4 k0 = *reinterpret_cast<const uint4*>(kr + k_at0);
-          const uint4 k1 = *reinterpret_cast<const uint4*>(kr + k_at1);
-          mma16816_first<T16>(s[u][e], qf[0].x, qf[2].x, qf[0].y, qf[2].y, k0.x, k0.y);
-          mma16816<T16>(s[u][e], qf[0].z, qf[2].z, qf[0].w, qf[2].w, k0.z, k0.w);
-          mma16816<T16>(s[u][e], qf[1].x, qf[3].x, qf[1].y, qf[3].y, k1.x, k1.y);
-          mma16816<T16>(s[u][e], qf[1].z, qf[3].z, qf[1].w, qf[3].w, k1.z, k1.w);
-        }
-      uint32_t hidden = 0;  // bit 8u + 4e + 2g + k: score s[u][e][2g + k] is not visible
-      if (!whole) {
-#pragma unroll
-        for (int g = 0; g < kHalves; ++g) {
-          const int i_row = min(i0 + 8 * g + r, x.rows - 1);
-          const int t = (x.row0 + i_row) / a.group;
-          const unsigned long long anc = tree.anc[t];
-          const int first = a.window > 0 ? len + tree.depth[t] + 1 - a.window : 0;
-#pragma unroll
-          for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const int p = pos0[u] + 8 * e + 2 * j + k;
-                const bool seen = rows[u] >= 0 && (p < len ? (p >= first || p < a.sinks)
-                                                           : p < end && ((anc >> (p - len)) & 1));
-                if (!seen) {
-                  s[u][e][2 * g + k] = -INFINITY;
-                  hidden |= 1u << (8 * u + 4 * e + 2 * g + k);
-                }
-              }
-        }
-      }
-      float alpha[2] = {1.f, 1.f};
-#pragma unroll
-      for (int g = 0; g < kHalves; ++g) {
-        float mx = max3f(s[0][0][2 * g], s[0][0][2 * g + 1], s[0][1][2 * g]);
-        if constexpr (U == 1)
-          mx = fmaxf(mx, s[0][1][2 * g + 1]);
-        else
-          mx = max3f(max3f(mx, s[0][1][2 * g + 1], s[U - 1][0][2 * g]), s[U - 1][0][2 * g + 1],
-                     fmaxf(s[U - 1][1][2 * g], s[U - 1][1][2 * g + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(acc.m[g], mx * a.scale_log2);
-        const float ms = mn == -INFINITY ? 0.f : mn;  // every score so far is -inf
-        alpha[g] = acc.m[g] == mn ? 1.f : ex2_approx(acc.m[g] - ms);
-        acc.m[g] = mn;
-        const float bias = kShift<T16> - ms;
-        float sum = 0.f;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              s[u][e][2 * g + k] = ex2_approx(fmaf(s[u][e][2 * g + k], a.scale_log2, bias));
-          sum += (s[u][0][2 * g] + s[u][0][2 * g + 1]) + (s[u][1][2 * g] + s[u][1][2 * g + 1]);
-        }
-        acc.l[g] = fmaf(acc.l[g], alpha[g], sum);
-      }
-      if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          acc.o[k][0] *= alpha[0];
-          acc.o[k][1] *= alpha[0];
-          acc.o[k][2] *= alpha[RIDE ? 0 : 1];
-          acc.o[k][3] *= alpha[RIDE ? 0 : 1];
-        }
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        uint32_t vf[8][2];
-        const uint32_t vb = smem_u32(tiles + u * kTileBytes) + v_row;
-#pragma unroll
-        for (int k = 0; k < 8; k += 2)
-          load_transposed(vb + (((k + v_unit) ^ v_swz) << 4), vf[k][0], vf[k][1], vf[k + 1][0], vf[k + 1][1]);
-        bool odd = false;  // a value that is not finite, in a tile that not every row sees all of
-        if (!whole) {
-          // places that nothing wrote may hold anything
-          const int left = rows[u] >= 0 ? end - pos0[u] - 2 * j : 0;
-          const uint32_t m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
-          const uint32_t m1 = left >= 10 ? 0xffffffffu : left == 9 ? 0xffffu : 0u;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            vf[k][0] &= m0;
-            vf[k][1] &= m1;
-            const uint32_t f0 = only_finite2<T16>(vf[k][0]), f1 = only_finite2<T16>(vf[k][1]);
-            odd |= f0 != vf[k][0] || f1 != vf[k][1];
-            vf[k][0] = f0;
-            vf[k][1] = f1;
-          }
-          odd = __any_sync(0xffffffffu, odd);
-        }
-        uint32_t ph[2][2], pl[2][2];  // [position half][row half]
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int g = 0; g < kHalves; ++g) split2<T16>(s[u][e][2 * g], s[u][e][2 * g + 1], ph[e][g], pl[e][g]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          if constexpr (RIDE) {
-            mma16816<T16>(acc.o[k], ph[0][0], pl[0][0], ph[1][0], pl[1][0], vf[k][0], vf[k][1]);
-          } else {
-            mma16816<T16>(acc.o[k], ph[0][0], ph[0][1], ph[1][0], ph[1][1], vf[k][0], vf[k][1]);
-            mma16816<T16>(acc.o[k], pl[0][0], pl[0][1], pl[1][0], pl[1][1], vf[k][0], vf[k][1]);
-          }
-        }
-        if (odd) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if ((hidden >> (8 * u + 4 * e + k)) & 1) s[u][e][k] = -1.f;
-          add_not_finite<T16, RIDE>(acc, s[u], tiles + u * kTileBytes + kBoxBytes, min(kTile, end - pos0[u]));
-        }
+    if (!idle) {
+      const uint8_t* tiles = ring.buf + now.slot * U * kTileBytes;
+      const Unit<U> unit = ring.unit[now.slot];
+      if (unit.pos[0] < 0) {
+        take<T16, RIDE, false, U>(a, x, i0, q, tiles, unit, tree, acc);
+      } else if (unit.row[0] >= 0 || unit.row[U - 1] >= 0) {
+        if (first && a.k && x.block == 0) store_drafts(a, x, tiles, unit);
+        take<T16, RIDE, true, U>(a, x, i0, q, tiles, unit, tree, acc);
       }
     }
-    // the slot is read: the unit kStages further on (where warps share the ring, into the slot before, which
-    // the others have read by now)
     __syncwarp();
-    if constexpr (WR == 1) {
-      if (lane == 0) fence_proxy_async_smem();
-      if (fetched < mine) issue(ring.slot);
+    if constexpr (S::kBringer) {
+      if (lane == 0) mbar_arrive(smem_u32(&ring.empty[now.slot]));
+      now.step(S::kGroups);
     } else {
-      if (lane == 0) mbar_arrive(smem_u32(&ring.empty[ring.slot]));
-      if (leader && i > 0 && fetched < mine) {
-        const int before = ring.slot == 0 ? kStages - 1 : ring.slot - 1;
-        const bool free = mbar_wait(smem_u32(&ring.empty[before]), ring.slot == 0 ? ring.parity ^ 1 : ring.parity);
-        if (!__all_sync(0xffffffffu, free)) {
-          if (lane == 0) record_error(a.err, kErrTimeout, kSitePagedLoad);
-          fetched = mine;  // (nothing more is brought: the waits for it run out)
-        } else {
-          issue(before);
-        }
-      }
-    }
-    if (++ring.slot == kStages) {
-      ring.slot = 0;
-      ring.parity ^= 1;
+      if (lane == 0) fence_proxy_async_smem();
+      if (fetched < mine) next(now.slot);
+      now.step(1);
     }
   }
+  if constexpr (S::kBringer)
+    turn.advance(units);
+  else
+    turn = now;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {  // sums over the four lanes of a row
     acc.l[g] += __shfl_xor_sync(0xffffffffu, acc.l[g], 1);
@@ -667,27 +757,28 @@ __device__ __forceinline__ Item<T16> item_of(const DraftArgs<T16>& a, int b, int
 // Work is cut into equal runs of tiles over all (sequence, key-value head, row
 // block) items laid end to end, one run per CTA, whatever the lengths are.  A CTA
 // that holds all tiles of an item writes its output, pieces of an item go to the
-// workspace and a second kernel joins them.  Rings of one or two warps take the
-// tiles of a piece in turn and meet in shared memory.
+// workspace and a second kernel joins them.  Groups of warps that took tiles of a
+// piece in turn meet in shared memory.
 template <typename T16, int WR, bool RIDE>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+__global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>::kCtas))
     draft_attn(const __grid_constant__ CUtensorMap map, const DraftArgs<T16> a) {
   using S = Shape<WR, RIDE>;
-  constexpr int kRings = S::kRings;
+  constexpr int kGroups = S::kGroups, kRows = S::kRows, kSlots = S::kSlots, U = S::kUnit;
   extern __shared__ uint8_t s_raw[];
-  __shared__ __align__(8) uint64_t s_bar[2][kRings * S::kStages];
+  __shared__ __align__(8) uint64_t s_bar[2][S::kRings * kSlots];
+  __shared__ __align__(16) Unit<U> s_unit[S::kRings * kSlots];
   __shared__ int s_sum[kWarps];
-  __shared__ float2 s_ml[kRings * S::kRows];
+  __shared__ float2 s_ml[kGroups * kRows];
   __shared__ Tree s_tree[kWarps];
   uint8_t* s_tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
-  int* s_base = reinterpret_cast<int*>(s_tiles + kRings * S::kRingBytes);  // [n_seq + 1]
+  uint8_t* s_meet = s_tiles + (S::kMeetBytes ? S::kRings * S::kRingBytes : 0);
+  constexpr int kMeetStep = S::kMeetBytes ? kRows * kHd * 4 : S::kRingBytes;  // from group to group
+  int* s_base = reinterpret_cast<int*>(s_tiles + S::kRings * S::kRingBytes + S::kMeetBytes);  // [n_seq + 1]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // which ring, and which 16 rows: not always the last ones on the same quarter of the SM
-  const int at = warp / WR, rank = (warp + static_cast<int>(blockIdx.x)) % WR;
-  const bool leader = rank == 0;
-  Ring ring{&map, s_tiles + at * S::kRingBytes, s_bar[0] + at * S::kStages, s_bar[1] + at * S::kStages, 0, 0};
+  const int of = S::kBringer ? 0 : warp * kSlots;  // this warp's ring
+  const Ring<U> ring{s_tiles + of * U * kTileBytes, s_unit + of, s_bar[0] + of, s_bar[1] + of};
   if (tid == 0) {
-    for (int s = 0; s < kRings * S::kStages; ++s) {
+    for (int s = 0; s < S::kRings * kSlots; ++s) {
       mbar_init(smem_u32(&s_bar[0][s]), 1);
       mbar_init(smem_u32(&s_bar[1][s]), WR);
     }
@@ -697,11 +788,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   griddep_wait();
   // base[b] = tiles of all items of sequences before b
   int carry = 0;
-  for (int b0 = 0; b0 < a.n_seq; b0 += kThreads) {
+  for (int b0 = 0; b0 < a.n_seq; b0 += kTakers) {
     const int b = b0 + tid;
     int v = 0;
-    if (b < a.n_seq) {
-      const Span sp = span_of<S::kRows>(a, b, blockIdx.x == 0);
+    if (tid < kTakers && b < a.n_seq) {
+      const Span sp = span_of<kRows>(a, b, blockIdx.x == 0);
       v = max(sp.nt, 0) * a.n_kv * sp.blocks;
     }
     int incl = v;
@@ -710,12 +801,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
       if (lane >= o) incl += up;
     }
-    if (lane == 31) s_sum[warp] = incl;
+    if (lane == 31 && warp < kWarps) s_sum[warp] = incl;
     __syncthreads();
     int before = carry;
-    for (int w = 0; w < warp; ++w) before += s_sum[w];
-    if (b < a.n_seq) s_base[b] = before + incl - v;
-    for (int w = 0; w < kWarps; ++w) carry += s_sum[w];
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += s_sum[w];
+      carry += s_sum[w];
+    }
+    if (tid < kTakers && b < a.n_seq) s_base[b] = before + incl - v;
     __syncthreads();
   }
   if (tid == 0) s_base[a.n_seq] = carry;
@@ -723,15 +816,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   const int total = carry;
   const int run = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinRun);
   if (blockIdx.x == 0) {
-    for (int b = tid; b <= a.n_seq; b += kThreads) a.plan[b] = s_base[b];
+    for (int b = tid; b <= a.n_seq; b += S::kThreads) a.plan[b] = s_base[b];
     if (tid == 0) a.plan[a.n_seq + 1] = run;
   }
   const long long t_first = static_cast<long long>(blockIdx.x) * run;
   if (t_first >= total) return;
-  int t = static_cast<int>(t_first);
   const int t_end = static_cast<int>(min(t_first + run, static_cast<long long>(total)));
-
-  while (t < t_end) {
+  // the piece that begins at t: its item, first tile in it, and tiles
+  auto piece_at = [&](int t, int& j0, int& cnt) {
     int lo = 0, hi = a.n_seq;  // last b with base[b] <= t
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -740,54 +832,74 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       else
         hi = mid;
     }
-    const Span sp = span_of<S::kRows>(a, lo, false);
+    const Span sp = span_of<kRows>(a, lo, false);
     const int item = (t - s_base[lo]) / sp.nt;
-    const int j0 = (t - s_base[lo]) - item * sp.nt;  // first tile of this piece within the item
-    const int cnt = min(sp.nt - j0, t_end - t);
-    const Item<T16> x = item_of(a, lo, item, sp, S::kRows);
-    const bool all = cnt == sp.nt;
+    j0 = (t - s_base[lo]) - item * sp.nt;
+    cnt = min(sp.nt - j0, t_end - t);
+    return item_of(a, lo, item, sp, kRows);
+  };
+  Turn<kSlots> turn{0, 0};
+  if constexpr (S::kBringer) {
+    if (warp == kWarps) {
+      bool around = false;
+      for (int t = static_cast<int>(t_first); t < t_end;) {
+        int j0, cnt;
+        const Item<T16> x = piece_at(t, j0, cnt);
+        if (!bring_all<T16, U, kSlots>(&map, a, x, j0, cnt, ring, turn, around)) break;
+        t += cnt;
+      }
+      // copies must not outlive the CTA: each slot's last use, from the oldest on
+      for (int s = around ? 0 : kSlots - turn.slot; s < kSlots; ++s) {
+        const int slot = (turn.slot + s) % kSlots;
+        (void)mbar_wait(smem_u32(&ring.full[slot]), slot < turn.slot ? turn.parity : turn.parity ^ 1);
+      }
+      return;
+    }
+  }
+  // which units, and which 16 rows: not always the last ones on the same quarter of the SM
+  const int at = warp / WR, rank = (warp + static_cast<int>(blockIdx.x)) % WR, i0 = RIDE ? 0 : 16 * rank;
+  for (int t = static_cast<int>(t_first); t < t_end;) {
+    int j0, cnt;
+    const Item<T16> x = piece_at(t, j0, cnt);
+    const bool all = cnt == x.sp.nt;
     const long long part = 2ll * blockIdx.x + (t == static_cast<int>(t_first) ? 0 : 1);
-    const int i0 = RIDE ? 0 : 16 * rank;
     Acc acc;
-    const bool ok = attend<T16, WR, RIDE>(a, x, i0, leader, at, j0, cnt, ring, s_tree[warp], acc);
+    const bool ok = attend<T16, WR, RIDE>(&map, a, x, i0, rank == 0, at, j0, cnt, ring, turn, s_tree[warp], acc);
     t += cnt;
     __syncwarp();
-    if constexpr (kRings == 1) {
-      if (!ok) {
-        // (the others' waits run out, too)
-      } else if (all) {
+    if constexpr (kGroups == 1) {
+      if (!ok) return;
+      if (all)
         put_rows(a, x, i0, acc);
-      } else {
-        put_piece<T16, RIDE>(acc, x.rows - i0, a.part_o + (part * S::kRows + i0) * kHd, a.part_ml + part * S::kRows + i0);
-      }
+      else
+        put_piece<T16, RIDE>(acc, x.rows - i0, a.part_o + (part * kRows + i0) * kHd, a.part_ml + part * kRows + i0);
       if (t >= t_end) griddep_launch_dependents();
-      fence_proxy_async_smem();
-      if (!__syncthreads_and(ok)) return;  // (and every warp is through with the ring)
     } else {
-      // a warp's result (fp32 rows of 64) takes the place of its ring
-      if (WR > 1 && !__syncthreads_and(ok)) return;
-      const int pieces = min((cnt + S::kUnits - 1) / S::kUnits, kRings);
+      const int pieces = min((cnt + U - 1) / U, kGroups);
       if (at < pieces && ok)
-        put_piece<T16, RIDE>(acc, x.rows - i0, reinterpret_cast<float*>(ring.buf) + i0 * kHd, s_ml + at * S::kRows + i0);
-      if (!__syncthreads_and(ok)) return;
+        put_piece<T16, RIDE>(acc, x.rows - i0, reinterpret_cast<float*>(s_meet + at * kMeetStep) + i0 * kHd,
+                             s_ml + at * kRows + i0);
+      __syncwarp();
+      if (!named_bar_and(ok, 1, kTakers)) return;
       if (t >= t_end) griddep_launch_dependents();
-      for (int k = tid; k < x.rows * 16; k += kThreads) {
+      for (int k = tid; k < x.rows * 16; k += kTakers) {
         const int i = k >> 4, d4 = k & 15;
         float M = -INFINITY, L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < pieces; ++w)
-          merge(o, M, L, *reinterpret_cast<const float4*>(s_tiles + w * S::kRingBytes + (i * kHd + 4 * d4) * 4),
-                s_ml[w * S::kRows + i]);
+          merge(o, M, L, *reinterpret_cast<const float4*>(s_meet + w * kMeetStep + (i * kHd + 4 * d4) * 4),
+                s_ml[w * kRows + i]);
         if (all) {
           put_row(a, x, i, d4, o, M, L);
         } else {
-          *reinterpret_cast<float4*>(a.part_o + (part * S::kRows + i) * kHd + 4 * d4) = o;
-          if (d4 == 0) a.part_ml[part * S::kRows + i] = make_float2(M, L);
+          *reinterpret_cast<float4*>(a.part_o + (part * kRows + i) * kHd + 4 * d4) = o;
+          if (d4 == 0) a.part_ml[part * kRows + i] = make_float2(M, L);
         }
       }
-      // the rings take tiles again: generic accesses before asynchronous writes
-      fence_proxy_async_smem();
-      __syncthreads();
+      // (a ring takes tiles again: generic accesses before asynchronous writes)
+      if (!S::kBringer) fence_proxy_async_smem();
+      __syncwarp();
+      named_bar_sync(1, kTakers);
     }
   }
 }
@@ -863,10 +975,12 @@ int rows_of(int T, int group) {
   return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
 }
 
+int ctas_of(int rows) { return rows <= 16 ? Shape<1, false>::kCtas : Shape<2, false>::kCtas; }
+
 template <typename T16, int WR, bool RIDE>
 cudaError_t launch_kind(const CUtensorMap& map, const DraftArgs<T16>& a, cudaStream_t s) {
   using S = Shape<WR, RIDE>;
-  constexpr int kFixed = S::kRings * S::kRingBytes + 1024;
+  constexpr int kFixed = S::kRings * S::kRingBytes + S::kMeetBytes + 1024;
   static int configured[64] = {0};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -882,7 +996,7 @@ cudaError_t launch_kind(const CUtensorMap& map, const DraftArgs<T16>& a, cudaStr
     configured[dev] = 1;
   }
   const int sms = num_sms();
-  cudaError_t e = launch_pdl(draft_attn<T16, WR, RIDE>, sms * kCtasPerSm, kThreads, kFixed + (a.n_seq + 1) * 4, s, 0,
+  cudaError_t e = launch_pdl(draft_attn<T16, WR, RIDE>, sms * S::kCtas, S::kThreads, kFixed + (a.n_seq + 1) * 4, s, 0,
                              map, a);
   if (e != cudaSuccess) return e;
   const int max_blocks = (a.T * a.group + S::kRows - 1) / S::kRows;
@@ -930,7 +1044,7 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   a.sinks = sinks;
   a.scale_log2 = score_scale * 1.4426950408889634f;
   const int rows = rows_of(T, a.group);
-  const size_t slots = 2ull * num_sms() * kCtasPerSm * rows;
+  const size_t slots = 2ull * num_sms() * ctas_of(rows) * rows;
   char* base = static_cast<char*>(ws);
   a.plan = reinterpret_cast<int*>(base);
   base += align256((static_cast<size_t>(c->n_seq) + 2) * 4);
@@ -953,7 +1067,8 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
 }  // namespace
 
 size_t attention_draft_workspace(const gpt2_paged_cache* c, int T, int n_head) {
-  const size_t slots = 2ull * num_sms() * kCtasPerSm * rows_of(T, n_head / c->n_kv_head);
+  const int rows = rows_of(T, n_head / c->n_kv_head);
+  const size_t slots = 2ull * num_sms() * ctas_of(rows) * rows;
   return align256((static_cast<size_t>(c->n_seq) + 2) * 4) + align256(slots * sizeof(float2)) +
          align256(slots * kHd * 4);
 }
