@@ -48,6 +48,10 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
 // out-of-range elements read as zero.  False if the driver rejects it.
 bool encode_tma_2d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
                    uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer);
+// The same over four dimensions, the innermost first; strides in bytes, from the
+// second dimension's on.
+bool encode_tma_4d(CUtensorMap* map, CUtensorMapDataType dt, const void* base, const uint64_t (&dims)[4],
+                   const uint64_t (&stride_bytes)[3], const uint32_t (&box)[4]);
 
 // Each launcher validates nothing beyond what its kernel needs (the C-ABI
 // layer has checked the arguments) and returns the launch status.

@@ -72,6 +72,7 @@ struct DraftArgs {
   float* lse;  // nullable, [n_seq * T, H]
   T16* pages;  // the layer's part of page 0
   int row0, page_rows;  // the pool as rows of 64: the layer's first row, rows per page
+  int n_layer, layer;
   const int32_t* table;
   const int32_t* lens;
   const int32_t* refs;
@@ -123,8 +124,9 @@ struct Tree {
   uint8_t depth[64];
 };
 
+// The paths up to the cached positions.
 template <typename T16>
-__device__ __forceinline__ void build_tree(const DraftArgs<T16>& a, int b, const Span& sp, Tree& tree) {
+__device__ __forceinline__ void find_ancestors(const DraftArgs<T16>& a, int b, const Span& sp, Tree& tree) {
   const int lane = threadIdx.x & 31;
   int up[2];  // the nearest ancestor that anc does not have yet
 #pragma unroll
@@ -132,7 +134,7 @@ __device__ __forceinline__ void build_tree(const DraftArgs<T16>& a, int b, const
     const int t = lane + 32 * e;
     up[e] = -1;
     if (t < sp.n) {
-      int p = a.parents ? a.parents[static_cast<long long>(b) * a.T + t] : t - 1;
+      int p = a.parents[static_cast<long long>(b) * a.T + t];
       if (p < -1 || p >= t) {
         record_error(a.err, kErrRange, kSiteDraftParent);
         p = -1;
@@ -164,19 +166,31 @@ __device__ __forceinline__ void build_tree(const DraftArgs<T16>& a, int b, const
     }
     __syncwarp();
   }
-  unsigned long long own[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    own[e] = tree.anc[lane + 32 * e];
-    tree.depth[lane + 32 * e] = static_cast<uint8_t>(__popcll(own[e]) - 1);
-  }
+  for (int e = 0; e < 2; ++e)
+    tree.depth[lane + 32 * e] = static_cast<uint8_t>(__popcll(tree.anc[lane + 32 * e]) - 1);
   __syncwarp();
+}
+
+template <typename T16>
+__device__ __forceinline__ void build_tree(const DraftArgs<T16>& a, int b, const Span& sp, Tree& tree) {
+  const int lane = threadIdx.x & 31;
+  if (!a.parents) {  // a chain
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      tree.anc[lane + 32 * e] = ~0ull >> (63 - lane - 32 * e);
+      tree.depth[lane + 32 * e] = static_cast<uint8_t>(lane + 32 * e);
+    }
+    __syncwarp();
+  } else {
+    find_ancestors(a, b, sp, tree);
+  }
   if (a.window > 0 && a.window < sp.n) {  // ancestors may be out of the window
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int d = tree.depth[lane + 32 * e];
       unsigned long long keep = 0;
-      for (unsigned long long m = own[e]; m != 0; m &= m - 1) {
+      for (unsigned long long m = tree.anc[lane + 32 * e]; m != 0; m &= m - 1) {
         const int u = __ffsll(static_cast<long long>(m)) - 1, du = tree.depth[u];
         if (d - du < a.window || sp.len + du < a.sinks) keep |= 1ull << u;
       }
@@ -316,7 +330,7 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
 // from k and v.
 template <typename T16, int U>
 __device__ __forceinline__ void bring(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, Unit<U> unit,
-                                      const Ring<U>& ring, int slot) {
+                                      const int (&page)[U], const Ring<U>& ring, int slot) {
   const int lane = threadIdx.x & 31, len = x.sp.len, end = len + x.sp.n;
   bool whole = true;
   int boxes = 0, tma[U];
@@ -357,24 +371,25 @@ __device__ __forceinline__ void bring(const CUtensorMap* map, const DraftArgs<T1
       mbar_arrive(bar);
 #pragma unroll
     for (int u = 0; u < U; ++u)
-      if (tma[u] >= 0) {
-        tma_load_2d(base + u * kTileBytes, map, bar, 0, tma[u]);
-        tma_load_2d(base + u * kTileBytes + kBoxBytes, map, bar, 0, tma[u] + a.n_kv * a.page_size);
-      }
+      if (tma[u] >= 0)  // K and V
+        tma_load_4d(base + u * kTileBytes, map, bar, 0, tma[u] - page[u] * a.page_rows - a.row0, 0,
+                    page[u] * a.n_layer + a.layer);
   }
   __syncwarp();
 }
 
-// First positions and rows of tiles j0, j0 + step, ... of an item, 32 at a time: those
+// First positions, rows and pages of tiles j0, j0 + step, ... of an item, 32 at a time: those
 // of tile i + lane of them.
 template <typename T16>
 __device__ __forceinline__ void find_tiles(const DraftArgs<T16>& a, const Item<T16>& x, int j0, int step, int i, int cnt,
-                                           int& row, int& pos) {
+                                           int& row, int& pos, int& page) {
   const int n = i + static_cast<int>(threadIdx.x & 31), t = j0 + n * step;
   row = -1;
+  page = 0;
   pos = (t < x.sp.ts ? t : x.sp.tw + (t - x.sp.ts)) * kTile;
   if (n >= cnt) return;
-  const int c = pos / a.page_size, page = x.pages[c];
+  const int c = pos / a.page_size;
+  page = x.pages[c];
   if (page >= 0 && page < a.n_pages)
     row = page * a.page_rows + a.row0 + x.kvh * a.page_size + (pos - c * a.page_size);
   else
@@ -385,9 +400,9 @@ __device__ __forceinline__ void find_tiles(const DraftArgs<T16>& a, const Item<T
 template <typename T16, int U, int SLOTS>
 __device__ __forceinline__ bool bring_all(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, int j0,
                                           int cnt, const Ring<U>& ring, Turn<SLOTS>& turn, bool& around) {
-  int row = -1, pos = 0;
+  int row = -1, pos = 0, page = 0;
   for (int i = 0; i < cnt; i += U) {
-    if ((i & 31) == 0) find_tiles(a, x, j0, 1, i, cnt, row, pos);
+    if ((i & 31) == 0) find_tiles(a, x, j0, 1, i, cnt, row, pos, page);
     if (around) {
       const bool free = mbar_wait(smem_u32(&ring.empty[turn.slot]), turn.parity ^ 1);
       if (!__all_sync(0xffffffffu, free)) {
@@ -396,12 +411,14 @@ __device__ __forceinline__ bool bring_all(const CUtensorMap* map, const DraftArg
       }
     }
     Unit<U> unit;
+    int of[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      of[u] = __shfl_sync(0xffffffffu, page, (i + u) & 31);
       unit.row[u] = __shfl_sync(0xffffffffu, row, (i + u) & 31);
       unit.pos[u] = __shfl_sync(0xffffffffu, pos, (i + u) & 31);
     }
-    bring<T16, U>(map, a, x, unit, ring, turn.slot);
+    bring<T16, U>(map, a, x, unit, of, ring, turn.slot);
     turn.step(1);
     if (turn.slot == 0) around = true;
   }
@@ -591,15 +608,16 @@ __device__ __forceinline__ bool attend(const CUtensorMap* map, const DraftArgs<T
   acc.l[0] = acc.l[1] = 0.f;
   const int units = (cnt + U - 1) / U, mine = units > at ? (units - at + S::kGroups - 1) / S::kGroups : 0;
   // a warp with a ring of its own: tiles j0 + at, j0 + at + kGroups, ...
-  int row = -1, pos = 0, fetched = 0;
+  int row = -1, pos = 0, page = 0, fetched = 0;
   auto next = [&](int slot) {
     if constexpr (!S::kBringer) {
-      if ((fetched & 31) == 0) find_tiles(a, x, j0 + at, S::kGroups, fetched, mine, row, pos);
+      if ((fetched & 31) == 0) find_tiles(a, x, j0 + at, S::kGroups, fetched, mine, row, pos, page);
       Unit<U> unit;
       unit.row[0] = __shfl_sync(0xffffffffu, row, fetched & 31);
       unit.pos[0] = __shfl_sync(0xffffffffu, pos, fetched & 31);
+      const int of[1] = {__shfl_sync(0xffffffffu, page, fetched & 31)};
       ++fetched;
-      bring<T16, U>(map, a, x, unit, ring, slot);
+      bring<T16, U>(map, a, x, unit, of, ring, slot);
     }
   };
   if constexpr (!S::kBringer) {
@@ -1051,10 +1069,14 @@ cudaError_t launch_t(const gpt2_paged_cache* c, int layer, const void* q, int64_
   a.part_ml = reinterpret_cast<float2*>(base);
   base += align256(slots * sizeof(float2));
   a.part_o = reinterpret_cast<float*>(base);
-  // the pool as one [rows, 64] matrix
+  a.n_layer = c->n_layer;
+  a.layer = layer;
+  // the pool: dimensions, rows of all heads, K or V, layers of pages; a box is a tile's K and V
+  const uint64_t rows_kv = static_cast<uint64_t>(c->n_kv_head) * c->page_size, row_bytes = kHd * 2;
   CUtensorMap map;
-  if (!encode_tma_2d(&map, Type16<T16>::kTma, c->pages, kHd, static_cast<uint64_t>(c->n_pages) * a.page_rows, kHd * 2,
-                     kHd, kTile))
+  if (!encode_tma_4d(&map, Type16<T16>::kTma, c->pages,
+                     {kHd, rows_kv, 2, static_cast<uint64_t>(c->n_pages) * c->n_layer},
+                     {row_bytes, rows_kv * row_bytes, 2 * rows_kv * row_bytes}, {kHd, kTile, 2, 1}))
     return cudaErrorInvalidValue;
   switch (rows) {
     case 8: return launch_kind<T16, 1, true>(map, a, s);
