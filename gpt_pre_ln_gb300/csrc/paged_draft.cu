@@ -25,8 +25,10 @@
 // 81).  Up to 16 rows the fifth warp cost more than it gave (12 rows, 32 sequences
 // up to 2048: 29 us without, 39 with it).
 //
-// What bounds it is the instructions around the products (exponentials, the split
-// of p, running maxima), not memory: 2.3 TB/s at 64 rows, 5.0 at 5.
+// What bounds it with many rows is how fast one warp gets through the instructions
+// around the products (exponentials, the split of p, running maxima: 400 for 16 rows
+// and 32 positions at 4 cycles each), not memory and not the products: 2.3 TB/s and
+// 39% of the tensor pipes at 64 rows; with 7 rows it is memory (5.0 TB/s).
 #include <algorithm>
 
 #include "internal.h"
@@ -78,13 +80,14 @@ struct DraftArgs {
   const int32_t* refs;
   const int32_t* parents;  // null: a chain
   const int32_t* counts;   // null: T each
-  int* plan;        // base[n_seq + 1], then tiles per CTA
+  int* plan;        // base[n_seq + 1], then tiles per CTA (below 0: items are rounded up to whole runs)
   float* part_o;    // [2 * CTAs, rows, 64]
   float2* part_ml;  // [2 * CTAs, rows]: running maximum (log2 units) and sum
   unsigned* err;
   long long ldq, ldkv, ldo;
   int n_pages, page_size, max_pages, n_seq, n_kv, H, group, T;
   int window, sinks;
+  int items;  // at most
   float scale_log2;  // score scale times log2(e)
 };
 
@@ -772,8 +775,13 @@ __device__ __forceinline__ Item<T16> item_of(const DraftArgs<T16>& a, int b, int
   return x;
 }
 
+__device__ __forceinline__ int rounded(int n, int to) { return to == 1 ? n : (n + to - 1) / to * to; }
+
 // Work is cut into equal runs of tiles over all (sequence, key-value head, row
-// block) items laid end to end, one run per CTA, whatever the lengths are.  A CTA
+// block) items laid end to end, one run per CTA, whatever the lengths are.  Where
+// there are CTAs enough items are rounded up to whole runs, so that none takes pieces
+// of two, one after the other (8 tokens of one sequence of 777, 12 heads: 9.6 us,
+// 12.1 without it).  A CTA
 // that holds all tiles of an item writes its output, pieces of an item go to the
 // workspace and a second kernel joins them.  Groups of warps that took tiles of a
 // piece in turn meet in shared memory.
@@ -785,7 +793,7 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
   extern __shared__ uint8_t s_raw[];
   __shared__ __align__(8) uint64_t s_bar[2][S::kRings * kSlots];
   __shared__ __align__(16) Unit<U> s_unit[S::kRings * kSlots];
-  __shared__ int s_sum[kWarps];
+  __shared__ int s_sum[kWarps], s_whole;
   __shared__ float2 s_ml[kGroups * kRows];
   __shared__ Tree s_tree[kWarps];
   uint8_t* s_tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(s_raw) + 1023) & ~uintptr_t(1023));
@@ -804,38 +812,45 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
     tma_prefetch_desc(&map);
   }
   griddep_wait();
-  // base[b] = tiles of all items of sequences before b
-  int carry = 0;
-  for (int b0 = 0; b0 < a.n_seq; b0 += kTakers) {
-    const int b = b0 + tid;
-    int v = 0;
-    if (tid < kTakers && b < a.n_seq) {
-      const Span sp = span_of<kRows>(a, b, blockIdx.x == 0);
-      v = max(sp.nt, 0) * a.n_kv * sp.blocks;
-    }
-    int incl = v;
+  // base[b] = tiles of all items of sequences before b, those of an item rounded up to `whole`
+  auto count = [&](int whole, bool record) {
+    int carry = 0;
+    for (int b0 = 0; b0 < a.n_seq; b0 += kTakers) {
+      const int b = b0 + tid;
+      int v = 0;
+      if (tid < kTakers && b < a.n_seq) {
+        const Span sp = span_of<kRows>(a, b, record);
+        v = rounded(max(sp.nt, 0), whole) * a.n_kv * sp.blocks;
+      }
+      int incl = v;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
+      }
+      if (lane == 31 && warp < kWarps) s_sum[warp] = incl;
+      __syncthreads();
+      int before = carry;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_sum[w];
+        carry += s_sum[w];
+      }
+      if (tid < kTakers && b < a.n_seq) s_base[b] = before + incl - v;
+      __syncthreads();
     }
-    if (lane == 31 && warp < kWarps) s_sum[warp] = incl;
+    if (tid == 0) s_base[a.n_seq] = carry;
     __syncthreads();
-    int before = carry;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_sum[w];
-      carry += s_sum[w];
-    }
-    if (tid < kTakers && b < a.n_seq) s_base[b] = before + incl - v;
-    __syncthreads();
-  }
-  if (tid == 0) s_base[a.n_seq] = carry;
+    return carry;
+  };
+  int total = count(1, blockIdx.x == 0);
+  const int grid = static_cast<int>(gridDim.x), run = max((total + grid - 1) / grid, kMinRun);
+  const bool few = total <= (grid - min(a.items, grid)) * kMinRun;
+  if (tid == 0) s_whole = few ? kMinRun : 1;
+  if (few) total = count(kMinRun, false);
   __syncthreads();
-  const int total = carry;
-  const int run = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinRun);
   if (blockIdx.x == 0) {
     for (int b = tid; b <= a.n_seq; b += S::kThreads) a.plan[b] = s_base[b];
-    if (tid == 0) a.plan[a.n_seq + 1] = run;
+    if (tid == 0) a.plan[a.n_seq + 1] = few ? -run : run;
   }
   const long long t_first = static_cast<long long>(blockIdx.x) * run;
   if (t_first >= total) return;
@@ -851,8 +866,9 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
         hi = mid;
     }
     const Span sp = span_of<kRows>(a, lo, false);
-    const int item = (t - s_base[lo]) / sp.nt;
-    j0 = (t - s_base[lo]) - item * sp.nt;
+    const int nt = rounded(sp.nt, s_whole);
+    const int item = (t - s_base[lo]) / nt;
+    j0 = (t - s_base[lo]) - item * nt;
     cnt = min(sp.nt - j0, t_end - t);
     return item_of(a, lo, item, sp, kRows);
   };
@@ -864,7 +880,7 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
         int j0, cnt;
         const Item<T16> x = piece_at(t, j0, cnt);
         if (!bring_all<T16, U, kSlots>(&map, a, x, j0, cnt, ring, turn, around)) break;
-        t += cnt;
+        t = s_whole > 1 ? t_end : t + cnt;
       }
       // copies must not outlive the CTA: each slot's last use, from the oldest on
       for (int s = around ? 0 : kSlots - turn.slot; s < kSlots; ++s) {
@@ -883,7 +899,7 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
     const long long part = 2ll * blockIdx.x + (t == static_cast<int>(t_first) ? 0 : 1);
     Acc acc;
     const bool ok = attend<T16, WR, RIDE>(&map, a, x, i0, rank == 0, at, j0, cnt, ring, turn, s_tree[warp], acc);
-    t += cnt;
+    t = s_whole > 1 ? t_end : t + cnt;
     __syncwarp();
     if constexpr (kGroups == 1) {
       if (!ok) return;
@@ -940,8 +956,8 @@ __global__ void __launch_bounds__(kJoinThreads) draft_join(const DraftArgs<T16> 
   const Item<T16> x = item_of(a, b, item, sp, ROWS);
   const int first_row = blockIdx.y * width;
   if (first_row >= x.rows) return;
-  const int run = a.plan[a.n_seq + 1];
-  const int start = a.plan[b] + item * sp.nt;
+  const int run_few = a.plan[a.n_seq + 1], run = abs(run_few);
+  const int start = a.plan[b] + item * (run_few < 0 ? rounded(sp.nt, run) : sp.nt);
   const int w0 = start / run, w1 = (start + sp.nt - 1) / run;
   if (w0 == w1) return;  // that CTA wrote the output
   const bool second = start != w0 * run;  // the item began within the first CTA's run: its second piece
@@ -996,7 +1012,7 @@ int rows_of(int T, int group) {
 int ctas_of(int rows) { return rows <= 16 ? Shape<1, false>::kCtas : Shape<2, false>::kCtas; }
 
 template <typename T16, int WR, bool RIDE>
-cudaError_t launch_kind(const CUtensorMap& map, const DraftArgs<T16>& a, cudaStream_t s) {
+cudaError_t launch_kind(const CUtensorMap& map, DraftArgs<T16> a, cudaStream_t s) {
   using S = Shape<WR, RIDE>;
   constexpr int kFixed = S::kRings * S::kRingBytes + S::kMeetBytes + 1024;
   static int configured[64] = {0};
@@ -1013,12 +1029,12 @@ cudaError_t launch_kind(const CUtensorMap& map, const DraftArgs<T16>& a, cudaStr
     if (e != cudaSuccess) return e;
     configured[dev] = 1;
   }
-  const int sms = num_sms();
+  const int sms = num_sms(), max_blocks = (a.T * a.group + S::kRows - 1) / S::kRows;
+  const long long items = static_cast<long long>(a.n_seq) * a.n_kv * max_blocks;
+  a.items = static_cast<int>(std::min(items, 1ll << 30));
   cudaError_t e = launch_pdl(draft_attn<T16, WR, RIDE>, sms * S::kCtas, S::kThreads, kFixed + (a.n_seq + 1) * 4, s, 0,
                              map, a);
   if (e != cudaSuccess) return e;
-  const int max_blocks = (a.T * a.group + S::kRows - 1) / S::kRows;
-  const long long items = static_cast<long long>(a.n_seq) * a.n_kv * max_blocks;
   const int most = std::min(S::kRows, a.T * a.group);
   int width = 1;  // as many CTAs as there are places for
   while (width < 16 && items * ((most + width - 1) / width) > 4 * sms) width *= 2;
