@@ -7,8 +7,9 @@
 // stands for position len + j: in every layer its K and V go from place
 // len + path[j] to place len + j.  path[j] >= j, and places are left in
 // ascending order, so each 16-byte column of the rows may be moved in place by
-// one thread.  Bound by latency (a dependent chain of lengths, tree, page table
-// and rows), and by HBM for many sequences.
+// one thread.  Bound by latency for few sequences (a dependent chain of lengths,
+// tree, page table and rows: 5.5 us for one), and by HBM for many, which 128-byte
+// rows from all over a large pool reach less of (3.6 TB/s).
 #include <algorithm>
 
 #include "common.cuh"
@@ -19,8 +20,8 @@ namespace gpt2 {
 namespace {
 
 constexpr int kCtas = 8;  // per sequence, one cluster: its length is written when all of them have read it
-constexpr int kThreads = 512;
-constexpr int kBatch = 8;  // rows of a column on their way at a time
+constexpr int kThreads = 256;  // 64 sequences at 24 layers of 16 heads: 20.5 us; 128: 21.0, 512: 22.6, 1024: 30.6
+constexpr int kBatch = 8;      // rows of a column on their way at a time (there: 4 the same, 16 25.6 us)
 
 __global__ void __launch_bounds__(kThreads)
     draft_accept(uint4* __restrict__ pages, long long page_vecs, const int32_t* __restrict__ table, int32_t* lens,
