@@ -12,8 +12,8 @@
 // An id is right or wrong: a sum of fp32 weights is off by 5e-7 of itself, which
 // is more than many a token's share.  So where a decision lies within that bound,
 // the row is done once more with weights and sums of two floats each (2^-36 of the
-// row's weight at worst, 2^-42 as a rule): 1 to 4 rows of 100, at three times the
-// time.
+// row's weight at worst, 2^-42 as a rule): 1 to 5 rows of 100, at two to four times
+// the time (50257 logits: 110000 cycles more).
 //
 // One CTA per row, which it reads once into shared memory (rows that do not fit
 // are read from global memory, where they stay in L2) and goes over there: for
@@ -21,6 +21,12 @@
 // the border; for the weights' sums; and over the part that the random number
 // falls into.  Where the kept tokens are few (top-k, or top-p of a sharp row) they
 // are listed instead, and the rest is done on the list, in two floats at once.
+//
+// Bound by instructions and by steps that follow one another on one SM, not by
+// memory: a row of 50257 takes 20 us (its maximum 3, the histogram 7, the border 4 to
+// 15, the draw 4), one that is done twice 75.  64 such rows in fp32 with top-p 74 us,
+// 256 with top-k up to 400 35, 1024 in bf16 with mixed settings 140 (715 GB/s), 512
+// rows of 8000 18.
 #include <algorithm>
 #include <type_traits>
 
@@ -882,7 +888,8 @@ __device__ __forceinline__ float logprob_of(const Scale& s, float z, Two all) {
   float d, d_lo;
   two_sum(0.5f * z, -s.half_max, d, d_lo);
   const float t = d * s.c_hi, t_lo = fmaf(d, s.c_hi, -t) + fmaf(d, s.c_lo, d_lo * s.c_hi);
-  return 0.693147180559945f * (t + (t_lo - log2f(all.hi)));
+  // (the largest weights 1, so that neither part is above 0; of a share near 1 the sum's second float matters)
+  return 0.693147180559945f * (t + t_lo) - log1pf((all.hi - 1.f) + all.lo);
 }
 
 // Draws from the `kept` first of the ranked list, whose weight is `all`, `loose`

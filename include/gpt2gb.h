@@ -709,7 +709,8 @@ int gpt2_draft_step_paged(const gpt2_dims *dims, const gpt2_model_weights *w, co
  * the next step; pages stay reserved.
  * A sequence that lacks a page of its own for a position that it keeps, or whose
  * drafted tokens do not fit its table row, keeps its lens and its rows of path
- * and next_tokens; n_kept[b] is 0 and GPT2_ERR_RANGE is recorded.  Outputs must not overlap inputs.  0 <= T <= 64. */
+ * and next_tokens; n_kept[b] is 0 and GPT2_ERR_RANGE is recorded.  Outputs must
+ * not overlap inputs.  0 <= T <= 64. */
 int gpt2_draft_accept(const gpt2_paged_cache *cache, int T, const int32_t *tokens, const int32_t *parents,
                       const int32_t *n_draft, const int32_t *chosen, int32_t *path, int32_t *n_kept,
                       int32_t *next_tokens, gpt2_stream_t stream);
@@ -728,10 +729,10 @@ int gpt2_draft_accept(const gpt2_paged_cache *cache, int T, const int32_t *token
  * uniform[m] times the weight of all kept ones; logprob[m] (NULL or fp32 [M])
  * the logarithm of its share of that weight.  temperature, top_p, min_p: NULL
  * (1, 1 and 0 for every row) or fp32 [M] device, top_k: NULL (0) or int32 [M]
- * device, uniform: fp32 [M] device.  Temperatures other than 0 below 2^-100 count as 2^-100,
- * those above 2^100 as 2^100.
- *   The choice is that of exact arithmetic on the given numbers, up to about
- * 2^-40 of a row's weight, and does not depend on timing.  Log
+ * device, uniform: fp32 [M] device.  Temperatures other than 0 below 2^-100
+ * count as 2^-100, those above 2^100 as 2^100.
+ *   The choice is that of exact arithmetic on the given numbers, up to 2^-36 of
+ * a row's weight at worst, and does not depend on timing.  Log
  * probabilities are fp32, within 1e-5.
  *   A row with a NaN or +inf, or with nothing but -inf, gets token -1 and logprob
  * NaN.  So does, with GPT2_ERR_RANGE recorded, a row with a temperature that is

@@ -227,6 +227,19 @@ def test_long_caches_are_split_and_joined(T, heads, kv):
     Case([9001, 5, 2500], T, heads=heads, kv=kv, page=256, layers=1, layer=0, seed=T).run().check()
 
 
+@pytest.mark.parametrize("T, group", [(7, 1), (12, 1), (24, 1), (60, 1), (20, 3)])
+@pytest.mark.parametrize("window, sinks", [(0, 0), (500, 20)])
+def test_more_work_than_runs_of_eight_tiles(T, group, window, sinks):
+    # the CTAs' parts are longer than the shortest there are, and run over the items' ends
+    g = np.random.default_rng(T)
+    lens = [int(x) for x in g.integers(0, 1500, 28)]
+    lens[3], lens[11], lens[12] = -1, 0, 15
+    counts = [int(x) for x in g.integers(0, 7, 28)]
+    counts[5] = T
+    Case(lens, T, heads=7 * group, kv=7, page=64, counts=counts, window=window, sinks=sinks, layers=1, layer=0,
+         seed=T).run().check()
+
+
 def test_growing_scores_rescale():
     Case([300, 77], 40, grow=0.05, seed=3).run().check()
     Case([300, 77], 5, grow=0.05, seed=3, dtype="f16").run().check()

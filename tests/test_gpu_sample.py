@@ -319,3 +319,18 @@ def test_shares_of_many_draws():
     ids, w = kept(row[0, :V].double().cpu().numpy(), temperature=float(np.float32(0.8)))
     count = np.bincount(tok, minlength=V)
     assert np.abs(count - M * w / w.sum()).max() <= 1.5  # evenly spaced numbers: off by the two ends of a share
+
+
+def test_log_probabilities_of_shares_near_one():
+    # 20 tokens, 7 below the largest: the others' weight is 0.0009 to 0.02.  The sums of two floats are off by 2^-36,
+    # the logarithm, the exponent and its product by two steps of 2^-23 each.
+    V, M = 20, 8
+    g = np.random.default_rng(5)
+    z = torch.from_numpy((g.standard_normal((M, V)) * 0.3 - 7).astype(np.float32))
+    z[torch.arange(M), torch.arange(M)] = 0.0
+    z[:, 10:] -= torch.linspace(0, 3, M)[:, None]
+    tok, lp = run(z.cuda(), V, "f32", [0.5] * M)[:2]
+    for m in range(M):
+        t, ref = expect(z[m].double().numpy(), 0.5)
+        assert int(tok[m]) == t == m
+        assert abs(float(lp[m]) - ref) <= 2 ** -20 * abs(ref), (m, float(lp[m]), ref)
