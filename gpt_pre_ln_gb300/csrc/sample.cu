@@ -12,8 +12,8 @@
 // An id is right or wrong: a sum of fp32 weights is off by 5e-7 of itself, which
 // is more than many a token's share.  So where a decision lies within that bound,
 // the row is done once more with weights and sums of two floats each (2^-36 of the
-// row's weight at worst, 2^-42 as a rule): 1 to 5 rows of 100, at two to four times
-// the time (50257 logits: 110000 cycles more).
+// row's weight at worst, 2^-38 as a rule): 1 to 5 rows of 100, at two to four times
+// the time (50257 logits: 100000 cycles more).
 //
 // One CTA per row, which it reads once into shared memory (rows that do not fit
 // are read from global memory, where they stay in L2) and goes over there: for
@@ -24,9 +24,9 @@
 //
 // Bound by instructions and by steps that follow one another on one SM, not by
 // memory: a row of 50257 takes 20 us (its maximum 3, the histogram 7, the border 4 to
-// 15, the draw 4), one that is done twice 75.  64 such rows in fp32 with top-p 74 us,
-// 256 with top-k up to 400 35, 1024 in bf16 with mixed settings 140 (715 GB/s), 512
-// rows of 8000 18.
+// 15, the draw 4), one that is done twice 70.  64 such rows in fp32 with top-p 71 us,
+// 256 with top-k up to 400 35, 1024 in bf16 with mixed settings 140 (735 GB/s), 512
+// rows of 8000 17.
 #include <algorithm>
 #include <type_traits>
 
@@ -88,7 +88,7 @@ __device__ __forceinline__ Two warp_incl(Two a) {  // running sum over the lanes
   return a;
 }
 
-// 2^(k / 64), k = -32 .. 32, as hi + lo
+// 2^(k / 64), k = -32 .. 31 (and 32), as hi + lo
 __device__ const float2 kExp2[65] = {
     {0.7071067690849304f, 1.2101617485882343e-08f}, {0.7148066759109497f, -6.714964584375593e-09f}, {0.7225903868675232f, 1.662099968768871e-08f},
     {0.7304589152336121f, -1.814328776106322e-08f}, {0.7384130954742432f, -2.250449426810519e-08f}, {0.7464538812637329f, -1.7118100714696993e-08f},
@@ -152,14 +152,17 @@ __device__ __forceinline__ TwoPair two_sum2(float2 a, float2 b) {
   const float2 s = add_f32x2(a, b), t = sub2(s, a);
   return {s, add_f32x2(sub2(a, sub2(s, t)), sub2(b, t))};
 }
+// (sums of a few hundred weights: their second floats stay so far below the first ones that these are put in order
+// at the end, by total)
 __device__ __forceinline__ TwoPair add2(TwoPair a, TwoPair b) {
   const TwoPair s = two_sum2(a.hi, b.hi);
-  return norm2(s.hi, add_f32x2(s.lo, add_f32x2(a.lo, b.lo)));
+  return {s.hi, add_f32x2(s.lo, add_f32x2(a.lo, b.lo))};
 }
 __device__ __forceinline__ Two total(TwoPair a) { return add(norm(a.hi.x, a.lo.x), norm(a.hi.y, a.lo.y)); }
 
-// The weights of two logits to about 2^-45 of themselves: 2^t = 2^n 2^(k/64) e^x with
-// the integer n, the nearest k and |x| <= ln 2 / 128, whose series ends with x^5.
+// The weights of two logits to about 2^-38 of themselves: 2^t = 2^n 2^(k/64) e^x with
+// integers n and k, -32 <= k < 32, and |x| <= ln 2 / 128, whose series ends with x^4.
+// (The parts below x are single floats: 2^-16 of the weight, and they need no more.)
 // Below 2^-36 of the largest weight fp32 will do; below 2^-100 they count as 0.
 __device__ __forceinline__ TwoPair weights2(const Scale& s, const float2* table, float2 z) {
   const TwoPair d = two_sum2(mul_f32x2(z, splat(0.5f)), splat(-s.half_max));
@@ -168,36 +171,29 @@ __device__ __forceinline__ TwoPair weights2(const Scale& s, const float2* table,
     const float2 u = fma_f32x2(d.hi, splat(s.c_lo), t);
     return {make_float2(t.x > -100.f ? ex2_approx(u.x) : 0.f, t.y > -100.f ? ex2_approx(u.y) : 0.f), splat(0.f)};
   }
-  const float2 t_lo = add_f32x2(fma_f32x2(d.hi, splat(s.c_hi), make_float2(-t.x, -t.y)),
-                                fma_f32x2(d.hi, splat(s.c_lo), mul_f32x2(d.lo, splat(s.c_hi))));
+  const float2 t_lo =
+      fma_f32x2(d.lo, splat(s.c_hi), fma_f32x2(d.hi, splat(s.c_lo), fma_f32x2(d.hi, splat(s.c_hi), make_float2(-t.x, -t.y))));
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole numbers
-  const float2 nm = add_f32x2(t, splat(kRound)), n = add_f32x2(nm, splat(-kRound)), f = sub2(t, n);
-  const float2 km = fma_f32x2(f, splat(64.f), splat(kRound)), k = add_f32x2(km, splat(-kRound));
-  const float2 g = fma_f32x2(k, splat(-0.015625f), f);
+  const float2 im = fma_f32x2(t, splat(64.f), splat(kRound)), i = add_f32x2(im, splat(-kRound));
+  const float2 g = fma_f32x2(i, splat(-0.015625f), t);  // exact
   constexpr float kLn2Hi = 0.6931471824645996f, kLn2Lo = -1.9046542121259336e-09f;  // ln 2
   const float2 x = mul_f32x2(g, splat(kLn2Hi));
-  const float2 x_lo = add_f32x2(fma_f32x2(g, splat(kLn2Hi), make_float2(-x.x, -x.y)),
-                                fma_f32x2(g, splat(kLn2Lo), mul_f32x2(t_lo, splat(kLn2Hi))));
-  const float2 h = mul_f32x2(x, splat(0.5f)), q = mul_f32x2(h, x);
-  const float2 q_lo = add_f32x2(fma_f32x2(h, x, make_float2(-q.x, -q.y)), mul_f32x2(x, x_lo));
-  const float2 c = fma_f32x2(x, fma_f32x2(x, splat(1.f / 120.f), splat(1.f / 24.f)), splat(1.f / 6.f));
-  const float2 p = mul_f32x2(mul_f32x2(x, mul_f32x2(x, x)), c);
-  const TwoPair y = norm2(x, q);  // e^x - 1
-  const float2 y_lo = add_f32x2(y.lo, add_f32x2(x_lo, add_f32x2(q_lo, p)));
-  const float2 b0 = table[min(64, max(0, __float_as_int(km.x) - 0x4b400000 + 32))],
-               b1 = table[min(64, max(0, __float_as_int(km.y) - 0x4b400000 + 32))];
+  const float2 x_lo = fma_f32x2(t_lo, splat(kLn2Hi),
+                                fma_f32x2(g, splat(kLn2Lo), fma_f32x2(g, splat(kLn2Hi), make_float2(-x.x, -x.y))));
+  const float2 c = fma_f32x2(x, fma_f32x2(x, splat(1.f / 24.f), splat(1.f / 6.f)), splat(0.5f));
+  const float2 xx = mul_f32x2(x, x);
+  const float2 y = fma_f32x2(xx, c, fma_f32x2(fma_f32x2(xx, splat(0.5f), x), x_lo, x_lo));  // e^x - 1 = x + y
+  const int ix = __float_as_int(im.x) - 0x4b400000 + 32, iy = __float_as_int(im.y) - 0x4b400000 + 32;  // 64 n + k + 32
+  const float2 b0 = table[ix & 63], b1 = table[iy & 63];
   const float2 b = make_float2(b0.x, b1.x), b_lo = make_float2(b0.y, b1.y);
-  const float2 m = mul_f32x2(b, y.hi);
-  const float2 m_lo = add_f32x2(fma_f32x2(b, y.hi, make_float2(-m.x, -m.y)),
-                                fma_f32x2(b, y_lo, fma_f32x2(b_lo, y.hi, b_lo)));
+  const float2 m = mul_f32x2(b, x);
+  const float2 m_lo = add_f32x2(fma_f32x2(b_lo, x, fma_f32x2(b, y, fma_f32x2(b, x, make_float2(-m.x, -m.y)))), b_lo);
   const TwoPair w = norm2(b, m), r = norm2(w.hi, add_f32x2(w.lo, m_lo));
   // (a pair may be of one such element and one that is -inf or far below)
-  const float2 scale = make_float2(t.x > -100.f ? __int_as_float((__float_as_int(nm.x) - 0x4b400000 + 127) << 23) : 0.f,
-                                   t.y > -100.f ? __int_as_float((__float_as_int(nm.y) - 0x4b400000 + 127) << 23) : 0.f);
-  TwoPair out{mul_f32x2(r.hi, scale), mul_f32x2(r.lo, scale)};
-  if (!(t.x > -100.f)) out.hi.x = out.lo.x = 0.f;
-  if (!(t.y > -100.f)) out.hi.y = out.lo.y = 0.f;
-  return out;
+  const bool on_x = t.x > -100.f, on_y = t.y > -100.f;
+  const float2 scale = make_float2(__int_as_float(((ix >> 6) + 127) << 23), __int_as_float(((iy >> 6) + 127) << 23));
+  const TwoPair out{mul_f32x2(r.hi, scale), mul_f32x2(r.lo, scale)};
+  return {make_float2(on_x ? out.hi.x : 0.f, on_y ? out.hi.y : 0.f), make_float2(on_x ? out.lo.x : 0.f, on_y ? out.lo.y : 0.f)};
 }
 __device__ __forceinline__ Two weight2(const Scale& s, const float2* table, float z) {
   const TwoPair w = weights2(s, table, splat(z));
