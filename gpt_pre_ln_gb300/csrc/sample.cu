@@ -1001,9 +1001,8 @@ struct SubBins {
       : edge_first(bin_edge(first)), edge_last(bin_edge(last)), top((static_cast<float>(first) - 0.5f) * 0.015625f),
         per_t(64.f * static_cast<float>(kBins) / static_cast<float>(last - first + 1)),
         middle(static_cast<float>(first + last) * 0.0078125f) {}
-  __device__ __forceinline__ int of(float t) const {
-    return max(0, min(kBins - 1, static_cast<int>((-t - top) * per_t)));
-  }
+  __device__ __forceinline__ float place(float t) const { return (-t - top) * per_t; }
+  __device__ __forceinline__ int of(float t) const { return max(0, min(kBins - 1, static_cast<int>(place(t)))); }
 };
 
 // This warp's part of the row: the weight of the elements kept by `cut` ahead of
@@ -1098,6 +1097,7 @@ __device__ __noinline__ Two sum_both(Cut cut, int first, int last, int sub_first
   const SubBins sub(first, last);
   int from, to;
   part_of(threadIdx.x >> 5, from, to);
+  const float end_ahead = sub_first > 0 ? static_cast<float>(sub_first) : -INFINITY;
   TwoPair ahead{splat(0.f), splat(0.f)}, others = ahead;
 #pragma unroll 1
   for (int i = from * K::kN + 2 * (threadIdx.x & 31); i < to * K::kN; i += 64) {
@@ -1105,11 +1105,12 @@ __device__ __noinline__ Two sum_both(Cut cut, int first, int last, int sub_first
     if (!cut.keeps(z.x, i)) z.x = -INFINITY;
     if (!cut.keeps(z.y, i + 1)) z.y = -INFINITY;
     const TwoPair w = weights2(s, shared().table, z);
-    auto is_ahead = [&](float x) {
-      const float t = exponent(s, x), b = bin_at(t);
-      return b < sub.edge_first || (b <= sub.edge_last && sub.of(t) < sub_first);
+    const float2 t = exponent2(s, z);
+    auto is_ahead = [&](float t) {  // (of(t) < sub_first, without the conversion)
+      const float b = bin_at(t);
+      return (b < sub.edge_first) | ((b <= sub.edge_last) & (sub.place(t) < end_ahead));
     };
-    const bool x = is_ahead(z.x), y = is_ahead(z.y);
+    const bool x = is_ahead(t.x), y = is_ahead(t.y);
     ahead = add2(ahead, {make_float2(x ? w.hi.x : 0.f, y ? w.hi.y : 0.f), make_float2(x ? w.lo.x : 0.f, y ? w.lo.y : 0.f)});
     others = add2(others, {make_float2(x ? 0.f : w.hi.x, y ? 0.f : w.hi.y), make_float2(x ? 0.f : w.lo.x, y ? 0.f : w.lo.y)});
   }
