@@ -22,8 +22,8 @@
 // same tiles, 32 positions at a time, each with 16 rows of the block, and a fifth
 // warp brings them: the warp that also filled the ring held up all four (64 rows,
 // 16 sequences of 4096: 116 us, with the fifth warp 83; 48 rows, 8 of 32768: 109 and
-// 81).  Up to 16 rows the fifth warp cost more than it gave (12 rows, 32 sequences
-// up to 2048: 29 us without, 39 with it).
+// 81).  Up to 16 rows the fifth warp cost more than it gave (16 rows, 32 sequences
+// of up to 1087: 29 us without, 39 with it).
 //
 // What bounds it with many rows is how fast one warp gets through the instructions
 // around the products (exponentials, the split of p, running maxima: 400 for 16 rows

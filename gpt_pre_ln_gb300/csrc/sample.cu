@@ -24,8 +24,8 @@
 //
 // Bound by instructions and by steps that follow one another on one SM, not by
 // memory: a row of 50257 takes 20 us (its maximum 3, the histogram 7, the border 4 to
-// 15, the draw 4), one that is done twice 70.  64 such rows in fp32 with top-p 71 us,
-// 256 with top-k up to 400 35, 1024 in bf16 with mixed settings 140 (735 GB/s), 512
+// 15, the draw 4), one that is done twice 70.  64 such rows in fp32 with top-p 70 us,
+// 256 with top-k up to 400 35, 1024 in bf16 with mixed settings 139 (740 GB/s), 512
 // rows of 8000 17.
 #include <algorithm>
 #include <type_traits>
