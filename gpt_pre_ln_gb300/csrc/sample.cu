@@ -650,9 +650,13 @@ __device__ __forceinline__ Two listed_sum(int kept, Two ahead) {
 // (MASS false), or those before which less than `target` of weight stands (MASS).
 // For any row, at its own pace: histograms over ever smaller intervals of the
 // order, until few enough elements are left to rank; the first one of bins of equal
-// width in z, from the maximum to the least that is not -inf, later ones, where equal
-// or nearly equal logits crowd a bin, of bins of equal width in the place.  In *loose the weight of the elements that sums off by `err` leave
-// undecided (INFINITY: none decided).
+// width in z, later ones, where equal or nearly equal logits crowd a bin, of bins of
+// equal width in the place.  The first one's bins go from the maximum to the least
+// that is not -inf; with MASS no further than a weight of 2^-100, behind which no
+// border lies (what is there weighs 2^-79 in all).  A bin counts its weights in steps
+// of the heaviest that fits it, so it must not span more than a fraction of a factor
+// of two, however low the row's least logit (a mask's -1e9) is.  In *loose the weight
+// of the elements that sums off by `err` leave undecided (INFINITY: none decided).
 template <typename K, bool MASS, bool TWO>
 __device__ __noinline__ Cut select(Cut cut, int count, Two target, float err, float* loose) {
   constexpr int kPer = kBins / K::NT;
@@ -664,6 +668,7 @@ __device__ __noinline__ Cut select(Cut cut, int count, Two target, float err, fl
   from *= K::kN;
   to = min(to * K::kN, V);
   Place lo = cut.place(), hi = place_of(2.f * s.half_max, 0);  // the interval
+  if (MASS) lo = max(lo, static_cast<Place>(key_of(2.f * (s.half_max - 100.f / s.c_hi))) << 32);
   int n = V;         // elements that it holds, at most
   int before_n = 0;  // elements ahead of it
   auto weight = [&](float z, Two& sum) {
@@ -680,7 +685,7 @@ __device__ __noinline__ Cut select(Cut cut, int count, Two target, float err, fl
 #pragma unroll 1
   for (int i = from + lane; i < to; i += 32) {
     const float z = element<K>(i);
-    if (z > -INFINITY && cut.keeps(z, i)) {
+    if (z > -INFINITY && place_of(z, i) >= lo) {
       least = min(least, key_of(z));
       ++there;
     }
