@@ -468,7 +468,8 @@ __device__ __forceinline__ float bin_at(float t) { return __fmaf_rn(t, -64.f, kM
 // Counts a pair of weights, those above 2^-32, in units of their bins' steps
 // (2^(-b / 64) is `one` of them): integers, so that sums do not depend on the order
 // of the additions.  e^x with |x| <= ln 2 / 128 is taken as 1 + x: 1.5e-5 off at
-// most.
+// most.  Both steps round to whole numbers, and equal logits do so alike: a sum of
+// bins may be off by 1 / one of itself.
 __device__ __forceinline__ void count_weights(uint32_t* hist, float2 t, float one) {
   const float unit = 0.010830424696249145f * one;  // ln 2 / 64
   const float2 m = fma_f32x2(t, splat(-64.f), splat(kMagic)), b = add_f32x2(m, splat(-kMagic));
@@ -476,7 +477,8 @@ __device__ __forceinline__ void count_weights(uint32_t* hist, float2 t, float on
   if (t.x > -31.9f) atomicAdd(hist + (__float_as_int(m.x) - 0x4b000000), __float_as_uint(n.x) - 0x4b000000u);
   if (t.y > -31.9f) atomicAdd(hist + (__float_as_int(m.y) - 0x4b000000), __float_as_uint(n.y) - 0x4b000000u);
 }
-constexpr float kErrBin = 4e-5f;  // of a sum of bins: the above, the integers' step of 2^-15 at most half, fp32 sums
+// The error of a sum of bins, of itself: the above (a weight is 2^(-1 / 128) of its bin's at least) and fp32 sums.
+__device__ __forceinline__ float error_of_bins(float one) { return 2e-5f + 1.01f / one; }
 
 // Where the running sum over the bins, each h / one times 2^(-b / 64) (or 1, if
 // flat), comes within `margin` of `want`, and where it passes it by as much: bins
@@ -1148,7 +1150,7 @@ __device__ __noinline__ bool draw(Cut cut, float top_p, float u, int& token, flo
       err = 2.f * error_of(all.hi, V);  // of a border's two sides
       target = times(all, top_p);
       float count;
-      find_bins<K>(false, one, target.hi, kErrBin * all.hi + 0.5f * all.hi / one + err, first, last, count);
+      find_bins<K>(false, one, target.hi, error_of_bins(one) * all.hi + err, first, last, count);
       // (the border is far below the maximum, or among very different weights)
       int how = last >= kBins - 64 || last - first > 64 ? kCrowded : count * 1.02f <= kList / 2 ? kFew : kMany;
       if (how == kMany) {
