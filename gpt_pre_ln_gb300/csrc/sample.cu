@@ -896,21 +896,23 @@ __device__ __forceinline__ float logprob_of(const Scale& s, float z, Two all) {
 }
 
 // Draws from the `kept` first of the ranked list, whose weight is `all`, `loose`
-// of which may not belong.
+// of which may not belong.  The sums by id are those of a parallel scan, whose second
+// floats may differ by their roundings where nothing is added, or fall: so the row
+// belongs to the lowest kept id whose sum passes the target, and to no other.
 template <typename K>
 __device__ __forceinline__ bool draw_listed(int n, const Listed (&mine)[kListed<K>], int kept, Two all, float loose,
                                             float u, int& token, float& logprob) {
   Shared& sh = shared();
   const Two target = times(all, u);
   for (int i = threadIdx.x; i < kList; i += K::NT) sh.by_id[i] = {0.f, 0.f};
-  if (threadIdx.x == 0) sh.first = -1;
+  if (threadIdx.x == 0) {
+    sh.first = kList;
+    sh.last = -1;
+  }
   __syncthreads();
 #pragma unroll 1
   for (int e = 0; e < kListed<K>; ++e)
-    if (threadIdx.x + e * K::NT < n && mine[e].rank < kept) {
-      sh.by_id[mine[e].rank_id] = mine[e].w;
-      if (mine[e].w.hi > 0.f) atomicMax(&sh.first, mine[e].rank_id);
-    }
+    if (threadIdx.x + e * K::NT < n && mine[e].rank < kept) sh.by_id[mine[e].rank_id] = mine[e].w;
   __syncthreads();
   scan_list<K, true>();
 #pragma unroll 1
@@ -918,17 +920,24 @@ __device__ __forceinline__ bool draw_listed(int n, const Listed (&mine)[kListed<
     if (threadIdx.x + e * K::NT >= n) break;
     const Listed& x = mine[e];
     if (x.rank >= kept || !(x.w.hi > 0.f)) continue;
-    const Two end = sh.by_id[x.rank_id];
+    if (less(target, sh.by_id[x.rank_id])) atomicMin(&sh.first, x.rank_id);
+    atomicMax(&sh.last, x.rank_id);
+  }
+  __syncthreads();
+  // (rounding may leave the last one's end below the target)
+  const int owner = min(sh.first, sh.last);
+#pragma unroll 1
+  for (int e = 0; e < kListed<K>; ++e) {
+    if (threadIdx.x + e * K::NT >= n) break;
+    const Listed& x = mine[e];
+    if (x.rank_id != owner) continue;
     Two before{0.f, 0.f};
-    if (x.rank_id > 0) before = sh.by_id[x.rank_id - 1];
-    // (rounding may leave the last one's end below the target)
-    if (!less(target, before) && (less(target, end) || x.rank_id == sh.first)) {
-      sh.found = id_of(x.p);
-      // how far the random number is from the ends of this token's share (nothing is before the first)
-      sh.margin = minus(end, target);
-      if (before.hi > 0.f || loose > 0.f) sh.margin = fminf(sh.margin, minus(target, before));
-      sh.logprob = logprob_of(sh.scale, z_of(x.p), all);
-    }
+    if (owner > 0) before = sh.by_id[owner - 1];
+    sh.found = id_of(x.p);
+    // how far the random number is from the ends of this token's share (nothing is before the first)
+    sh.margin = minus(sh.by_id[owner], target);
+    if (before.hi > 0.f || loose > 0.f) sh.margin = fminf(sh.margin, minus(target, before));
+    sh.logprob = logprob_of(sh.scale, z_of(x.p), all);
   }
   __syncthreads();
   token = sh.found;

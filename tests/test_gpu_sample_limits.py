@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import gpt_pre_ln_gb300 as G  # noqa: E402
-from test_gpu_sample import expect, run  # noqa: E402
+from test_gpu_sample import expect, kept, run  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +60,45 @@ def test_a_border_behind_a_cluster(V, one, sign):
             want, ref = expect(x.astype(np.float64), float(u[m]), top_p=float(top_p[m]))
             assert tok[m] == ids[want], (float(zc), m, tok[m], ids[want], float(top_p[m]))
             assert abs(lp[m] - ref) <= 1e-5, (float(zc), m, lp[m], ref, float(top_p[m]))
+
+
+# ---- the very borders
+def _neighbours(z, V, u, left, **kw):
+    """Rows drawn with numbers next to the end of token left[m]'s share: the token is that one or the next one kept, and
+    the log probability its own."""
+    full = {k: np.full(len(u), v, np.int32 if k == "top_k" else np.float32) for k, v in kw.items()}
+    tok, lp = run(z, V, "f32", u, **full)
+    x = z[:, :V].double().cpu().numpy()
+    for m in range(len(u)):
+        ids, w = kept(x[m], **{k: np.float32(v).item() if k != "top_k" else v for k, v in kw.items()})
+        at = int(np.searchsorted(ids, left[m]))
+        assert tok[m] in ids[at:at + 2], (m, tok[m], ids[at:at + 2])
+        ref = math.log(w[np.searchsorted(ids, tok[m])] / w.sum())
+        assert abs(lp[m] - ref) <= 1e-5, (m, lp[m], ref)
+
+
+def test_each_row_belongs_to_one_token():
+    """Rows of 512 whose target falls between two sums that differ only by their roundings (found by trying 4e8)."""
+    V = 512
+    cases = [(261, 42, 0.8920871019363403, 435), (177, 5147, 0.26442840695381165, 113),
+             (187, 8942, 0.03250562772154808, 30), (703, 12524, 0.9267133474349976, 479),
+             (316, 15120, 0.9688754081726074, 470)]
+    rows = [2 * np.random.default_rng(s).standard_normal((m + 1, V), dtype=np.float32)[m] for s, m, _, _ in cases]
+    _neighbours(torch.from_numpy(np.stack(rows)).cuda(), V, np.float32([c[2] for c in cases]), [c[3] for c in cases],
+                top_k=256)
+
+
+@pytest.mark.parametrize("V, kw", [(512, dict(top_k=256)), (300, {}), (5000, dict(top_k=200)),
+                                   (30011, dict(top_p=0.9)), (30011, {}), (50257, dict(top_p=0.2))])
+def test_the_fp32_numbers_nearest_to_borders(V, kw):
+    """However near: either neighbour will do, but one of them it has to be."""
+    g = np.random.default_rng(V)
+    x = 1.5 * g.standard_normal(V, dtype=np.float32)
+    ids, w = kept(x.astype(np.float64), **{k: np.float32(v).item() if k != "top_k" else v for k, v in kw.items()})
+    part = np.cumsum(w) / w.sum()
+    dist = np.abs(part[:-1].astype(np.float32).astype(np.float64) - part[:-1])
+    at = np.argsort(dist)[:400]
+    u = part[at].astype(np.float32)
+    at, u = at[u < 1], u[u < 1]
+    z = torch.nn.functional.pad(torch.from_numpy(x), (0, -V % 4)).cuda().expand(len(u), -1).contiguous()
+    _neighbours(z, V, u, ids[at], **kw)
