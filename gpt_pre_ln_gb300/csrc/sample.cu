@@ -1416,10 +1416,11 @@ __global__ void __launch_bounds__(K::NT, K::NT >= 256 ? 1024 / K::NT : 7) sample
   const int top_k = a.top_k ? a.top_k[m] : 0;
   if (tid == K::NT - 1) {  // (one thread, while the row comes: 64-bit arithmetic is slow here)
     // 2 log2(e) / temperature
-    const double c = 2.8853900817779268 / fmin(fmax(static_cast<double>(temperature), 0x1p-100), 0x1p100);
+    const double counts = fmin(fmax(static_cast<double>(temperature), 0x1p-100), 0x1p100);
+    const double c = 2.8853900817779268 / counts;
     sh.scale.c_hi = __double2float_rd(c * (1.0 - 0x1p-25));  // (below c)
     sh.scale.c_lo = static_cast<float>(c - sh.scale.c_hi);
-    if (min_p > 0.f) sh.least = static_cast<double>(temperature) * log(static_cast<double>(min_p));
+    if (min_p > 0.f) sh.least = counts * log(static_cast<double>(min_p));
   }
   __syncwarp();
   // the row's maximum, and whether it has a NaN or +inf
@@ -1482,7 +1483,7 @@ __global__ void __launch_bounds__(K::NT, K::NT >= 256 ? 1024 / K::NT : 7) sample
       sh.scale.half_max = 0.5f * top;
       sh.cut_min = {-INFINITY, a.V - 1};
       if (min_p > 0.f) {
-        // the least z with z - max >= temperature log(min_p)
+        // the least z with z - max >= temperature log(min_p), for the temperature that counts
         const double least = sh.least;
         float z = static_cast<float>(top + least);
         if (!(z >= -3.402823466e38f)) z = -3.402823466e38f;

@@ -102,3 +102,21 @@ def test_the_fp32_numbers_nearest_to_borders(V, kw):
     at, u = at[u < 1], u[u < 1]
     z = torch.nn.functional.pad(torch.from_numpy(x), (0, -V % 4)).cuda().expand(len(u), -1).contiguous()
     _neighbours(z, V, u, ids[at], **kw)
+
+
+# ---- min_p and the ends of the temperatures
+def test_min_p_goes_by_the_temperature_that_counts():
+    """Temperatures below 2^-100 and above 2^100 count as these, for min_p too."""
+    hi, lo = 2.0 ** 100, 2.0 ** -100
+    z = np.zeros((6, 8), np.float32)
+    z[:, 1:] = -np.inf
+    z[0, 3] = z[1, 3] = z[2, 3] = -hi  # weights e^-1
+    z[3, 3] = z[4, 3] = z[5, 3] = -0.5 * lo  # e^-0.5
+    t = [2.0 ** 127, 2.0 ** 101, hi, 1e-38, 2.0 ** -101, lo]
+    u = [0.95] * 6
+    for min_p, stays in ((0.5, [0, 0, 0, 1, 1, 1]), (0.3, [1] * 6), (0.7, [0] * 6)):
+        tok, lp = run(torch.from_numpy(z).cuda(), 8, "f32", u, temperature=t, min_p=[min_p] * 6)
+        for m in range(6):
+            w = math.exp(-1.0 if m < 3 else -0.5)
+            assert tok[m] == (3 if stays[m] else 0), (min_p, m)
+            assert abs(lp[m] - (math.log(w / (1 + w)) if stays[m] else 0.0)) <= 1e-5
