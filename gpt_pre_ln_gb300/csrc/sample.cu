@@ -163,11 +163,12 @@ __device__ __forceinline__ Two total(TwoPair a) { return add(norm(a.hi.x, a.lo.x
 // The weights of two logits to about 2^-38 of themselves: 2^t = 2^n 2^(k/64) e^x with
 // integers n and k, -32 <= k < 32, and |x| <= ln 2 / 128, whose series ends with x^4.
 // (The parts below x are single floats: 2^-16 of the weight, and they need no more.)
-// Below 2^-36 of the largest weight fp32 will do; below 2^-100 they count as 0.
+// Below 2^-44 of the largest weight fp32 will do: t's roundings there are 2^-16 of the weight at most, alike for equal
+// logits, but 2^21 of them are 2^-23 of the largest.  Below 2^-100 they count as 0.
 __device__ __forceinline__ TwoPair weights2(const Scale& s, const float2* table, float2 z) {
   const TwoPair d = two_sum2(mul_f32x2(z, splat(0.5f)), splat(-s.half_max));
   const float2 t = mul_f32x2(d.hi, splat(s.c_hi));
-  if (!(fmaxf(t.x, t.y) > -36.f)) {
+  if (!(fmaxf(t.x, t.y) > -44.f)) {
     const float2 u = fma_f32x2(d.hi, splat(s.c_lo), t);
     return {make_float2(t.x > -100.f ? ex2_approx(u.x) : 0.f, t.y > -100.f ? ex2_approx(u.y) : 0.f), splat(0.f)};
   }

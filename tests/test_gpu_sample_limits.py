@@ -120,3 +120,21 @@ def test_min_p_goes_by_the_temperature_that_counts():
             w = math.exp(-1.0 if m < 3 else -0.5)
             assert tok[m] == (3 if stays[m] else 0), (min_p, m)
             assert abs(lp[m] - (math.log(w / (1 + w)) if stays[m] else 0.0)) <= 1e-5
+
+
+# ---- many equal tokens far below the maximum
+@pytest.mark.parametrize("z_tail", [-24.97173, -25.3, -26.7, -28.123, -31.0])
+def test_two_million_equal_tokens_far_below_the_maximum(z_tail):
+    """The random number falls into the share of 2^21 - 1 equal tokens; the largest weight has the last id.  Their prefix
+    sums are multiples of one weight, so that the id is a quotient; the documented bound is 2^-36 of the row's weight."""
+    V = 1 << 21
+    z = np.full(V, np.float32(z_tail), np.float32)
+    z[-1] = 0.0
+    w = math.exp(float(np.float32(z_tail)))
+    total = 1.0 + (V - 1) * w
+    us = np.float32([f * (V - 1) * w / total for f in (0.05, 0.2, 0.35, 0.5, 0.65, 0.8, 0.9, 0.97)])
+    tok, _ = run(torch.from_numpy(z).cuda().expand(len(us), -1).contiguous(), V, "f32", us)
+    for m, u in enumerate(us):
+        at = float(u) * total / w  # the id is its whole part
+        off = max(0.0, tok[m] - at, at - (tok[m] + 1)) * w / total
+        assert off <= 2.0 ** -36, (m, tok[m], at, math.log2(off))
