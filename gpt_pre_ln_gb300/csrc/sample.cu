@@ -160,6 +160,8 @@ __device__ __forceinline__ TwoPair add2(TwoPair a, TwoPair b) {
 }
 __device__ __forceinline__ Two total(TwoPair a) { return add(norm(a.hi.x, a.lo.x), norm(a.hi.y, a.lo.y)); }
 
+constexpr float kLn2Hi = 0.6931471824645996f, kLn2Lo = -1.9046542121259336e-09f;  // ln 2
+
 // The weights of two logits to about 2^-38 of themselves: 2^t = 2^n 2^(k/64) e^x with
 // integers n and k, -32 <= k < 32, and |x| <= ln 2 / 128, whose series ends with x^4.
 // (The parts below x are single floats: 2^-16 of the weight, and they need no more.)
@@ -177,7 +179,6 @@ __device__ __forceinline__ TwoPair weights2(const Scale& s, const float2* table,
   constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole numbers
   const float2 im = fma_f32x2(t, splat(64.f), splat(kRound)), i = add_f32x2(im, splat(-kRound));
   const float2 g = fma_f32x2(i, splat(-0.015625f), t);  // exact
-  constexpr float kLn2Hi = 0.6931471824645996f, kLn2Lo = -1.9046542121259336e-09f;  // ln 2
   const float2 x = mul_f32x2(g, splat(kLn2Hi));
   const float2 x_lo = fma_f32x2(t_lo, splat(kLn2Hi),
                                 fma_f32x2(g, splat(kLn2Lo), fma_f32x2(g, splat(kLn2Hi), make_float2(-x.x, -x.y))));
@@ -888,12 +889,20 @@ __device__ __forceinline__ int first_past(Two end, Two target, bool has) {
   return any ? 31 - __clz(static_cast<int>(any)) : 0;
 }
 
+// (t of 100 has steps of 2^-17: in two floats up to the last rounding)
 __device__ __forceinline__ float logprob_of(const Scale& s, float z, Two all) {
-  float d, d_lo;
+  float d, d_lo, r, r_lo;
   two_sum(0.5f * z, -s.half_max, d, d_lo);
   const float t = d * s.c_hi, t_lo = fmaf(d, s.c_hi, -t) + fmaf(d, s.c_lo, d_lo * s.c_hi);
-  // (the largest weights 1, so that neither part is above 0; of a share near 1 the sum's second float matters)
-  return 0.693147180559945f * (t + t_lo) - log1pf((all.hi - 1.f) + all.lo);
+  const float p = t * kLn2Hi, p_lo = fmaf(t, kLn2Hi, -p) + fmaf(t, kLn2Lo, t_lo * kLn2Hi);
+  // (the largest weighs 1, so that neither part is above 0; of a share near 1 the sum's second float matters)
+  two_sum(p, -log1pf((all.hi - 1.f) + all.lo), r, r_lo);
+  return r + (r_lo + p_lo);
+}
+// Whether a log probability stays within 1e-5 where `all` may be off by err: less what its own rounding (2^-24 of
+// it) and the logarithm of a sum of up to 2^21 (a step of 2^-20, and the rounding of its argument) take of that.
+__device__ __forceinline__ bool near_enough(float err, Two all, float logprob) {
+  return err <= (8.9e-6f + 6e-8f * logprob) * all.hi;
 }
 
 // Draws from the `kept` first of the ranked list, whose weight is `all`, `loose`
@@ -945,7 +954,7 @@ __device__ __forceinline__ bool draw_listed(int n, const Listed (&mine)[kListed<
   logprob = sh.logprob;
   const float margin = sh.margin;
   __syncthreads();
-  return loose == 0.f || (margin > 2.f * loose && loose <= 1e-5f * all.hi);
+  return loose == 0.f || (margin > 2.f * loose && near_enough(loose, all, logprob));
 }
 
 // The elements with z >= least that the cut keeps into the list; how many there
@@ -1341,7 +1350,8 @@ __device__ __noinline__ bool draw(Cut cut, float top_p, float u, int& token, flo
   logprob = sh.logprob;
   const float margin = sh.margin;
   __syncthreads();
-  return TWO || (margin > 2.f * (error_of(all.hi, V) + loose) && loose <= 1e-5f * all.hi);
+  const float off = error_of(all.hi, V) + loose;
+  return TWO || (margin > 2.f * off && near_enough(off, all, logprob));
 }
 
 // The least z that `count` of the threads' two largest logits reach, or a step

@@ -138,3 +138,43 @@ def test_two_million_equal_tokens_far_below_the_maximum(z_tail):
         at = float(u) * total / w  # the id is its whole part
         off = max(0.0, tok[m] - at, at - (tok[m] + 1)) * w / total
         assert off <= 2.0 ** -36, (m, tok[m], at, math.log2(off))
+
+
+# ---- log probabilities
+def test_log_probabilities_of_unlikely_tokens():
+    """u = 0 draws the lowest id, however small its share.  Half a step of the result, one of the logarithm of the sum
+    (below 4), and sums of two floats."""
+    M, V = 4096, 40
+    g = np.random.default_rng(8)
+    z = (0.5 * g.standard_normal((M, V))).astype(np.float32)
+    z[:, 0] = -g.uniform(20, 66, M).astype(np.float32)
+    tok, lp = run(torch.from_numpy(z).cuda(), V, "f32", np.zeros(M, np.float32))
+    for m in range(M):
+        want, ref = expect(z[m].astype(np.float64), 0.0)
+        assert tok[m] == want == 0
+        step = 2.0 ** (math.floor(math.log2(-ref)) - 23)
+        assert abs(lp[m] - ref) <= step / 2 + 2.0 ** -22 + 2.0 ** -30, (m, lp[m], ref)
+
+
+def test_log_probabilities_where_the_border_is_close():
+    """top_p's border is the nearest fp32 number to a token's, or a neighbour of that, and the token has 0.97e-5 to 1e-5
+    of the kept weight: fp32 sums may take it for the other side's."""
+    V, n, heavy, M = 65536, 50000, 10, 3000
+    g = np.random.default_rng(11)
+    for _ in range(8):
+        z = np.full(V, -np.inf, np.float32)
+        ids = g.permutation(V)
+        z[ids[:heavy]] = 0.0
+        z[ids[heavy:heavy + n]] = (math.log(heavy / n) - 0.05 + 0.1 * g.random(n)).astype(np.float32)
+        ranked = np.sort(z.astype(np.float64))[::-1][:n + heavy]
+        part = np.concatenate([[0.0], np.cumsum(np.exp(ranked))])
+        share = np.diff(part) / part[1:]
+        at = part[1:-1][(share[1:] > 0.97e-5) & (share[1:] < 1e-5)] / part[-1]
+        p = at.astype(np.float32)
+        p = np.concatenate([p, np.nextafter(p, np.float32(0)), np.nextafter(p, np.float32(2))])
+        p = p[g.permutation(len(p))[:M]]
+        u = g.random(len(p), dtype=np.float32)
+        tok, lp = run(torch.from_numpy(z).cuda().expand(len(p), -1).contiguous(), V, "f32", u, top_p=p)
+        count = np.searchsorted(part[:-1], p.astype(np.float64) * part[-1], side="left")
+        ref = z[tok].astype(np.float64) - np.log(part[count])
+        assert (np.abs(lp - ref) <= 1e-5).all(), np.abs(lp - ref).max()
