@@ -283,7 +283,8 @@ struct Shared {
   int count, first, last, found, bad;
   int how, bins[4];  // of draw: where top_p's border was found
   Cut cut, cut_min;
-  float loose, margin, logprob;
+  unsigned long long passed;  // of find_bins: the last bin + 1, and the count up to it
+  float margin, logprob;
   Scale scale;
   double least;
   const uint4* global;
@@ -512,8 +513,7 @@ __device__ __noinline__ void find_bins(bool flat, float one, float want, float m
   }
   if (tid == 0) {
     sh.first = kBins;
-    sh.last = -1;
-    sh.loose = 1e9f;
+    sh.passed = 0;
   }
   __syncthreads();
   float ahead = lane < warp ? sh.aux[lane] : 0.f, ahead_n = lane < warp ? sh.aux2[lane] : 0.f;
@@ -531,16 +531,16 @@ __device__ __noinline__ void find_bins(bool flat, float one, float want, float m
     n += h;
     run = fmaf(h, ex2_approx(static_cast<float>(b) * slope), run);
     if ((b == 0 || before < want - margin) && run >= want - margin) atomicMin(&sh.first, b);
-    if ((b == 0 || before < want + margin) && run >= want + margin) {
-      atomicMax(&sh.last, b);
-      sh.loose = n;
-    }
+    if ((b == 0 || before < want + margin) && run >= want + margin)
+      atomicMax(&sh.passed, (static_cast<unsigned long long>(b + 1) << 32) | __float_as_uint(n));
   }
   __syncthreads();
-  // (where one thread's sum ends a rounding below the next one's start a border may be found by neither)
+  // (where one thread's sum ends a rounding below the next one's start a border may be found by neither, where it
+  // ends above by both: then the later one's bin and count, whoever comes first)
+  const int bin = static_cast<int>(sh.passed >> 32) - 1;
   first = sh.first;
-  last = first < kBins && sh.last >= first ? sh.last : kBins - 1;
-  count = sh.loose;
+  last = first < kBins && bin >= first ? bin : kBins - 1;
+  count = bin >= 0 ? __uint_as_float(static_cast<uint32_t>(sh.passed)) : 1e9f;
   __syncthreads();
 }
 

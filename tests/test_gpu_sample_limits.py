@@ -178,3 +178,24 @@ def test_log_probabilities_where_the_border_is_close():
         count = np.searchsorted(part[:-1], p.astype(np.float64) * part[-1], side="left")
         ref = z[tok].astype(np.float64) - np.log(part[count])
         assert (np.abs(lp - ref) <= 1e-5).all(), np.abs(lp - ref).max()
+
+
+# ---- the same calls
+@pytest.mark.parametrize("V", [3000, 50257])
+def test_equal_calls_give_equal_bits(V):
+    """Rows with 150 to 400 tokens ahead of top_p's border, some listed and some summed by parts, and rows alike."""
+    M = 1500
+    g = np.random.default_rng(V)
+    x = (1.8 * g.exponential(size=(M // 3, V))).astype(np.float32)
+    x = np.concatenate([x, x, x])
+    w = np.sort(np.exp(x.astype(np.float64) - x.max(1, keepdims=True)), 1)[:, ::-1]
+    part = np.cumsum(w, 1) / w.sum(1, keepdims=True)
+    n = np.tile(g.integers(150, 400, M // 3), 3)
+    p = part[np.arange(M), n].astype(np.float32)
+    u = np.tile(g.random(M // 3, dtype=np.float32), 3)
+    z = torch.nn.functional.pad(torch.from_numpy(x), (0, -V % 4)).cuda()
+    first, lp = run(z, V, "f32", u, top_p=p)
+    assert (first.reshape(3, -1) == first[:M // 3]).all() and (lp.reshape(3, -1) == lp[:M // 3]).all()
+    for _ in range(5):
+        tok, again = run(z, V, "f32", u, top_p=p)
+        assert (tok == first).all() and (again == lp).all()
