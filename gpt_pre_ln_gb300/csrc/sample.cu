@@ -88,8 +88,8 @@ __device__ __forceinline__ Two warp_incl(Two a) {  // running sum over the lanes
   return a;
 }
 
-// 2^(k / 64), k = -32 .. 31 (and 32), as hi + lo
-__device__ const float2 kExp2[65] = {
+// 2^(k / 64), k = -32 .. 31, as hi + lo
+__device__ const float2 kExp2[64] = {
     {0.7071067690849304f, 1.2101617485882343e-08f}, {0.7148066759109497f, -6.714964584375593e-09f}, {0.7225903868675232f, 1.662099968768871e-08f},
     {0.7304589152336121f, -1.814328776106322e-08f}, {0.7384130954742432f, -2.250449426810519e-08f}, {0.7464538812637329f, -1.7118100714696993e-08f},
     {0.7545822262763977f, -1.2479686617439256e-08f}, {0.762799084186554f, -8.814284413460882e-09f}, {0.7711054086685181f, 4.035452416673024e-09f},
@@ -111,7 +111,7 @@ __device__ const float2 kExp2[65] = {
     {1.2690509557724f, 1.419333317542737e-09f}, {1.2828700542449951f, -3.816621685359678e-08f}, {1.2968395948410034f, -4.018999533172973e-08f},
     {1.3109612464904785f, -3.496571565619888e-08f}, {1.3252366781234741f, -3.496373324196611e-08f}, {1.339667558670044f, -3.4616739696957666e-08f},
     {1.3542555570602417f, -1.0123349269974824e-08f}, {1.3690024614334106f, -3.845881835218279e-08f}, {1.3839099407196045f, -5.875577357983275e-08f},
-    {1.398979663848877f, 8.689434061182055e-09f}, {1.4142135381698608f, 2.4203234971764687e-08f}
+    {1.398979663848877f, 8.689434061182055e-09f}
 };
 
 // The row's scale: t = (z - max) log2(e) / temperature = (z/2 - max/2) c (half
@@ -290,7 +290,7 @@ struct Shared {
   const uint4* global;
   int V, vecs, per_warp;  // of the row, in vectors; of one warp's part
   uint64_t bar[32];
-  float2 table[65];
+  float2 table[64];
 };
 constexpr size_t kFixed = (sizeof(Shared) + 15) / 16 * 16;
 __device__ __forceinline__ Shared& shared() {
@@ -1396,7 +1396,7 @@ __global__ void __launch_bounds__(K::NT, K::NT >= 256 ? 1024 / K::NT : 7) sample
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const long long m = blockIdx.x;
   const uint4* global = reinterpret_cast<const uint4*>(static_cast<const typename K::T*>(a.logits) + m * a.ld);
-  for (int i = tid; i < 65; i += K::NT) sh.table[i] = kExp2[i];
+  for (int i = tid; i < 64; i += K::NT) sh.table[i] = kExp2[i];
   if (tid == 0) {
     sh.bad = 0;
     sh.global = global;
