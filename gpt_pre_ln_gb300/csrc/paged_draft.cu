@@ -330,12 +330,12 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], uint32_t a0, uint3
 //
 // Tiles with places behind the cached positions are brought by the lanes
 // (16-byte asynchronous copies): cached places from their page, drafted ones
-// from k and v.
+// from k and v.  True if there were any.
 template <typename T16, int U>
-__device__ __forceinline__ void bring(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, Unit<U> unit,
+__device__ __forceinline__ bool bring(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, Unit<U> unit,
                                       const int (&page)[U], const Ring<U>& ring, int slot) {
   const int lane = threadIdx.x & 31, len = x.sp.len, end = len + x.sp.n;
-  bool whole = true;
+  bool whole = true, by_lanes = false;
   int boxes = 0, tma[U];
   const uint32_t bar = smem_u32(&ring.full[slot]), base = smem_u32(ring.buf + slot * U * kTileBytes);
 #pragma unroll
@@ -361,6 +361,7 @@ __device__ __forceinline__ void bring(const CUtensorMap* map, const DraftArgs<T1
       }
       asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
       tma[u] = -1;
+      by_lanes = true;
     }
     boxes += tma[u] >= 0 ? 1 : 0;
   }
@@ -379,6 +380,7 @@ __device__ __forceinline__ void bring(const CUtensorMap* map, const DraftArgs<T1
                     page[u] * a.n_layer + a.layer);
   }
   __syncwarp();
+  return by_lanes;
 }
 
 // First positions, rows and pages of tiles j0, j0 + step, ... of an item, 32 at a time: those
@@ -399,10 +401,12 @@ __device__ __forceinline__ void find_tiles(const DraftArgs<T16>& a, const Item<T
     record_error(a.err, kErrRange, kSitePagedPage);
 }
 
-// The warp that brings tiles j0 .. j0 + cnt - 1 of an item.  False if a wait ran out.
+// The warp that brings tiles j0 .. j0 + cnt - 1 of an item; by_lanes: a bit for each slot that lanes wrote last.
+// False if a wait ran out.
 template <typename T16, int U, int SLOTS>
 __device__ __forceinline__ bool bring_all(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, int j0,
-                                          int cnt, const Ring<U>& ring, Turn<SLOTS>& turn, bool& around) {
+                                          int cnt, const Ring<U>& ring, Turn<SLOTS>& turn, bool& around,
+                                          unsigned& by_lanes) {
   int row = -1, pos = 0, page = 0;
   for (int i = 0; i < cnt; i += U) {
     if ((i & 31) == 0) find_tiles(a, x, j0, 1, i, cnt, row, pos, page);
@@ -412,6 +416,8 @@ __device__ __forceinline__ bool bring_all(const CUtensorMap* map, const DraftArg
         if ((threadIdx.x & 31) == 0) record_error(a.err, kErrTimeout, kSitePagedLoad);
         return false;
       }
+      // what the lanes wrote there, before the asynchronous writes that may follow
+      if ((by_lanes >> turn.slot) & 1) fence_proxy_async_smem();
     }
     Unit<U> unit;
     int of[U];
@@ -421,7 +427,8 @@ __device__ __forceinline__ bool bring_all(const CUtensorMap* map, const DraftArg
       unit.row[u] = __shfl_sync(0xffffffffu, row, (i + u) & 31);
       unit.pos[u] = __shfl_sync(0xffffffffu, pos, (i + u) & 31);
     }
-    bring<T16, U>(map, a, x, unit, of, ring, turn.slot);
+    const unsigned bit = 1u << turn.slot;
+    by_lanes = bring<T16, U>(map, a, x, unit, of, ring, turn.slot) ? by_lanes | bit : by_lanes & ~bit;
     turn.step(1);
     if (turn.slot == 0) around = true;
   }
@@ -876,10 +883,11 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
   if constexpr (S::kBringer) {
     if (warp == kWarps) {
       bool around = false;
+      unsigned by_lanes = 0;
       for (int t = static_cast<int>(t_first); t < t_end;) {
         int j0, cnt;
         const Item<T16> x = piece_at(t, j0, cnt);
-        if (!bring_all<T16, U, kSlots>(&map, a, x, j0, cnt, ring, turn, around)) break;
+        if (!bring_all<T16, U, kSlots>(&map, a, x, j0, cnt, ring, turn, around, by_lanes)) break;
         t = s_whole > 1 ? t_end : t + cnt;
       }
       // copies must not outlive the CTA: each slot's last use, from the oldest on
