@@ -39,11 +39,18 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 template <typename T16>
 constexpr float kShift = std::is_same<T16, __half>::value ? 12.f : 0.f;
 
-// Adds a piece (its 4 values x, its m and l) to (acc, M, L).
+// Adds a piece (its 4 values x, its m and l) to (acc, M, L).  KEEP_INF: an infinity stays
+// one however little it counts: 2^-149 times at least, with which finite values add
+// 2^-21 at most.
+template <bool KEEP_INF = false>
 __device__ __forceinline__ void merge(float4& acc, float& M, float& L, const float4& x, const float2& ml) {
   if (ml.y == 0.f) return;  // nothing in it but scores of -inf
   const float mn = fmaxf(M, ml.x);
-  const float c0 = M == mn ? 1.f : ex2_approx(M - mn), c1 = ml.x == mn ? 1.f : ex2_approx(ml.x - mn);
+  float c0 = M == mn ? 1.f : ex2_approx(M - mn), c1 = ml.x == mn ? 1.f : ex2_approx(ml.x - mn);
+  if constexpr (KEEP_INF) {
+    c0 = __int_as_float(max(__float_as_int(c0), 1));
+    c1 = __int_as_float(max(__float_as_int(c1), 1));
+  }
   M = mn;
   L = L * c0 + ml.y * c1;
   acc.x = acc.x * c0 + x.x * c1;

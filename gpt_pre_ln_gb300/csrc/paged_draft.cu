@@ -125,6 +125,7 @@ __device__ __forceinline__ Span span_of(const DraftArgs<T16>& a, int b, bool rec
 struct Tree {
   unsigned long long anc[64];
   uint8_t depth[64];
+  int odd;  // values that are not finite have been left out of the products
 };
 
 // The paths up to the cached positions.
@@ -272,36 +273,6 @@ __device__ __forceinline__ uint32_t only_finite2(uint32_t w) {
   return w;
 }
 
-// p times a value that is not finite, of the first `places` places of the tile
-// whose values are at vb: what the products with zero in their place have left out.
-// (p below 0: not visible.)
-template <typename T16, bool RIDE>
-__device__ __forceinline__ void add_not_finite(Acc& acc, const float (&s)[2][4], const uint8_t* vb, int places) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
-#pragma unroll 1
-  for (int at = 0; at < places; ++at) {
-    const int from = (r << 2) | ((at & 7) >> 1);
-    float p[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const float lo = (at & 1) ? s[0][2 * g + 1] : s[0][2 * g], hi = (at & 1) ? s[1][2 * g + 1] : s[1][2 * g];
-      p[g] = __shfl_sync(0xffffffffu, at < 8 ? lo : hi, from);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(vb + at * 128 + ((i ^ (at & 7)) << 4) + 4 * j);
-      if (w == only_finite2<T16>(w)) continue;
-      const float2 v = Type16<T16>::unpack2(w);
-#pragma unroll
-      for (int g = 0; g < (RIDE ? 1 : 2); ++g) {
-        if (p[g] < 0.f) continue;
-        if (!isfinite(v.x)) acc.o[i][2 * g] += p[g] * v.x;
-        if (!isfinite(v.y)) acc.o[i][2 * g + 1] += p[g] * v.y;
-      }
-    }
-  }
-}
-
 // Four 8 x 8 tiles of 16-bit values, transposed; lane i gives the address of row
 // i & 7 of tile i >> 3.
 __device__ __forceinline__ void load_transposed(uint32_t addr, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
@@ -440,7 +411,8 @@ struct Query {
   uint32_t a[4][4];
 };
 
-// One unit of tiles by one warp; MASKED: not every row sees all of it.
+// One unit of tiles by one warp; MASKED: not every row sees all of it, and values that
+// are not finite are left out.
 //
 // The B fragments of q . k come out of shared memory as they are: sums over
 // dimensions are free in their order, so lane (r, j) reads of key rows r and r + 8
@@ -449,7 +421,7 @@ struct Query {
 // read twice in a phase.
 template <typename T16, bool RIDE, bool MASKED, int U>
 __device__ __forceinline__ void take(const DraftArgs<T16>& a, const Item<T16>& x, int i0, const Query& q,
-                                     const uint8_t* tiles, const Unit<U>& unit, const Tree& tree, Acc& acc) {
+                                     const uint8_t* tiles, const Unit<U>& unit, Tree& tree, Acc& acc) {
   constexpr int kHalves = RIDE ? 1 : 2;  // row groups of a lane that hold rows
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
   const int len = x.sp.len, end = len + x.sp.n;
@@ -466,7 +438,6 @@ __device__ __forceinline__ void take(const DraftArgs<T16>& a, const Item<T16>& x
       mma16816<T16>(s[u][e], q.a[2][0], q.a[2][1], q.a[2][2], q.a[2][3], k1.x, k1.y);
       mma16816<T16>(s[u][e], q.a[3][0], q.a[3][1], q.a[3][2], q.a[3][3], k1.z, k1.w);
     }
-  uint32_t hidden = 0;  // bit 8u + 4e + 2g + k: score s[u][e][2g + k] is not visible
   if constexpr (MASKED) {
 #pragma unroll
     for (int g = 0; g < kHalves; ++g) {
@@ -483,10 +454,7 @@ __device__ __forceinline__ void take(const DraftArgs<T16>& a, const Item<T16>& x
             const int p = unit.pos[u] + 8 * e + 2 * j + k;
             const bool seen = unit.row[u] >= 0 && (p < len ? (p >= first || p < a.sinks)
                                                            : p < end && ((anc >> (p - len)) & 1));
-            if (!seen) {
-              s[u][e][2 * g + k] = -INFINITY;
-              hidden |= 1u << (8 * u + 4 * e + 2 * g + k);
-            }
+            if (!seen) s[u][e][2 * g + k] = -INFINITY;
           }
     }
   }
@@ -532,8 +500,8 @@ __device__ __forceinline__ void take(const DraftArgs<T16>& a, const Item<T16>& x
     for (int k = 0; k < 8; k += 2)
       load_transposed(v_row + u * kTileBytes + (((k + (lane >> 4)) ^ (lane & 7)) << 4), vf[k][0], vf[k][1], vf[k + 1][0],
                       vf[k + 1][1]);
-    bool odd = false;  // a value that is not finite, in a tile that not every row sees all of
     if constexpr (MASKED) {
+      bool odd = false;
       // places that nothing wrote may hold anything
       const int left = unit.row[u] >= 0 ? end - unit.pos[u] - 2 * j : 0;
       const uint32_t m0 = left >= 2 ? 0xffffffffu : left == 1 ? 0xffffu : 0u;
@@ -547,7 +515,7 @@ __device__ __forceinline__ void take(const DraftArgs<T16>& a, const Item<T16>& x
         vf[k][0] = f0;
         vf[k][1] = f1;
       }
-      odd = __any_sync(0xffffffffu, odd);
+      if (odd) tree.odd = 1;
     }
     uint32_t ph[2][2], pl[2][2];  // [position half][row half]
 #pragma unroll
@@ -561,16 +529,6 @@ __device__ __forceinline__ void take(const DraftArgs<T16>& a, const Item<T16>& x
       } else {
         mma16816<T16>(acc.o[k], ph[0][0], ph[0][1], ph[1][0], ph[1][1], vf[k][0], vf[k][1]);
         mma16816<T16>(acc.o[k], pl[0][0], pl[0][1], pl[1][0], pl[1][1], vf[k][0], vf[k][1]);
-      }
-    }
-    if constexpr (MASKED) {
-      if (odd) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if ((hidden >> (8 * u + 4 * e + k)) & 1) s[u][e][k] = -1.f;
-        add_not_finite<T16, RIDE>(acc, s[u], tiles + u * kTileBytes + kBoxBytes, min(kTile, end - unit.pos[u]));
       }
     }
   }
@@ -600,13 +558,111 @@ __device__ __forceinline__ void store_drafts(const DraftArgs<T16>& a, const Item
   }
 }
 
+// What the values that are not finite make of the results of query rows i0 .. i0 + 15
+// of an item, over units at, at + step, ... (of U tiles) of tiles j0 .. j0 + cnt - 1.
+// p v is infinite wherever p is above 0, however small, and NaN with p = 0 (a score of
+// -inf) or beside the other infinity, wherever the value stands.  The products
+// would have it by the tile: with p in two parts 0 * inf or a negative remainder makes
+// NaN of inf, and where rows differ in what they see they cannot have it at all.
+//
+// Bit 4k + 2g + e of a lane (r, j), for dimension 8k + 2j + e of row r + 8g: +inf or NaN
+// in the low half, -inf or NaN in the high one.  From global memory, a tile's values at
+// once (1 us); a place that has such values is looked at for itself, and its score where
+// they decide something.  16 sequences of 4096, 64 tokens each: 84 us, 187 with one
+// infinity in one of them, 314 with one in each page, 1000 with nothing but NaN, 3100
+// with nothing but infinities.
+template <typename T16, int U>
+__device__ __noinline__ unsigned long long not_finite(const DraftArgs<T16>& a, const Item<T16>& x, int i0, int at,
+                                                      int step, int j0, int cnt, const Tree& tree) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
+  const int len = x.sp.len, end = len + x.sp.n;
+  unsigned up = 0, down = 0;
+#pragma unroll 1
+  for (int n = at * U; n < cnt; n += (n + 1) % U ? 1 : 1 + (step - 1) * U) {
+    const int tile = j0 + n, pos = (tile < x.sp.ts ? tile : x.sp.tw + (tile - x.sp.ts)) * kTile, c = pos / a.page_size;
+    const int page = x.pages[c];
+    if (page < 0 || page >= a.n_pages) continue;
+    const int places = min(kTile, end - pos);
+    // K and V of the tile's first place, in the cache and (drafted places) where they are brought from
+    const T16* ck =
+        a.pages + (static_cast<long long>(page) * a.page_rows + x.kvh * a.page_size + (pos - c * a.page_size)) * kHd;
+    const T16* cv = ck + static_cast<long long>(a.n_kv) * a.page_size * kHd;
+    const long long ld = a.k ? a.ldkv : kHd, first = (static_cast<long long>(x.b) * a.T + (pos - len)) * ld + x.kvh * kHd;
+    const T16 *dk = a.k ? a.k + first : ck, *dv = a.k ? a.v + first : cv;
+    uint32_t w[kTile];  // (no load waits for a branch or for another: one after another they take ten times as long)
+#pragma unroll
+    for (int y = 0; y < kTile; ++y) {
+      const int z = min(y, places - 1);
+      const T16* v = pos + z >= len ? dv + z * ld : cv + z * kHd;
+      w[y] = reinterpret_cast<const uint32_t*>(v)[lane];
+    }
+    unsigned odd = 0;  // bit y: place y has some
+#pragma unroll
+    for (int y = 0; y < kTile; ++y) odd |= w[y] != only_finite2<T16>(w[y]) ? 1u << y : 0u;
+    odd = __reduce_or_sync(0xffffffffu, odd) & ((1u << places) - 1);
+#pragma unroll 1
+    for (; odd != 0; odd &= odd - 1) {
+      const int y = __ffs(static_cast<int>(odd)) - 1, p = pos + y;
+      const T16 *k_row = p >= len ? dk + y * ld : ck + y * kHd, *v_row = p >= len ? dv + y * ld : cv + y * kHd;
+      unsigned plus = 0, minus = 0;  // bit 4k + e: the value of dimension 8k + 2j + e is +inf or NaN, -inf or NaN
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 v = Type16<T16>::unpack2(reinterpret_cast<const uint32_t*>(v_row)[4 * k + j]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float u = e ? v.y : v.x;
+          if (isfinite(u)) continue;
+          if (!(u < 0.f)) plus |= 1u << (4 * k + e);
+          if (!(u > 0.f)) minus |= 1u << (4 * k + e);
+        }
+      }
+      unsigned open = 0;
+#pragma unroll
+      for (int g = 0; g < 2; ++g)
+        if (i0 + 8 * g + r < x.rows) open |= (plus | minus) << (2 * g);
+      if (!__any_sync(0xffffffffu, (open & ~(up & down)) != 0)) continue;
+      const uint4 k0 = reinterpret_cast<const uint4*>(k_row + 16 * j)[0],
+                  k1 = reinterpret_cast<const uint4*>(k_row + 16 * j)[1];
+      const uint32_t kw[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const int i = i0 + 8 * g + r;
+        const uint4* from = reinterpret_cast<const uint4*>(q_row(a, x, min(i, x.rows - 1)) + 16 * j);
+        const uint4 q0 = from[0], q1 = from[1];
+        const uint32_t qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+        float s = 0.f;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          const float2 qv = Type16<T16>::unpack2(qw[d]), kv = Type16<T16>::unpack2(kw[d]);
+          s = fmaf(qv.x, kv.x, fmaf(qv.y, kv.y, s));
+        }
+        s += __shfl_xor_sync(0xffffffffu, s, 1);
+        s += __shfl_xor_sync(0xffffffffu, s, 2);
+        if (i < x.rows) {
+          const int t = (x.row0 + i) / a.group;
+          const bool seen = p >= len ? (tree.anc[t] >> (p - len)) & 1
+                                     : a.window <= 0 || p >= len + tree.depth[t] + 1 - a.window || p < a.sinks;
+          const bool none = s == -INFINITY;
+          if (seen) {
+            up |= (none ? plus | minus : plus) << (2 * g);
+            down |= (none ? plus | minus : minus) << (2 * g);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  return (static_cast<unsigned long long>(down) << 32) | up;
+}
+
 // Attention of query rows i0 .. i0 + 15 of an item over its tiles j0 .. j0 + cnt - 1 by
 // one warp: units at, at + kGroups, ... of them; `first`: of the warps with the same
-// units the one that stores drafted K and V.  False if a wait ran out.
+// units the one that stores drafted K and V; `odd`: there may be values that are not
+// finite among them.  False if a wait ran out.
 template <typename T16, int WR, bool RIDE>
 __device__ __forceinline__ bool attend(const CUtensorMap* map, const DraftArgs<T16>& a, const Item<T16>& x, int i0,
                                        bool first, int at, int j0, int cnt, const Ring<Shape<WR, RIDE>::kUnit>& ring,
-                                       Turn<Shape<WR, RIDE>::kSlots>& turn, Tree& tree, Acc& acc) {
+                                       Turn<Shape<WR, RIDE>::kSlots>& turn, Tree& tree, Acc& acc, bool& odd) {
   using S = Shape<WR, RIDE>;
   constexpr int U = S::kUnit, kSlots = S::kSlots;
   const int lane = threadIdx.x & 31, r = lane >> 2, j = lane & 3;
@@ -661,6 +717,8 @@ __device__ __forceinline__ bool attend(const CUtensorMap* map, const DraftArgs<T
   // way.
   const int last = j0 + cnt - 1;
   const bool drafts = ((last < x.sp.ts ? last : x.sp.tw + last - x.sp.ts) + 1) * kTile > x.sp.len;
+  if (lane == 0) tree.odd = 0;
+  __syncwarp();
   if ((drafts || a.window > 0) && !idle) build_tree(a, x.b, x.sp, tree);
   Turn<kSlots> now = turn;
   if constexpr (S::kBringer) now.step(at);
@@ -714,7 +772,25 @@ __device__ __forceinline__ bool attend(const CUtensorMap* map, const DraftArgs<T
       acc.o[i][1] += acc.o[i][3];
     }
   }
+  float any[4] = {0.f, 0.f, 0.f, 0.f};  // NaN if a result is not finite
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) any[e] = fmaf(acc.o[i][e], 0.f, any[e]);
+  odd = __any_sync(0xffffffffu, tree.odd != 0 || (any[0] + any[1]) + (any[2] + any[3]) != 0.f);
   return true;
+}
+
+// The results that not_finite's bits are of.
+__device__ __forceinline__ void put_not_finite(Acc& acc, unsigned long long bits) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool up = (bits >> (4 * i + e)) & 1, down = (bits >> (32 + 4 * i + e)) & 1;
+      if (up || down) acc.o[i][e] = up ? (down ? NAN : INFINITY) : -INFINITY;
+      if (acc.l[e >> 1] == 0.f) acc.o[i][e] = 0.f;  // nothing but scores of -inf: zeros, whatever the values are
+    }
 }
 
 // The rows of one warp's result: dst[row][64], ml[row] = (m, l).
@@ -794,7 +870,7 @@ __device__ __forceinline__ int rounded(int n, int to) { return to == 1 ? n : (n 
 // piece in turn meet in shared memory.
 template <typename T16, int WR, bool RIDE>
 __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>::kCtas))
-    draft_attn(const __grid_constant__ CUtensorMap map, const DraftArgs<T16> a) {
+    draft_attn(const __grid_constant__ CUtensorMap map, const __grid_constant__ DraftArgs<T16> a) {
   using S = Shape<WR, RIDE>;
   constexpr int kGroups = S::kGroups, kRows = S::kRows, kSlots = S::kSlots, U = S::kUnit;
   extern __shared__ uint8_t s_raw[];
@@ -906,7 +982,13 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
     const bool all = cnt == x.sp.nt;
     const long long part = 2ll * blockIdx.x + (t == static_cast<int>(t_first) ? 0 : 1);
     Acc acc;
-    const bool ok = attend<T16, WR, RIDE>(&map, a, x, i0, rank == 0, at, j0, cnt, ring, turn, s_tree[warp], acc);
+    bool odd = false;
+    const bool ok = attend<T16, WR, RIDE>(&map, a, x, i0, rank == 0, at, j0, cnt, ring, turn, s_tree[warp], acc, odd);
+    if (odd) {
+      int from, tiles;  // (found again, so that the way to here need not keep them)
+      const Item<T16> again = piece_at(t, from, tiles);
+      put_not_finite(acc, not_finite<T16, U>(a, again, i0, at, kGroups, from, tiles, s_tree[warp]));
+    }
     t = s_whole > 1 ? t_end : t + cnt;
     __syncwarp();
     if constexpr (kGroups == 1) {
@@ -929,7 +1011,7 @@ __global__ void __launch_bounds__((Shape<WR, RIDE>::kThreads), (Shape<WR, RIDE>:
         float M = -INFINITY, L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int w = 0; w < pieces; ++w)
-          merge(o, M, L, *reinterpret_cast<const float4*>(s_meet + w * kMeetStep + (i * kHd + 4 * d4) * 4),
+          merge<true>(o, M, L, *reinterpret_cast<const float4*>(s_meet + w * kMeetStep + (i * kHd + 4 * d4) * 4),
                 s_ml[w * kRows + i]);
         if (all) {
           put_row(a, x, i, d4, o, M, L);
@@ -990,7 +1072,7 @@ __global__ void __launch_bounds__(kJoinThreads) draft_join(const DraftArgs<T16> 
         }
       }
 #pragma unroll
-      for (int u = 0; u < kAhead; ++u) merge(acc, M, L, o[u], ml[u]);
+      for (int u = 0; u < kAhead; ++u) merge<true>(acc, M, L, o[u], ml[u]);
     }
   }
   // pairwise, in an order that the number of threads alone gives
@@ -999,7 +1081,7 @@ __global__ void __launch_bounds__(kJoinThreads) draft_join(const DraftArgs<T16> 
   for (int k = ways >> 1; k > 0; k >>= 1) {
     __syncthreads();
     if (way < k) {
-      merge(acc, M, L, s_o[tid + 16 * width * k], s_ml[tid + 16 * width * k]);
+      merge<true>(acc, M, L, s_o[tid + 16 * width * k], s_ml[tid + 16 * width * k]);
       s_o[tid] = acc;
       s_ml[tid] = make_float2(M, L);
     }

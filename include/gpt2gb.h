@@ -669,8 +669,10 @@ size_t gpt2_attention_paged_draft_workspace_bytes(const gpt2_paged_cache *cache,
  *   1024; n_pages * n_layer * 2 * n_kv_head * page_size < 2^31; n_seq *
  *   n_kv_head * T * (n_head / n_kv_head) / 8 * max_pages * page_size < 2^34.
  * Numerics as gpt2_attention_paged.  A value that is not finite at a place
- * that a token does not see changes nothing for it.  A token that sees nothing
- * but scores of -inf, or no place at all, gets zeros and an lse of -inf.  Places
+ * that a token does not see changes nothing for it; an infinity at one that it sees
+ * makes that dimension infinite, however small its share, and NaN beside one of the
+ * other sign, a NaN or a score of -inf at that place.  A token that sees nothing but
+ * scores of -inf, or no place at all, gets zeros and an lse of -inf.  Places
  * on a page that the table does not name are left out, and a sequence whose
  * drafted tokens do not fit its table row is skipped; both record
  * GPT2_ERR_RANGE.  Results do not depend on timing.  ws:
