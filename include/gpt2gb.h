@@ -667,7 +667,8 @@ size_t gpt2_attention_paged_draft_workspace_bytes(const gpt2_paged_cache *cache,
  *   overlap q, k or v.
  *   1 <= T <= 64 (0 is a no-op); n_head a multiple of n_kv_head and at most
  *   1024; n_pages * n_layer * 2 * n_kv_head * page_size < 2^31; n_seq *
- *   n_kv_head * T * (n_head / n_kv_head) / 8 * max_pages * page_size < 2^34.
+ *   n_kv_head * max_pages * page_size, times T * (n_head / n_kv_head) / 64 rounded
+ *   up, < 2^34 (GPT2_ERR_UNSUPPORTED otherwise).
  * Numerics as gpt2_attention_paged.  A value that is not finite at a place
  * that a token does not see changes nothing for it; an infinity at one that it sees
  * makes that dimension infinite, however small its share, and NaN beside one of the
