@@ -709,7 +709,9 @@ int gpt2_draft_step_paged(const gpt2_dims *dims, const gpt2_model_weights *w, co
  * next_tokens[b] the token chosen behind its end (int32 [n_seq] each); in
  * every layer the K and V of token path[b, j] are at position lens[b] + j; and
  * lens[b] grows by n_kept[b].  Positions behind the new length are free for
- * the next step; pages stay reserved.
+ * the next step; pages stay reserved.  A sequence without drafted tokens (n <= 0)
+ * or with lens[b] < 0 keeps all of this, n_kept[b] and next_tokens[b] included: where
+ * both kinds are in one call, set n_kept to 0 before it.
  * A sequence that lacks a page of its own for a position that it keeps, or whose
  * drafted tokens do not fit its table row, keeps its lens and its rows of path
  * and next_tokens; n_kept[b] is 0 and GPT2_ERR_RANGE is recorded.  Outputs must
