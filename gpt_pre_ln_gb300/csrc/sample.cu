@@ -700,6 +700,7 @@ __device__ __noinline__ Cut select(Cut cut, int count, Two target, float err, fl
   there = block_add<K>(there);
   if (!MASS && there <= count) return cut;
   const float per_z = static_cast<float>(kBins - 8) / (s.half_max - 0.5f * z_of(sh.lo));  // (halves: no overflow)
+  lo = max(lo, static_cast<Place>(sh.lo) << 32);
   __syncthreads();
   auto bin_of = [&](float z) {
     return static_cast<int>(fminf((s.half_max - 0.5f * z) * per_z, static_cast<float>(kBins - 1)));
@@ -707,6 +708,10 @@ __device__ __noinline__ Cut select(Cut cut, int count, Two target, float err, fl
   bool linear = per_z < 3e38f;
 #pragma unroll 1
   while (true) {
+    if (lo >> 32 == hi >> 32) {  // one value: of its places the ids there are
+      lo = max(lo, place_at(static_cast<uint32_t>(lo >> 32), V - 1));
+      hi = min(hi, place_at(static_cast<uint32_t>(hi >> 32), 0));
+    }
     const int shift = max(0, 64 - __clzll(static_cast<long long>(hi - lo)) - 11);
     const int digits = 31 - min(31, 32 - __clz(n));  // n elements of at most 2^digits
     const float one = static_cast<float>(1u << digits);
@@ -820,10 +825,6 @@ __device__ __noinline__ Cut select(Cut cut, int count, Two target, float err, fl
       } else {
         lo = in_lo;
         hi = in_hi;
-      }
-      if (lo >> 32 == hi >> 32) {  // one value: of its places the ids there are
-        lo = max(lo, place_at(static_cast<uint32_t>(lo >> 32), V - 1));
-        hi = min(hi, place_at(static_cast<uint32_t>(hi >> 32), 0));
       }
       before_n = ahead_n;
       if (MASS && !linear && hi - lo > was / 2) {
