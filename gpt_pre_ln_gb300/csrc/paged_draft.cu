@@ -21,14 +21,14 @@
 // ring of TMA boxes that it fills itself.  With more rows two or four warps take the
 // same tiles, 32 positions at a time, each with 16 rows of the block, and a fifth
 // warp brings them: the warp that also filled the ring held up all four (64 rows,
-// 16 sequences of 4096: 116 us, with the fifth warp 83; 48 rows, 8 of 32768: 109 and
-// 81).  Up to 16 rows the fifth warp cost more than it gave (16 rows, 32 sequences
-// of up to 1087: 29 us without, 39 with it).
+// 16 sequences of 4096: 116 us, with the fifth warp 82; 48 rows, 8 of 32768: 109 and
+// 80).  Up to 16 rows the fifth warp cost more than it gave (16 rows, 32 sequences
+// of up to 1087: 28 us without, 39 with it).
 //
 // What bounds it with many rows is how fast one warp gets through the instructions
 // around the products (exponentials, the split of p, running maxima: 400 for 16 rows
-// and 32 positions at 4 cycles each), not memory and not the products: 2.3 TB/s and
-// 39% of the tensor pipes at 64 rows; with 7 rows it is memory (5.0 TB/s).
+// and 32 positions at 4 cycles each), not memory and not the products: 2.4 TB/s and
+// 39% of the tensor pipes at 64 rows; with 7 rows it is memory (5.1 TB/s).
 #include <algorithm>
 
 #include "internal.h"
@@ -863,7 +863,7 @@ __device__ __forceinline__ int rounded(int n, int to) { return to == 1 ? n : (n 
 // Work is cut into equal runs of tiles over all (sequence, key-value head, row
 // block) items laid end to end, one run per CTA, whatever the lengths are.  Where
 // there are CTAs enough items are rounded up to whole runs, so that none takes pieces
-// of two, one after the other (8 tokens of one sequence of 777, 12 heads: 9.6 us,
+// of two, one after the other (8 tokens of one sequence of 777, 12 heads: 9.2 us,
 // 12.1 without it).  A CTA
 // that holds all tiles of an item writes its output, pieces of an item go to the
 // workspace and a second kernel joins them.  Groups of warps that took tiles of a

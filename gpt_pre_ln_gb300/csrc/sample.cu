@@ -23,10 +23,10 @@
 // are listed instead, and the rest is done on the list, in two floats at once.
 //
 // Bound by instructions and by steps that follow one another on one SM, not by
-// memory: a row of 50257 takes 20 us (its maximum 3, the histogram 7, the border 4 to
-// 15, the draw 4), one that is done twice 70.  64 such rows in fp32 with top-p 70 us,
-// 256 with top-k up to 400 35, 1024 in bf16 with mixed settings 139 (740 GB/s), 512
-// rows of 8000 17.
+// memory: a row of 50257 takes 19 us (its maximum 3, the histogram 7, the border 4 to
+// 15, the draw 4), one that is done twice 38 to 70.  64 such rows in fp32 with top-p 69
+// us, 256 with top-k up to 400 34, 1024 in bf16 with mixed settings 137 (750 GB/s), 512
+// rows of 8000 16.
 #include <algorithm>
 #include <type_traits>
 
